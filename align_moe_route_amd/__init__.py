@@ -26,6 +26,9 @@ MRS_ERR_LAUNCH = -6
 MRS_ERR_SCRATCH = -7
 MRS_DTYPE_F32 = 0
 MRS_DTYPE_BF16 = 1
+MRS_DTYPE_F16 = 2
+MRS_X_TOKENS = 0
+MRS_X_SORTED = 1
 FLAG_FORCE_SINGLE_WG = 1
 FLAG_FORCE_MULTI_WG = 2
 FLAG_FORCE_EXACT = 4
@@ -47,6 +50,11 @@ EXPORTED = [
     "moe_grouped_gemm1",
     "moe_grouped_gemm1_profiled",
     "moe_gate_route_sort",
+    "moe_mxfp4_quantize",
+    "moe_grouped_gemm_mxfp4",
+    "moe_balance_workspace_bytes",
+    "moe_balance_loss",
+    "moe_router_backward",
 ]
 
 _lib = None
@@ -100,6 +108,17 @@ def lib() -> ctypes.CDLL:
     L.moe_grouped_gemm1_profiled.restype = i32
     L.moe_gate_route_sort.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     L.moe_gate_route_sort.restype = i32
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.moe_mxfp4_quantize.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp, vp]
+    L.moe_mxfp4_quantize.restype = i32
+    L.moe_grouped_gemm_mxfp4.argtypes = [vp] * 7 + [i32] * 8 + [vp, vp]
+    L.moe_grouped_gemm_mxfp4.restype = i32
+    L.moe_balance_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.moe_balance_workspace_bytes.restype = sz
+    L.moe_balance_loss.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_loss.restype = i32
+    L.moe_router_backward.argtypes = [vp, i32] + [vp] * 7 + [i32] * 4 + [f32, vp, vp]
+    L.moe_router_backward.restype = i32
     _lib = L
     return L
 
@@ -530,3 +549,253 @@ def gate_route_sort(hidden, w_gate, bias, k: int, n_group: int, topk_group: int,
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return logits, out
+
+
+class MXFP4(NamedTuple):
+    """4-bit rows (include/moe_mxfp4.h): K columns padded with zeros to Kp, a
+    multiple of 128, in blocks of 32 that share a scale byte."""
+    codes: "torch.Tensor"   # uint8 [..., Kp / 2], two codes a byte, the even column in the low half
+    scales: "torch.Tensor"  # uint8 [..., Kp / 32], 2^(byte - 127), 255 = NaN
+
+
+def _check_mxfp4(q, dev, dims: int, name: str) -> int:
+    """q holds contiguous 4-bit rows with `dims` dimensions on dev; returns Kp."""
+    import torch
+    if not (isinstance(q, MXFP4) and all(isinstance(t, torch.Tensor) and t.device == dev and t.dtype == torch.uint8
+                                         and t.dim() == dims and t.is_contiguous() for t in q)):
+        raise ValueError(f"{name} must be an MXFP4 of contiguous uint8 tensors with {dims} dimensions on {dev}")
+    Kp = q.codes.shape[-1] * 2
+    if Kp == 0 or Kp % 128 or tuple(q.scales.shape) != tuple(q.codes.shape[:-1]) + (Kp // 32,):
+        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / 32] of the same rows, Kp a multiple of 128")
+    return Kp
+
+
+def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) -> MXFP4:
+    """Rows of x to 4-bit rows (moe_mxfp4_quantize).
+
+    x: float32, bfloat16 or float16 GPU tensor [..., K], 1 <= K <= 262144; the
+    last dimension is consecutive and the leading ones collapse to rows of one
+    stride (a slice of a wider buffer's columns is fine).
+    values: optional contiguous tensor of x's shape and type that takes the
+    values the 4-bit rows stand for (for training with rounded values).
+    out: optional MXFP4 to write into, codes [..., Kp / 2], scales [..., Kp / 32]."""
+    import torch
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() >= 1):
+        raise ValueError("x must be a GPU tensor of at least one dimension")
+    dts = {torch.float32: MRS_DTYPE_F32, torch.bfloat16: MRS_DTYPE_BF16, torch.float16: MRS_DTYPE_F16}
+    if x.dtype not in dts:
+        raise NotImplementedError(f"x dtype {x.dtype} (float32, bfloat16 or float16 only)")
+    K, lead = x.shape[-1], tuple(x.shape[:-1])
+    if not 1 <= K <= 262144:
+        raise ValueError("the last dimension must hold 1 to 262144 values")
+    rows = 1
+    for n in lead:
+        rows *= n
+    row_stride = K
+    if x.numel():
+        if K > 1 and x.stride(-1) != 1:
+            raise ValueError("x's last dimension must be consecutive")
+        step = None  # stride of the rows, from the innermost leading dimension outwards
+        span = 1
+        for n, st in zip(reversed(lead), reversed(x.stride()[:-1])):
+            if n == 1:
+                continue
+            if step is None:
+                step = st
+            elif st != step * span:
+                raise ValueError("x's leading dimensions must collapse to rows of one stride")
+            span *= n
+        row_stride = K if step is None else step
+        if row_stride < K:
+            raise ValueError("x's rows must not overlap")
+    dev = x.device
+    Kp = (K + 127) // 128 * 128
+    if out is None:
+        out = MXFP4(torch.empty(lead + (Kp // 2,), dtype=torch.uint8, device=dev),
+                    torch.empty(lead + (Kp // 32,), dtype=torch.uint8, device=dev))
+    else:
+        _check_mxfp4(out, dev, x.dim(), "out")
+        if tuple(out.codes.shape) != lead + (Kp // 2,):
+            raise ValueError(f"out.codes must have shape {lead + (Kp // 2,)}")
+    if values is not None:
+        _check_tensor(values, dev, x.dtype, x.numel(), "values")
+        if values.shape != x.shape:
+            raise ValueError("values must have x's shape")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    rc = int(lib().moe_mxfp4_quantize(x.data_ptr(), dts[x.dtype], rows, K, row_stride, out.codes.data_ptr(),
+                                      out.scales.data_ptr(), values.data_ptr() if values is not None else None,
+                                      stream.cuda_stream))
+    if rc != MRS_OK:
+        raise RouteSortError(rc)
+    return out
+
+
+def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post_pad, k: int, block: int, *,
+                       tokens: Optional[int] = None, out_dtype=None, out=None, stream=None):
+    """Grouped product of 4-bit rows over the route-sort metadata
+    (moe_grouped_gemm_mxfp4): y[r] = x[row(r)] . W[expert_of_block[r // block]]^T
+    for sorted rows below num_post_pad, zeros for padding rows.
+
+    x: 4-bit rows of the M tokens, row(r) = sorted_ids[r] // k; with `tokens` = M
+    given, x holds max_rows rows in sorted order and row(r) = r (a later product
+    on the rows an earlier one wrote).  w: 4-bit rows [E, N].  block: a multiple
+    of 16.  out_dtype: bfloat16 (default) or float32.  Returns y [max_rows, N];
+    rows at or past num_post_pad are left as they were."""
+    import torch
+    if not (isinstance(x, MXFP4) and isinstance(x.codes, torch.Tensor) and x.codes.is_cuda):
+        raise ValueError("x must be an MXFP4 of GPU tensors")
+    dev = x.codes.device
+    Kp = _check_mxfp4(x, dev, 2, "x")
+    if _check_mxfp4(w, dev, 3, "w") != Kp:
+        raise ValueError("x and w disagree on K")
+    E, N = w.codes.shape[:2]
+    M = x.codes.shape[0] if tokens is None else int(tokens)
+    rows, blocks = max_rows(M, E, k, block), max_blocks(M, E, k, block)
+    if rows < 0:
+        raise ValueError("invalid sizes or row capacity overflow")
+    if tokens is not None and x.codes.shape[0] < rows:
+        raise ValueError(f"x must hold at least {rows} rows in sorted order")
+    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    if out is None:
+        out = torch.empty((max(rows, 1), N), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif not (isinstance(out, torch.Tensor) and out.device == dev and out.is_contiguous() and out.dim() == 2
+              and out.shape[1] == N and out.shape[0] >= rows and (out_dtype is None or out.dtype == out_dtype)):
+        raise ValueError("out must be a contiguous [max_rows, N] tensor of out_dtype on x's device")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise NotImplementedError(f"y dtype {out.dtype} (bfloat16 or float32 only)")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    rc = int(lib().moe_grouped_gemm_mxfp4(
+        x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), sorted_ids.data_ptr(),
+        expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, Kp, N, block,
+        MRS_X_TOKENS if tokens is None else MRS_X_SORTED,
+        MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), stream.cuda_stream))
+    if rc != MRS_OK:
+        raise RouteSortError(rc)
+    return out
+
+
+class BalanceOutput(NamedTuple):
+    loss: "torch.Tensor"    # [1] float32
+    counts: "torch.Tensor"  # [B, E] int32, routes per sequence and expert
+    tokens: "torch.Tensor"  # [B + 1] int32, unmasked tokens per sequence, then the sequences that have any
+    shares: "torch.Tensor"  # [B, E] float32, mean normalised score
+
+
+def _check_router(logits, ids, seq_offsets, mask):
+    """Common checks of balance_loss and router_backward: (dtype code, M, E, k, B)."""
+    import torch
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2 and logits.is_contiguous()):
+        raise ValueError("logits must be a contiguous [M, E] GPU tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise NotImplementedError(f"logits dtype {logits.dtype} (float32 or bfloat16 only)")
+    M, E = logits.shape
+    dev = logits.device
+    _check_tensor(ids, dev, torch.int32, 0, "ids")
+    if ids.dim() != 2 or ids.shape[0] != M:
+        raise ValueError(f"ids must have shape ({M}, k)")
+    B = 1
+    if seq_offsets is not None:
+        _check_tensor(seq_offsets, dev, torch.int32, 2, "seq_offsets")
+        if seq_offsets.dim() != 1:
+            raise ValueError("seq_offsets must have one dimension")
+        B = seq_offsets.numel() - 1
+    if mask is not None:
+        if not (isinstance(mask, torch.Tensor) and mask.dtype in (torch.bool, torch.uint8)):
+            raise ValueError("mask must be a bool or uint8 tensor")
+        _check_tensor(mask, dev, None, M, "mask")
+        if tuple(mask.shape) != (M,):
+            raise ValueError(f"mask must have shape ({M},)")
+    return (MRS_DTYPE_F32 if logits.dtype == torch.float32 else MRS_DTYPE_BF16), M, E, ids.shape[1], B
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def balance_workspace_bytes(M: int, E: int, k: int, B: int = 1) -> int:
+    v = int(lib().moe_balance_workspace_bytes(M, E, k, B))
+    if v == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid sizes")
+    return v
+
+
+def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None, out: Optional[BalanceOutput] = None,
+                 workspace=None, stream=None) -> BalanceOutput:
+    """Balance loss, per-expert counts and mean scores of a routing
+    (moe_balance_loss, include/moe_balance.h).
+
+    logits: [M, E] float32 or bfloat16, ids: [M, k] int32 as route_sort returns
+    them (ids outside [0, E) are dropped routes).  seq_offsets: int32 [B + 1],
+    the loss is the mean over the sequences; mask: bool or uint8 [M], zero for
+    padding tokens.  workspace: as for route_sort (balance_workspace_bytes)."""
+    import torch
+    dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
+    dev = logits.device
+    nbytes = balance_workspace_bytes(M, E, k, B)
+    if out is None:
+        out = BalanceOutput(torch.empty((1,), dtype=torch.float32, device=dev),
+                            torch.empty((B, E), dtype=torch.int32, device=dev),
+                            torch.empty((B + 1,), dtype=torch.int32, device=dev),
+                            torch.empty((B, E), dtype=torch.float32, device=dev))
+    else:
+        for t, dtype, shape, name in ((out.loss, torch.float32, (1,), "out.loss"),
+                                      (out.counts, torch.int32, (B, E), "out.counts"),
+                                      (out.tokens, torch.int32, (B + 1,), "out.tokens"),
+                                      (out.shares, torch.float32, (B, E), "out.shares")):
+            _check_tensor(t, dev, dtype, 1, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if workspace is None:
+        workspace = _workspace(dev, stream.cuda_stream, nbytes)
+    else:
+        _check_tensor(workspace, dev, None, 0, "workspace")
+    rc = int(lib().moe_balance_loss(logits.data_ptr(), dt, ids.data_ptr(), _ptr(seq_offsets), _ptr(mask), M, E, k, B,
+                                    float(coef), out.loss.data_ptr(), out.counts.data_ptr(), out.tokens.data_ptr(),
+                                    out.shares.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), stream.cuda_stream))
+    if rc != MRS_OK:
+        raise RouteSortError(rc)
+    return out
+
+
+def router_backward(logits, ids, *, grad_weights=None, balance: Optional[BalanceOutput] = None, coef: float = 1.0,
+                    grad_loss=None, seq_offsets=None, mask=None, out=None, stream=None):
+    """Gradient of the logits (moe_router_backward): of the balance loss when
+    `balance` (what balance_loss returned for the same logits, ids, seq_offsets
+    and mask) is given, times grad_loss (float32 [1], default 1), plus that of
+    the routing weights when grad_weights ([M, k] float32) is given.  Returns
+    [M, E] of the logits' type."""
+    import torch
+    dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
+    dev = logits.device
+    if grad_weights is not None:
+        _check_tensor(grad_weights, dev, torch.float32, M * k, "grad_weights")
+        if tuple(grad_weights.shape) != (M, k):
+            raise ValueError(f"grad_weights must have shape ({M}, {k})")
+    if balance is not None:
+        for t, shape, name in ((balance.counts, (B, E), "balance.counts"), (balance.tokens, (B + 1,), "balance.tokens")):
+            _check_tensor(t, dev, torch.int32, 1, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}")
+    if grad_loss is not None:
+        _check_tensor(grad_loss, dev, torch.float32, 1, "grad_loss")
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _check_tensor(out, dev, logits.dtype, M * E, "out")
+        if out.shape != logits.shape:
+            raise ValueError("out must have the logits' shape")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    rc = int(lib().moe_router_backward(logits.data_ptr(), dt, ids.data_ptr(), _ptr(grad_weights),
+                                       _ptr(balance.counts) if balance is not None else None,
+                                       _ptr(balance.tokens) if balance is not None else None, _ptr(grad_loss),
+                                       _ptr(seq_offsets), _ptr(mask), M, E, k, B, float(coef), out.data_ptr(),
+                                       stream.cuda_stream))
+    if rc != MRS_OK:
+        raise RouteSortError(rc)
+    return out

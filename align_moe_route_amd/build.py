@@ -2,10 +2,12 @@
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route_sort.hip", "moe_gemm1.hip", "moe_gate.hip")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route_sort.hip", "moe_gemm1.hip", "moe_gate.hip",
+                                                  "moe_mxfp4.hip", "moe_balance.hip")]
 OUT = os.path.join(HERE, "libmoe_route_sort.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -14,7 +16,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-ffp-contract=off",          # every rounding step is the one the source spells out
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",  # no packed FP32 ops
     "-Wall",
@@ -50,16 +51,26 @@ def build_table(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
+    """Compile every source (side by side) and link the library."""
     build_table(verbose)
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"), *SRCS,
-           "-o", OUT + ".tmp"]
+
+    def compile_one(src):
+        obj = src[:-len(".hip")] + ".o"
+        cmd = [HIPCC, *FLAGS, "-c", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"), src,
+               "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return obj, _run(cmd, f"compiling {os.path.basename(src)}")
+
+    with ThreadPoolExecutor(min(len(SRCS), os.cpu_count() or 1)) as pool:
+        done = list(pool.map(compile_one, SRCS))
+    objs = [obj for obj, _ in done]
+    cmd = [HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", OUT + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    msg = "\n".join(l for l in (res.stdout + res.stderr).splitlines()
-                    if "packed-fp32-ops" not in l and l.strip())
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msg}")
+    msg = "\n".join(m for m in [m for _, m in done] + [_run(cmd, "linking")] if m)
+    for obj in objs:
+        os.remove(obj)
     if verbose and msg:
         print(msg, flush=True)
     os.replace(OUT + ".tmp", OUT)
