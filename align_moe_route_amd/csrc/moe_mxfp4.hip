@@ -165,15 +165,24 @@ struct PArgs {
 };
 
 // Workgroup h goes to XCD h mod 8; runs of kRunRows consecutive row tiles go to
-// the XCDs in turn and, inside a run, the row tiles of one column tile come one
-// after another, so the row tiles of an expert read its weights from one L2.
+// the XCDs in turn, the column tiles of a row tile one after another, so an
+// expert's row tiles read its weights, and a row tile's column tiles its rows,
+// from one L2 at about the same time.
 constexpr int kXcds = 8;
 constexpr int kRunRows = 8;
-__device__ __forceinline__ bool tile_of(int h, int ntn, int nrt, int& rt, int& ct) {
+__device__ __forceinline__ void tile_of(int h, int ntn, int& rt, int& ct) {
+  const int x = h % kXcds, j = h / kXcds, i = j / ntn;
+  rt = (i / kRunRows * kXcds + x) * kRunRows + i % kRunRows;
+  ct = j % ntn;
+}
+
+// Few rows an expert: the row tiles of one padding block (G of them) and one
+// column tile come one after another on one XCD; the pairs go to the XCDs in turn.
+__device__ __forceinline__ bool tile_of_block(int h, int G, int ntn, int nrt, int& rt, int& ct) {
   const int x = h % kXcds, j = h / kXcds;
-  const int m = j / (kRunRows * ntn), c = (j / kRunRows) % ntn, r = j % kRunRows;
-  rt = (m * kXcds + x) * kRunRows + r;
-  ct = c;
+  const int u = j / G * kXcds + x;
+  rt = u / ntn * G + j % G;
+  ct = u % ntn;
   return rt < nrt;
 }
 
@@ -196,12 +205,17 @@ __device__ __forceinline__ i32x8 frag(u32x4 q) {
 // straight into the matrix operand's registers (v_mfma_scale_f32_16x16x128:
 // lane l holds columns 32 (l / 16) .. + 31 of row l mod 16, which is one chunk
 // and one scale byte), U steps in flight at a time, and nothing goes through
-// LDS but the partial sums.  Padding rows load nothing.
-template <typename Y, int FN, int U>
+// LDS but the partial sums.  Padding rows load nothing.  Eight steps in flight
+// and 32 columns measured best: 64 tokens, 896 experts, K = 3584, N = 768 in
+// 219 us, 901 MB of weights at 4.1 TB/s (a 2 GiB copy moves 4.9); 16 columns
+// 235 us, 48 columns 235 us, four steps 238 us.
+constexpr int kRowsFN = 2, kRowsDeep = 8, kRowsCols = 16 * kRowsFN;
+template <typename Y>
 __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
+  constexpr int FN = kRowsFN, U = kRowsDeep;
   __shared__ f32x4 part[4][FN][64];
   int rt, ct;
-  if (!tile_of((int)blockIdx.x, a.ntn, a.nrt, rt, ct)) return;
+  if (!tile_of_block((int)blockIdx.x, a.block / 16, a.ntn, a.nrt, rt, ct)) return;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
   const int r0 = rt * 16, n0 = ct * 16 * FN;
@@ -274,200 +288,265 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
 
 // Tiles of BM rows x 256 columns, four waves of 64 columns each
 // (v_mfma_scale_f32_32x32x64: lane l holds columns 32 (l / 32) .. + 31 of row
-// l mod 32).  Steps of 256 columns: the x rows are shared by the waves and
-// staged through two LDS buffers (rows of 128 bytes, 16-byte chunks XOR-swizzled
-// so that the 32 rows of an operand read hit distinct banks); each wave's
-// weights are its own and go from memory to its registers, the next step's
-// while the present one is multiplied.
-template <int CH>
-__device__ __forceinline__ int swz(int r, int c) {
-  return r * CH + (c ^ (r & 7) ^ ((r >> 3) & 1));
-}
+// l mod 32).  Steps of 256 columns, 128 bytes a row: the x rows are shared by the
+// waves, each wave's weight rows are its own.  Both are read eight lanes to a
+// row and turned in LDS (16-byte chunks XOR-swizzled, so that the 32 rows of an
+// operand read hit distinct banks), the next step's into registers while the
+// present one is multiplied.  Reading the weights straight into operand
+// registers, every lane another row, kept the address unit busy 87 % of the time
+// and bounded the kernel.  8192 tokens, 896 experts, top-16, K = 3584, N = 768 in
+// 450 us: 1.5 GB that must move at 3.4 TB/s; with the experts' rows read again
+// from the L2's misses and y written, 2.0 GB at 4.5 TB/s (a 2 GiB copy: 4.9), which
+// bounds it now (without the multiplications it takes 410 us).
+constexpr int kFN = 2, kNW = 4;  // 32-column operands a wave, waves
+constexpr int kCols = kNW * kFN * 32, kTileThreads = kNW * 64;
 
-struct __attribute__((packed, aligned(4))) Scale8 {
+__device__ __forceinline__ int swz(int r, int c) { return r * 8 + (c ^ (r & 7) ^ ((r >> 3) & 1)); }
+
+struct alignas(8) Scale8 {
   uint32_t lo, hi;
 };
 
-template <typename Y, int BM, int FM>
-__device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int e, u32x4 (*xl)[BM * 8],
-                                          Scale8 (*sl)[BM]) {
-  constexpr int XP = BM * 8 / 256;  // x chunks a thread stages in a step
+// Scale words of a run of kScaleSteps steps (64 bytes a row), staged into LDS at
+// once: fetched step by step, a row's line left the L2 between two steps and came
+// from memory for each of them (2.1 GB read in place of 1.7 on 8192 tokens x 896
+// experts).  Row r keeps the pair of step t at slot t ^ ((r / 4) mod 8), so that
+// the 32 rows of an operand lie on distinct banks.
+constexpr int kScaleSteps = 8;
+__device__ __forceinline__ int scale_slot(int r, int t) { return r * kScaleSteps + (t ^ ((r >> 2) & 7)); }
+
+// ROWS rows' words into LDS (slot order above), straight from memory: lane l of
+// the wave's instruction i (the wave's q-th) fills word i * 64 + l, `src(row)` is
+// the row's first word of the run, words past `left` repeat the last one and are
+// not used.
+template <int ROWS, typename F>
+__device__ __forceinline__ void stage_scales(Scale8* dst, int left, F src) {
+  constexpr int kEach = ROWS * kScaleSteps * 2 / 64 / kNW;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll 2
+  for (int q = 0; q < kEach; ++q) {
+    const int i = wv * kEach + q, o = i * 64 + lane, r = o / (2 * kScaleSteps);
+    const int t = ((o / 2) % kScaleSteps) ^ ((r >> 2) & 7), w = min(2 * t + (o & 1), left - 1);
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src(r) + w * 4),
+                                     (__attribute__((address_space(3))) void*)(reinterpret_cast<uint32_t*>(dst) + i * 64),
+                                     4, 0, 0);
+  }
+}
+
+template <int BM>
+struct Tile {
+  u32x4 x[BM * 8], w[kCols * 8];
+  Scale8 sx[BM * kScaleSteps], sw[kCols * kScaleSteps];
+  uint32_t row[BM];        // row of x
+  uint32_t mask[BM / 32];  // rows that hold a route
+};
+
+constexpr int kWP = kFN * 32 * 8 / 64;  // weight chunks a lane stages in a step
+typedef u32x4 WeightRegs[kWP];
+
+// The rows of W that this wave stages: lane l takes chunk l mod 8 of rows l / 8, + 8, ...
+struct Weights {
+  const uint8_t *codes, *scales;  // of the tile's first column
+  int row, last;                  // this lane's first row, the last row that exists
+  uint32_t kb;                    // bytes of a row
+  __device__ __forceinline__ void load(WeightRegs& q, int o) const {  // o: byte of the row
+#pragma unroll
+    for (int p = 0; p < kWP; ++p) {
+      int r = row + p * 8;
+      asm volatile("" : "+v"(r));  // opaque: eight row addresses kept over the loop spill
+      q[p] = *reinterpret_cast<const u32x4*>(codes + ((uint32_t)min(r, last) * kb + (uint32_t)o));
+    }
+  }
+};
+
+__device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+// `live`: the leading 32-row parts of the tile that hold a route
+template <typename Y, int BM>
+__device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int live, const Weights& w, WeightRegs& wr,
+                                          Tile<BM>& l) {
+  constexpr int FM = BM / 32;
+  constexpr int XP = BM * 8 / kTileThreads;  // x chunks a thread stages in a step
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int lr = lane & 31, lh = lane >> 5;
-  const int routes = a.M * a.k;
   const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
   const int steps = (a.K + 255) / 256;
   const bool half = a.K % 256 != 0;  // the last step has 128 columns
 
+  // Padding rows read row 0: each row's result is its own, and theirs is
+  // replaced by zero.  Past K, in the second half of a last step of 128 columns,
+  // the first half is read again with both scale words zero: 2^-254 times any
+  // codes vanishes in FP32.
+  const int c16 = tid % 8 * 16, back = tid % 8 >= 4 ? 64 : 0;
+  auto at = [&](int t) { return t * 128 + c16 - (half && t == steps - 1 ? back : 0); };
   const uint8_t* xsrc[XP];
-  bool xok[XP];
 #pragma unroll
-  for (int p = 0; p < XP; ++p) {
-    const int r = (tid + p * 256) / 8, c = tid % 8;
-    const int s = a.sid[r0 + r];
-    xok[p] = s >= 0 && s < routes;
-    const size_t row = xok[p] ? (size_t)(a.sorted ? r0 + r : s / a.k) : 0;
-    xsrc[p] = a.xc + row * kb + c * 16;
-  }
-  const uint8_t* ssrc = a.xs;
-  bool sok = false;
-  if (tid < BM) {
-    const int s = a.sid[r0 + tid];
-    sok = s >= 0 && s < routes;
-    const size_t row = sok ? (size_t)(a.sorted ? r0 + tid : s / a.k) : 0;
-    ssrc = a.xs + row * ks;
-  }
-  const uint8_t *wc[2], *ws[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const size_t n = (size_t)e * a.N + min(n0 + wv * 64 + j * 32 + lr, a.N - 1);
-    wc[j] = a.wc + n * kb + lh * 16;
-    ws[j] = a.ws + n * ks;
-  }
-
+  for (int p = 0; p < XP; ++p) xsrc[p] = a.xc + (size_t)l.row[(tid + p * kTileThreads) / 8] * kb;
   u32x4 xr[XP];
-  Scale8 sr;
-  u32x4 wq[2][4];
-  uint32_t we[2][2];
-  // a step's second half past the end of K is not read: zero codes and scales
   auto load_x = [&](int t) {
-    const bool full = !(half && t == steps - 1);
 #pragma unroll
-    for (int p = 0; p < XP; ++p) {
-      xr[p] = u32x4{0u, 0u, 0u, 0u};
-      if (xok[p] && (full || tid % 8 < 4)) xr[p] = *reinterpret_cast<const u32x4*>(xsrc[p] + (size_t)t * 128);
-    }
-    sr.lo = sr.hi = 0u;
-    if (sok) {
-      sr.lo = *reinterpret_cast<const uint32_t*>(ssrc + t * 8);
-      if (full) sr.hi = *reinterpret_cast<const uint32_t*>(ssrc + t * 8 + 4);
-    }
+    for (int p = 0; p < XP; ++p) xr[p] = *reinterpret_cast<const u32x4*>(xsrc[p] + at(t));
   };
-  auto store_x = [&](int buf) {
+  auto store = [&]() {
 #pragma unroll
-    for (int p = 0; p < XP; ++p) xl[buf][swz<8>((tid + p * 256) / 8, tid % 8)] = xr[p];
-    if (tid < BM) sl[buf][tid] = sr;
+    for (int p = 0; p < XP; ++p) l.x[swz((tid + p * kTileThreads) / 8, tid % 8)] = xr[p];
+#pragma unroll
+    for (int p = 0; p < kWP; ++p) l.w[swz(wv * kFN * 32 + lane / 8 + p * 8, tid % 8)] = wr[p];
   };
-  auto load_w = [&](int t, u32x4 (&q)[2][4], uint32_t (&s)[2][2]) {
-    const bool full = !(half && t == steps - 1);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[j][i] = u32x4{0u, 0u, 0u, 0u};
-        if (i < 2 || full) q[j][i] = *reinterpret_cast<const u32x4*>(wc[j] + (size_t)t * 128 + i * 32);
-      }
-      s[j][0] = *reinterpret_cast<const uint32_t*>(ws[j] + t * 8);
-      s[j][1] = full ? *reinterpret_cast<const uint32_t*>(ws[j] + t * 8 + 4) : 0u;
-    }
+  auto load_scales = [&](int t, bool weights) {
+    // opaque, or the addresses of the runs after the first are made ahead of the
+    // loop and kept (100 registers spilled)
+    uint32_t kv = (uint32_t)ks;
+    asm volatile("" : "+s"(kv));
+    const int left = (int)kv / 4 - t * 2;  // words left in a row
+    stage_scales<BM>(l.sx, left, [&](int r) { return a.xs + (size_t)l.row[r] * kv + t * 8; });
+    if (weights)
+      stage_scales<kCols>(l.sw, left, [&](int r) { return w.scales + (size_t)min(r, w.last) * kv + t * 8; });
   };
 
-  f32x16 acc[FM][2];
+  load_x(0);
+  load_scales(0, false);
+  store();
+  wait_memory();  // the scales are in LDS
+  __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
+  f32x16 acc[FM][kFN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    for (int j = 0; j < kFN; ++j) acc[i][j] = f32x16{};
 
-  load_x(0);
-  load_w(0, wq, we);
-  store_x(0);
-  __syncthreads();
   for (int t = 0; t < steps; ++t) {
-    const int cur = t & 1;
-    u32x4 wn[2][4];
-    uint32_t wne[2][2];
-    const bool more = t + 1 < steps;
-    if (more) {
-      load_x(t + 1);
-      load_w(t + 1, wn, wne);
+    const int next = min(t + 1, steps - 1);
+    if (t > 0 && t % kScaleSteps == 0) {  // past the last step's barrier
+      load_scales(t, true);
+      wait_memory();
+      __syncthreads();
     }
+    const uint32_t keep = half && t == steps - 1 ? 0u : ~0u;
+    w.load(wr, at(next));
+    load_x(next);
     // scale of columns 64 g + 32 lh ..: byte 2 (g mod 2) of the word g / 2 shifted by 8 lh
-    uint32_t xe[FM][2];
+    Scale8 we[kFN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const Scale8 v = sl[cur][i * 32 + lr];
-      xe[i][0] = v.lo >> (8 * lh);
-      xe[i][1] = v.hi >> (8 * lh);
+    for (int j = 0; j < kFN; ++j) {
+      we[j] = l.sw[scale_slot((wv * kFN + j) * 32 + lr, t % kScaleSteps)];
+      we[j].lo >>= 8 * lh;
+      we[j].hi = (we[j].hi & keep) >> (8 * lh);
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      i32x8 xf[FM], wf[2];
+    for (int h = 0; h < 2; ++h) {  // two groups of 64 columns
+      i32x8 wf[kFN][2], xf[2];
+      Scale8 xe;
+      auto read = [&](int i) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) xf[i] = frag(xl[cur][swz<8>(i * 32 + lr, 2 * g + lh)]);
+        for (int g = 0; g < 2; ++g) xf[g] = frag(l.x[swz(i * 32 + lr, 4 * h + 2 * g + lh)]);
+        xe = l.sx[scale_slot(i * 32 + lr, t % kScaleSteps)];
+      };
 #pragma unroll
-      for (int j = 0; j < 2; ++j) wf[j] = frag(wq[j][g]);
+      for (int j = 0; j < kFN; ++j)
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+        for (int g = 0; g < 2; ++g) wf[j][g] = frag(l.w[swz((wv * kFN + j) * 32 + lr, 4 * h + 2 * g + lh)]);
+      read(0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int sx = (int)xe[i][g / 2], sw = (int)(we[j][g / 2] >> (8 * lh));
-          if (g % 2 == 0)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xf[i], wf[j], acc[i][j], 4, 4, 0, sx, 0, sw);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xf[i], wf[j], acc[i][j], 4, 4, 2, sx, 2, sw);
-        }
-    }
-    if (more) {
-      store_x(cur ^ 1);
+      for (int i = 0; i < FM; ++i) {
+        const i32x8 x0 = xf[0], x1 = xf[1];
+        const int xs = (int)((h == 0 ? xe.lo : xe.hi & keep) >> (8 * lh));
+        if (i + 1 < FM) read(i + 1);
+        if (i < live)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wq[j][i] = wn[j][i];
-        we[j][0] = wne[j][0];
-        we[j][1] = wne[j][1];
+          for (int j = 0; j < kFN; ++j) {
+            const int ws = (int)(h == 0 ? we[j].lo : we[j].hi);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x0, wf[j][0], acc[i][j], 4, 4, 0, xs, 0, ws);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x1, wf[j][1], acc[i][j], 4, 4, 2, xs, 2, ws);
+          }
       }
     }
     __syncthreads();
+    store();
+    __syncthreads();
   }
 
-  // result register v of lane l: row 8 (v / 4) + 4 (l / 32) + v mod 4, column l mod 32
+  // Result register v of lane l: row 8 (v / 4) + 4 (l / 32) + v mod 4, column
+  // l mod 32.  A wave turns its 32 x 64 results in its own part of the LDS (the
+  // last barrier has passed, rows and scales are used up) into whole 16-byte
+  // chunks of y's rows.
+  constexpr int kRow = kFN * 32 * sizeof(Y), kPad = kRow + 16;  // bytes of a row in LDS
+  static_assert(kNW * 32 * kPad <= (int)(sizeof(l.x) + sizeof(l.w)), "the results fit");
+  // 16-byte chunks stay inside the row and are aligned
+  const bool wide = a.N % (16 / sizeof(Y)) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  char* stage = reinterpret_cast<char*>(&l) + wv * 32 * kPad;
+  const int n1 = n0 + wv * kFN * 32;
 #pragma unroll
   for (int i = 0; i < BM / 32; ++i) {
-    const int sr32 = a.sid[r0 + i * 32 + lr];
-    const uint32_t rows = (uint32_t)__ballot(sr32 >= 0 && sr32 < routes);
+    const uint32_t rows = l.mask[i];
+    Y* y = static_cast<Y*>(a.y) + (size_t)(r0 + i * 32) * a.N;
+    if (wide) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = n0 + wv * 64 + j * 32 + lr;
-      if (n < a.N)
+      for (int j = 0; j < kFN; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const int r = 8 * (v / 4) + 4 * lh + v % 4;
-          float o = 0.0f;
-          if (i < FM) o = (rows >> r) & 1u ? acc[i < FM ? i : 0][j][v] : 0.0f;
-          put_y(static_cast<Y*>(a.y) + (size_t)(r0 + i * 32 + r) * a.N + n, o);
+          const float o = (rows >> r) & 1u ? acc[i][j][v] : 0.0f;
+          put_y(reinterpret_cast<Y*>(stage + r * kPad) + j * 32 + lr, o);
         }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int q = 0; q < 32 * kRow / 1024; ++q) {
+        const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
+        const int n = n1 + c * (16 / (int)sizeof(Y));
+        const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
+        if (n < a.N) *reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n) = o;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    } else {
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) {
+        const int n = n1 + j * 32 + lr;
+        if (n < a.N)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int r = 8 * (v / 4) + 4 * lh + v % 4;
+            const float o = (rows >> r) & 1u ? acc[i][j][v] : 0.0f;
+            put_y(y + (size_t)r * a.N + n, o);
+          }
+      }
     }
   }
 }
 
 template <typename Y, int BM>
-__global__ __launch_bounds__(256) void k_product_tile(PArgs a) {
-  __shared__ u32x4 xl[2][BM * 8];
-  __shared__ Scale8 sl[2][BM];
+__global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
+  __shared__ Tile<BM> l;
   int rt, ct;
-  if (!tile_of((int)blockIdx.x, a.ntn, a.nrt, rt, ct)) return;
-  const int r0 = rt * BM;
+  tile_of((int)blockIdx.x, a.ntn, rt, ct);
+  if (rt >= a.nrt) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int r0 = rt * BM, n0 = ct * kCols;
   const int npp = min(*a.npp, a.row_limit);
-  if (r0 + BM > npp) return;  // npp is a multiple of block and BM divides block
-  const int e = a.eob[r0 / a.block];
-  if (e < 0 || e >= a.E) return;
+  const int e = __builtin_amdgcn_readfirstlane(a.eob[r0 / a.block]);
+  const int s = tid < BM ? a.sid[r0 + tid] : -1;
+  if (r0 + BM > npp || e < 0 || e >= a.E) return;  // npp is a multiple of block and BM divides block
+  const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
+  const Weights w{a.wc + ((size_t)e * a.N + n0) * kb, a.ws + ((size_t)e * a.N + n0) * ks,
+                  wv * kFN * 32 + lane / 8, a.N - 1 - n0, (uint32_t)kb};
+  WeightRegs wr;
+  w.load(wr, tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0));
+  stage_scales<kCols>(l.sw, (int)ks / 4, [&](int r) { return w.scales + (size_t)min(r, w.last) * ks; });
+  const bool ok = s >= 0 && s < a.M * a.k;
+  if (tid < BM) {
+    l.row[tid] = ok ? (a.sorted ? r0 + tid : s / a.k) : 0;
+    const uint64_t m = __ballot(ok);
+    if (lane % 32 == 0) l.mask[tid / 32] = (uint32_t)(lane ? m >> 32 : m);
+  }
+  __syncthreads();
   // a segment's routes come first: the last 32 rows that hold one bound the work
-  int live = 0;
-  const int lane = threadIdx.x & 63;
+  int live = 1;
 #pragma unroll
-  for (int i = 0; i < BM / 32; ++i) {
-    const int s = a.sid[r0 + i * 32 + (lane & 31)];
-    if (__ballot(s >= 0 && s < a.M * a.k)) live = i + 1;
-  }
+  for (int i = 1; i < BM / 32; ++i)
+    if (l.mask[i]) live = i + 1;
   live = __builtin_amdgcn_readfirstlane(live);
-  if constexpr (BM == 128) {
-    if (live == 4) return tile_body<Y, BM, 4>(a, r0, ct * 256, e, xl, sl);
-    if (live == 3) return tile_body<Y, BM, 3>(a, r0, ct * 256, e, xl, sl);
-  }
-  if constexpr (BM >= 64) {
-    if (live == 2) return tile_body<Y, BM, 2>(a, r0, ct * 256, e, xl, sl);
-  }
-  return tile_body<Y, BM, 1>(a, r0, ct * 256, e, xl, sl);
+  tile_body<Y, BM>(a, r0, n0, live, w, wr, l);
 }
 
 template <typename Y>
@@ -476,7 +555,7 @@ const void* product_kernel(int bm) {
     case 128: return reinterpret_cast<const void*>(k_product_tile<Y, 128>);
     case 64: return reinterpret_cast<const void*>(k_product_tile<Y, 64>);
     case 32: return reinterpret_cast<const void*>(k_product_tile<Y, 32>);
-    default: return reinterpret_cast<const void*>(k_product_rows<Y, 1, 4>);
+    default: return reinterpret_cast<const void*>(k_product_rows<Y>);
   }
 }
 
@@ -512,7 +591,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
                                       const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k,
                                       int E, int K, int N, int block, int x_rows, int y_dtype, void* y,
                                       void* stream) {
-  if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K <= 0 || K % 128 != 0 || N < 1 || block < 16 ||
+  if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K <= 0 || K > (1 << 22) || K % 128 != 0 || N < 1 || block < 16 ||
       block % 16 != 0 || (x_rows != MRS_X_TOKENS && x_rows != MRS_X_SORTED) ||
       (y_dtype != MRS_DTYPE_BF16 && y_dtype != MRS_DTYPE_F32))
     return MRS_ERR_INVALID_ARG;
@@ -530,15 +609,21 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
   if (block % 32 == 0 && routes > 16 * used) {
     bm = block % 128 == 0 && routes > 64 * used ? 128 : (block % 64 == 0 && routes > 32 * used ? 64 : 32);
   }
-  const int bn = bm == 16 ? 16 : 256;
+  const int bn = bm == 16 ? kRowsCols : kCols;
   const int64_t nrt = row_limit / bm, ntn = ((int64_t)N + bn - 1) / bn;
-  const int64_t runs = (nrt + kXcds * kRunRows - 1) / (kXcds * kRunRows) * kRunRows;
-  if (runs * kXcds * ntn > INT32_MAX) return MRS_ERR_OVERFLOW;
+  int64_t grid;
+  if (bm == 16) {  // whole rounds of pairs (padding block, column tile)
+    const int64_t pairs = row_limit / block * ntn;
+    grid = (pairs + kXcds - 1) / kXcds * kXcds * (block / 16);
+  } else {
+    grid = (nrt + kXcds * kRunRows - 1) / (kXcds * kRunRows) * kRunRows * kXcds * ntn;
+  }
+  if (grid > INT32_MAX) return MRS_ERR_OVERFLOW;
   PArgs a{x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, y,
           M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn};
   const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm) : product_kernel<float>(bm);
   void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)(runs * kXcds * ntn)), dim3(256), params, 0,
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(bm == 16 ? 256 : kTileThreads), params, 0,
                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? MRS_OK
              : MRS_ERR_LAUNCH;

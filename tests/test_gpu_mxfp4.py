@@ -142,6 +142,10 @@ SHAPES = [  # M, E, k, K, N, block, drop, skew
     (400, 5, 3, 33, 31, 96, 0, 0),
     (90, 6, 2, 2000, 70, 32, 1.0, 0),   # every route dropped
     (611, 1, 1, 256, 48, 128, 0, 0),
+    (400, 3, 1, 2200, 72, 128, 0, 0),   # more than eight steps of 256: scales staged again
+    (150, 3, 1, 4500, 40, 64, 0, 0),
+    (70, 2, 1, 6200, 264, 32, 0, 0.5),
+    (9, 3, 1, 9000, 33, 48, 0, 0),
 ]
 
 
