@@ -1,14 +1,16 @@
 // Balance loss, per-expert counts and the router's gradient, MI355X (gfx950,
 // CDNA4, wave64).  Definitions and argument contracts: include/moe_balance.h.
 //
-// Both directions read each row of logits once: a wave takes a row, its lanes
-// hold the row's scores in registers, a wave-wide sum gives the row's total.
-// Forward: the waves of a workgroup walk a chunk of tokens, each adding its
-// rows' shares into registers; the workgroup's column sums and its LDS
+// Both directions read each row of logits once: a wave (up to 1024 experts) or a
+// workgroup of four takes a row, up to sixteen columns of it to a thread, the
+// next rows on their way meanwhile; a thread keeps its columns (their running
+// shares, or their counts) in registers throughout.
+// Forward: a workgroup walks a chunk of tokens; its column sums and its LDS
 // histogram of the ids go to the workspace as one piece per (chunk, sequence),
-// and a second kernel adds the pieces up in their order.  Backward: the row's
-// counts-weighted mean comes from the same registers, and the picks' gradient
-// joins in FP32 before the one rounding.
+// and a second kernel adds the pieces up in their order (one workgroup alone
+// finishes a small batch itself).  Backward: the row's counts-weighted mean comes
+// from the same pass, and the picks' gradient joins in FP32 before the one
+// rounding.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -20,8 +22,6 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
 constexpr float kLog2e = 1.44269504088896340736f;
 // A row total below this is renormalised from shifted logits: above it a score
 // that FP32 flushes to zero (below 2^-126) is under 2^-66 of the total.
@@ -32,7 +32,7 @@ struct BArgs {
   const int32_t* ids;
   const int32_t* off;   // null: one sequence
   const uint8_t* mask;  // null: every token
-  int M, E, k, B, chunk, chunks;
+  int M, E, k, B, chunk;
   float coef;
   // forward
   float* loss;
@@ -85,7 +85,7 @@ __device__ __forceinline__ float sigmoid(float x, float& slope) {
   const float u = fast_exp(-__builtin_fabsf(x));
   const float r = fast_rcp(1.0f + u), ur = u * r;
   slope = ur * r;
-  return x >= 0.0f ? r : (x != x ? x : ur);
+  return x >= 0.0f ? r : ur;
 }
 __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
@@ -101,26 +101,40 @@ template <>
 struct Row<MRS_DTYPE_BF16> {
   typedef uint16_t T;
   static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-  static __device__ __forceinline__ uint16_t put(float v) {  // to nearest even; NaN stays NaN
-    const uint32_t u = __float_as_uint(v);
-    return v != v ? (uint16_t)0x7FC0u : (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
-  }
+  // to nearest even, NaN stays NaN (v_cvt_pk_bf16_f32)
+  static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
 
-// VEC consecutive columns (one load) at column (i * 64 + lane) * VEC; columns
-// past E read as -infinity, whose score is zero.
-template <int DT, int VEC, int NI>
-__device__ __forceinline__ void load_row(const typename Row<DT>::T* row, int E, int lane, float (&x)[NI][VEC]) {
-  typedef typename Row<DT>::T T;
-  struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
-  };
+// A workgroup has 256 threads, of which G share a row; a thread has NI times four
+// columns, at (i G + its place in the group) * 4.
+constexpr int kThreads = 256;
+
+// Four columns from c of a row of E, as stored; columns past E read as -infinity,
+// whose score is zero.  Rows need no more alignment than their elements.
+template <int DT>
+struct __attribute__((packed, aligned(sizeof(typename Row<DT>::T)))) Four {
+  typename Row<DT>::T v[4];
+};
+// `inner`: of a thread's column groups all but the last lie inside the row.
+template <int DT>
+__device__ __forceinline__ Four<DT> load4(const typename Row<DT>::T* row, int c, int E, bool inner) {
+  if (inner || c + 4 <= E) return *reinterpret_cast<const Four<DT>*>(row + c);
+  Four<DT> q;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = (i * 64 + lane) * VEC;
-    const Pack p = *reinterpret_cast<const Pack*>(row + (c < E ? c : 0));
+  for (int v = 0; v < 4; ++v) q.v[v] = c + v < E ? row[c + v] : Row<DT>::put(-__builtin_inff());
+  return q;
+}
+template <int DT>
+__device__ __forceinline__ void store4(typename Row<DT>::T* row, int c, int E, bool inner, const float (&x)[4]) {
+  if (inner || c + 4 <= E) {
+    Four<DT> q;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) x[i][v] = c < E ? Row<DT>::get(p.v[v]) : -__builtin_inff();
+    for (int v = 0; v < 4; ++v) q.v[v] = Row<DT>::put(x[v]);
+    *reinterpret_cast<Four<DT>*>(row + c) = q;
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (c + v < E) row[c + v] = Row<DT>::put(x[v]);
   }
 }
 
@@ -141,126 +155,266 @@ __device__ __forceinline__ int sequence_of(const BArgs& a, int t) {
   return lo;
 }
 
-// p of a row in place of its logits: s / sum s, or exp(x - max) / sum where the
-// total underflows (there sigmoid(x) and exp(x) agree far past FP32).
-template <int VEC, int NI>
-__device__ __forceinline__ void shares_of_row(float (&x)[NI][VEC]) {
-  float m = -__builtin_inff();
+// Sum or maximum over a group, the same bits in each of its threads.  `box` holds
+// a word for each of the group's waves; every thread of the workgroup calls it.
+template <int G>
+__device__ __forceinline__ float group_sum(float v, float* box) {
+  v = wave_sum(v);
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+    for (int w = 0; w < G / 64; ++w) v += box[w];
+    __syncthreads();
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v, float* box) {
+  v = wave_max(v);
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = v;
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) m = fmaxf(m, x[i][v]);
-  m = wave_max(m);
-  float total = 0.0f;
+    for (int w = 0; w < G / 64; ++w) v = fmaxf(v, box[w]);
+    __syncthreads();
+  }
+  return v;
+}
+
+// out[r] = sum over the W waves of box[w * R + r], the same bits in every lane:
+// the W R words spread over the lanes, lane l with row l mod R, and a butterfly.
+template <int W, int R>
+__device__ __forceinline__ void sum_waves(const float* box, float (&out)[R]) {
+  constexpr int V = W * R, L = V < 64 ? V : 64;
+  const int lane = threadIdx.x & 63;
+  float v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < V; i += 64) v += box[i + lane % L];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      x[i][v] = m > -__builtin_inff() ? fast_exp(x[i][v] - m) : 0.0f;
-      total += x[i][v];
+  for (int m = R; m < L; m *= 2) v += __shfl_xor(v, m, 64);
+#pragma unroll
+  for (int r = 0; r < R; ++r) out[r] = lane_value(v, r);
+}
+
+// Shares of a row whose total underflows: exp(x - max) / sum (there sigmoid(x)
+// and exp(x) agree far past FP32); zero where every logit is -infinity.
+template <int DT, int G, int NI>
+__device__ __forceinline__ void far_shares(const typename Row<DT>::T* row, int c0, int E, float* box, float (&p)[NI][4]) {
+  float m = -__builtin_inff(), total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const Four<DT> q = load4<DT>(row, c0 + i * G * 4, E, i < NI - 1);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      p[i][v] = Row<DT>::get(q.v[v]);
+      m = fmaxf(m, p[i][v]);
     }
-  total = wave_sum(total);
+  }
+  m = group_max<G>(m, box);
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      p[i][v] = m > -__builtin_inff() ? fast_exp(p[i][v] - m) : 0.0f;
+      total += p[i][v];
+    }
+  total = group_sum<G>(total, box);
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) x[i][v] *= inv;
+    for (int v = 0; v < 4; ++v) p[i][v] *= inv;
 }
 
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+__device__ __forceinline__ float loss_of(const BArgs& a, double total, int filled) {
+  return filled > 0 ? (float)((double)a.coef * total * a.E / ((double)a.k * filled)) : 0.0f;
+}
+
+constexpr int kRows = 2;  // rows of a group in flight
+
 // Piece c + b holds chunk c's part of sequence b: along the tokens every next
-// (chunk, sequence) pair raises c or b, so no two pairs share a piece.
-template <int DT, int VEC, int NI>
+// (chunk, sequence) pair raises c or b, so no two pairs share a piece.  SINGLE:
+// the grid is one workgroup, which writes the results itself.
+template <int DT, int G, int NI, bool SINGLE>
 __global__ __launch_bounds__(kThreads) void k_balance_part(BArgs a) {
   typedef typename Row<DT>::T T;
-  extern __shared__ char lds[];
-  float* share = reinterpret_cast<float*>(lds);                  // [E]
-  int32_t* hist = reinterpret_cast<int32_t*>(lds) + a.E;         // [E]
+  constexpr int kGroups = kThreads / G, R = kRows;
+  extern __shared__ int32_t hist[];                     // [E]
+  float* share = reinterpret_cast<float*>(hist + a.E);  // [kGroups][E]
+  __shared__ float box[2][G / 64 * R], far_box[4];
   __shared__ int live_tokens;
+  __shared__ double loss_part[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = G == 64 ? wv : 0, c0 = (G == 64 ? lane : tid) * 4;
   const int c = blockIdx.x;
-  if (c == 0 && tid == 0) *a.ws_ticket = 0u;
+  if (!SINGLE && c == 0 && tid == 0) *a.ws_ticket = 0u;
   const int t_end = min(a.M, (c + 1) * a.chunk);
-  int t0 = c * a.chunk;
-  for (int b = sequence_of(a, t0); b < a.B && t0 < t_end; ++b) {
-    const int t1 = b == a.B - 1 ? t_end : min(offset_of(a, b + 1), t_end);
-    if (t1 <= t0) continue;
-    for (int e = tid; e < a.E; e += kThreads) {
-      share[e] = 0.0f;
-      hist[e] = 0;
-    }
+  int t0 = c * a.chunk, filled = 0;
+  double loss = 0.0;
+  for (int b = SINGLE ? 0 : sequence_of(a, t0); b < a.B && (SINGLE || t0 < t_end); ++b) {
+    const int t1 = max(t0, b == a.B - 1 ? t_end : min(offset_of(a, b + 1), t_end));
+    if (!SINGLE && t1 == t0) continue;
+    Four<DT> next[R][NI];
+    auto fetch = [&](int t) {  // rows past the sequence's last one repeat it
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          next[r][i] = load4<DT>(static_cast<const T*>(a.logits) + (size_t)min(t + r, t1 - 1) * a.E, c0 + i * G * 4, a.E,
+                                  i < NI - 1);
+    };
+    if (t1 > t0) fetch(t0 + grp * R);  // on their way while the ids are counted
+    for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
     if (tid == 0) live_tokens = 0;
     __syncthreads();
-    float acc[NI][VEC];
+    for (int i = tid; i < (t1 - t0) * a.k; i += kThreads) {
+      const int id = a.ids[(size_t)t0 * a.k + i];
+      if (id >= 0 && id < a.E && (!a.mask || a.mask[t0 + i / a.k])) atomicAdd(&hist[id], 1);
+    }
+    float acc[NI][4] = {};
+    int n = 0, turn = 0;
+    for (int tb = t0; tb < t1; tb += R * kGroups, turn ^= 1) {
+      const int t = tb + grp * R;
+      float s[R][NI][4], total[R];
+      bool live[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        live[r] = t + r < t1 && (!a.mask || a.mask[t + r]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s[r][i][v] = Row<DT>::get(next[r][i].v[v]);
+      }
+      if (tb + R * kGroups < t1) fetch(t + R * kGroups);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        total[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            s[r][i][v] = sigmoid(s[r][i][v]);
+            total[r] += s[r][i][v];
+          }
+        total[r] = wave_sum(total[r]);
+      }
+      if constexpr (G > 64) {
+        if (lane == 0)
+#pragma unroll
+          for (int r = 0; r < R; ++r) box[turn][wv * R + r] = total[r];
+        __syncthreads();
+        sum_waves<G / 64, R>(box[turn], total);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!live[r]) continue;
+        ++n;
+        float inv = 1.0f;
+        if (total[r] < kTiny)
+          far_shares<DT, G, NI>(static_cast<const T*>(a.logits) + (size_t)(t + r) * a.E, c0, a.E, far_box, s[r]);
+        else
+          inv = 1.0f / total[r];
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(s[r][i][v], inv, acc[i][v]);
+      }
+    }
+    if (kGroups > 1 && lane == 0) atomicAdd(&live_tokens, n);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[i][v] = 0.0f;
-    int n = 0;
-    for (int t = t0 + wv; t < t1; t += kWaves) {
-      if (a.mask && !a.mask[t]) continue;
-      ++n;
-      if (lane < a.k) {
-        const int id = a.ids[(size_t)t * a.k + lane];
-        if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+      for (int v = 0; v < 4; ++v)
+        if (i < NI - 1 || c0 + i * G * 4 + v < a.E) share[grp * a.E + c0 + i * G * 4 + v] = acc[i][v];
+    __syncthreads();  // the histogram is complete as well
+    if (kGroups > 1) n = live_tokens;
+    auto sum = [&](int e) {  // over the groups, in their order
+      float v = share[e];
+#pragma unroll
+      for (int w = 1; w < kGroups; ++w) v += share[w * a.E + e];
+      return v;
+    };
+    if constexpr (SINGLE) {
+      for (int e = tid; e < a.E; e += kThreads) {
+        const double mean = n > 0 ? (double)sum(e) / n : 0.0;
+        a.counts[(size_t)b * a.E + e] = hist[e];
+        a.shares[(size_t)b * a.E + e] = (float)mean;
+        if (n > 0) loss += (double)hist[e] * mean / n;
       }
-      float x[NI][VEC];
-      const T* row = static_cast<const T*>(a.logits) + (size_t)t * a.E;
-      load_row<DT, VEC, NI>(row, a.E, lane, x);
-      float s[NI][VEC], total = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          s[i][v] = sigmoid(x[i][v]);
-          total += s[i][v];
-        }
-      total = wave_sum(total);
-      if (total < kTiny) {
-        shares_of_row<VEC, NI>(x);
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) acc[i][v] += x[i][v];
-      } else {
-        const float inv = 1.0f / total;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) acc[i][v] = fmaf(s[i][v], inv, acc[i][v]);
+      filled += n > 0;
+      if (tid == 0) a.tokens[b] = n;
+    } else {
+      const size_t piece = (size_t)(c + b) * a.E;
+      for (int e = tid; e < a.E; e += kThreads) {
+        a.ws_share[piece + e] = sum(e);
+        a.ws_count[piece + e] = hist[e];
       }
+      if (tid == 0) a.ws_n[c + b] = n;
     }
-    if (lane == 0) atomicAdd(&live_tokens, n);
-    for (int w = 0; w < kWaves; ++w) {  // in wave order
-      if (wv == w)
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const int e = (i * 64 + lane) * VEC + v;
-            if (e < a.E) share[e] += acc[i][v];
-          }
-      __syncthreads();
-    }
-    const size_t piece = (size_t)(c + b);
-    for (int e = tid; e < a.E; e += kThreads) {
-      a.ws_share[piece * a.E + e] = share[e];
-      a.ws_count[piece * a.E + e] = hist[e];
-    }
-    if (tid == 0) a.ws_n[piece] = live_tokens;
     __syncthreads();
     t0 = t1;
   }
+  if constexpr (SINGLE) {
+    loss = wave_sum(loss);
+    if (lane == 0) loss_part[wv] = loss;
+    __syncthreads();
+    if (tid == 0) {
+      loss = ((loss_part[0] + loss_part[1]) + loss_part[2]) + loss_part[3];
+      a.loss[0] = loss_of(a, loss, filled);
+      a.tokens[a.B] = filled;
+    }
+  }
 }
 
-constexpr int kTile = 64;  // experts a workgroup of the second kernel adds up
+constexpr int kTile = 32;  // experts a workgroup of the second kernel adds up, a half wave to a piece
 
-__global__ __launch_bounds__(kThreads) void k_balance_sum(BArgs a) {
-  __shared__ double sh[kWaves][kTile];
-  __shared__ int ct[kWaves][kTile], nn[kWaves];
+// The tiles' parts of the loss, in their order, by one workgroup.
+__device__ __forceinline__ void finish(const BArgs& a, int tiles, double* sh, int* nn) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, waves = blockDim.x / 64;
+  double total = 0.0;
+  int filled = 0;
+#pragma unroll 4
+  for (int i = tid; i < tiles * a.B; i += blockDim.x)
+    total += __hip_atomic_load(&a.ws_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = tid; i < a.B; i += blockDim.x)
+    filled += __hip_atomic_load(&a.tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
+  total = wave_sum(total);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) filled += __shfl_xor(filled, m, 64);
+  if (lane == 0) {
+    sh[wv] = total;
+    nn[wv] = filled;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < waves; ++w) {
+      total += sh[w];
+      filled += nn[w];
+    }
+    a.tokens[a.B] = filled;
+    a.loss[0] = loss_of(a, total, filled);
+  }
+}
+
+// A half wave adds every (half waves)-th piece, eight at a time in flight.
+// TICKET: the workgroup that finishes last adds up the loss, else a third
+// launch does.
+template <bool TICKET>
+__global__ __launch_bounds__(1024) void k_balance_sum(BArgs a) {
+  __shared__ double sh[32][kTile + 1];
+  __shared__ int ct[32][kTile + 1], nn[16];
   __shared__ bool last;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int tiles = gridDim.x, b = blockIdx.y;
-  const int e = blockIdx.x * kTile + lane;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int halves = blockDim.x / 32, half = tid / 32, l = tid % 32, tiles = gridDim.x, b = blockIdx.y;
+  const int e = blockIdx.x * kTile + l, ec = min(e, a.E - 1);
   const int t0 = offset_of(a, b), t1 = b == a.B - 1 ? a.M : offset_of(a, b + 1);
   int first = 0, end = 0;
   if (t1 > t0) {
@@ -269,223 +423,352 @@ __global__ __launch_bounds__(kThreads) void k_balance_sum(BArgs a) {
   }
   double s = 0.0;
   int count = 0, n = 0;
-  for (int p = first + wv; p < end; p += kWaves) {
-    if (e < a.E) {
-      s += (double)a.ws_share[(size_t)p * a.E + e];
-      count += a.ws_count[(size_t)p * a.E + e];
+  for (int p = first + tid; p < end; p += blockDim.x) n += a.ws_n[p];
+  for (int p0 = first + half; p0 < end; p0 += 8 * halves) {
+    float f[8];
+    int i[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t at = (size_t)min(p0 + u * halves, end - 1) * a.E + ec;
+      f[u] = a.ws_share[at];
+      i[u] = a.ws_count[at];
     }
-    n += a.ws_n[p];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (p0 + u * halves < end) {
+        s += (double)f[u];
+        count += i[u];
+      }
   }
-  sh[wv][lane] = s;
-  ct[wv][lane] = count;
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m, 64);
+  sh[half][l] = s;
+  ct[half][l] = count;
   if (lane == 0) nn[wv] = n;
   __syncthreads();
-  if (wv == 0) {
-    n = nn[0] + nn[1] + nn[2] + nn[3];
-    s = ((sh[0][lane] + sh[1][lane]) + sh[2][lane]) + sh[3][lane];
-    count = ct[0][lane] + ct[1][lane] + ct[2][lane] + ct[3][lane];
-    const double share = n > 0 ? s / n : 0.0;
-    if (e < a.E) {
-      a.counts[(size_t)b * a.E + e] = count;
-      a.shares[(size_t)b * a.E + e] = (float)share;
-    }
-    double part = e < a.E && n > 0 ? (double)count * share / n : 0.0;
+  // the halves of a column lie side by side now, for a butterfly
+  const int h = tid % halves, col = tid / halves, ecol = blockIdx.x * kTile + col;
+  s = sh[h][col];
+  count = ct[h][col];
+  for (int m = halves / 2; m >= 1; m >>= 1) {
+    s += __shfl_xor(s, m, 64);
+    count += __shfl_xor(count, m, 64);
+  }
+  n = nn[0];
+  for (int w = 1; w < halves / 2; ++w) n += nn[w];
+  const double share = n > 0 ? s / n : 0.0;
+  if (h == 0 && ecol < a.E) {
+    a.counts[(size_t)b * a.E + ecol] = count;
+    a.shares[(size_t)b * a.E + ecol] = (float)share;
+  }
+  __syncthreads();
+  if (h == 0) sh[0][col] = ecol < a.E && n > 0 ? (double)count * share / n : 0.0;
+  __syncthreads();
+  if (tid < 32) {
+    double part = sh[0][tid];
 #pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, 64);
-    if (lane == 0) {
+    for (int m = 16; m >= 1; m >>= 1) part += __shfl_xor(part, m, 32);
+    if (tid == 0) {
       a.ws_loss[(size_t)b * tiles + blockIdx.x] = part;
       if (blockIdx.x == 0) a.tokens[b] = n;
+      if constexpr (TICKET) {
+        __threadfence();
+        last = atomicAdd(a.ws_ticket, 1u) == (uint32_t)tiles * (uint32_t)a.B - 1u;
+        __threadfence();
+      }
     }
   }
-  // the workgroup that finishes last adds the tiles up in their order
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    last = atomicAdd(a.ws_ticket, 1u) == (uint32_t)tiles * (uint32_t)a.B - 1u;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  double total = 0.0;
-  int filled = 0;
-  for (int i = tid; i < tiles * a.B; i += kThreads) total += __hip_atomic_load(&a.ws_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = tid; i < a.B; i += kThreads)
-    filled += __hip_atomic_load(&a.tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    total += __shfl_xor(total, m, 64);
-    filled += __shfl_xor(filled, m, 64);
-  }
-  if (lane == 0) {
-    sh[wv][0] = total;
-    nn[wv] = filled;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    filled = nn[0] + nn[1] + nn[2] + nn[3];
-    total = ((sh[0][0] + sh[1][0]) + sh[2][0]) + sh[3][0];
-    a.tokens[a.B] = filled;
-    a.loss[0] = filled > 0 ? (float)((double)a.coef * total * a.E / ((double)a.k * filled)) : 0.0f;
+  if constexpr (TICKET) {
+    __syncthreads();
+    if (last) finish(a, tiles, &sh[0][0], nn);
   }
 }
 
+__global__ __launch_bounds__(1024) void k_balance_loss(BArgs a, int tiles) {
+  __shared__ double sh[16];
+  __shared__ int nn[16];
+  finish(a, tiles, sh, nn);
+}
+
 // No token: zeros, one workgroup.
-__global__ __launch_bounds__(kThreads) void k_balance_none(BArgs a) {
-  for (size_t i = threadIdx.x; i < (size_t)a.B * a.E; i += kThreads) {
+__global__ __launch_bounds__(256) void k_balance_none(BArgs a) {
+  for (size_t i = threadIdx.x; i < (size_t)a.B * a.E; i += 256) {
     a.counts[i] = 0;
     a.shares[i] = 0.0f;
   }
-  for (int i = threadIdx.x; i <= a.B; i += kThreads) a.tokens[i] = 0;
+  for (int i = threadIdx.x; i <= a.B; i += 256) a.tokens[i] = 0;
   if (threadIdx.x == 0) a.loss[0] = 0.0f;
+}
+
+// Rows of a group in flight in the backward pass: one keeps three workgroups of
+// 896 experts on a compute unit that two do not (8192 x 896: 18 and 26 us); a
+// workgroup's barriers want two (16384 x 4096: 139 and 133 us).
+__host__ __device__ constexpr int back_rows(int G) { return G == 64 ? 1 : 2; }
+
+// Reductions over segments of S lanes, the same bits in each lane of a segment.
+template <int S>
+__device__ __forceinline__ float seg_sum(float v) {
+  if constexpr (S == 64) return wave_sum(v);
+  v += dpp<0x128, 0xF>(0.0f, v);  // rows of 16 lanes rotated by 8, 4, 2, 1
+  v += dpp<0x124, 0xF>(0.0f, v);
+  v += dpp<0x122, 0xF>(0.0f, v);
+  return v + dpp<0x121, 0xF>(0.0f, v);
+}
+template <int S>
+__device__ __forceinline__ float seg_max(float v) {
+  if constexpr (S == 64) return wave_max(v);
+  v = fmaxf(v, dpp<0x128, 0xF>(0.0f, v));
+  v = fmaxf(v, dpp<0x124, 0xF>(0.0f, v));
+  v = fmaxf(v, dpp<0x122, 0xF>(0.0f, v));
+  return fmaxf(v, dpp<0x121, 0xF>(0.0f, v));
+}
+
+// The gradient that a row's routing weights give the logit of this lane's pick:
+// xk its logit (-infinity: no pick), gw its weight's gradient.
+template <int S>
+__device__ __forceinline__ float pick_grad(float xk, float gw) {
+  // scores relative to exp(min(max x, 0)), so they never all underflow
+  const float m = fminf(seg_max<S>(xk), 0.0f);
+  const float u = fast_exp(-__builtin_fabsf(xk)), q = fast_rcp(1.0f + u);
+  float w = xk > 0.0f ? q : (xk != xk ? xk : fast_exp(xk - m) * q);  // s / exp(m)
+  const float rest = xk > 0.0f ? u * q : q;                          // 1 - s
+  if (m == -__builtin_inff()) w = 0.0f;
+  const float sum = seg_sum<S>(w);
+  w = sum > 0.0f || sum != sum ? w / sum : 0.0f;
+  return w * rest * (gw - seg_sum<S>(gw * w));
 }
 
 // d/dx of the balance loss of row t: g_b s' / S * (count[b,e] - sum_e' count[b,e'] p[e']),
 // g_b = grad_loss coef E / (k n_b^2 B'); of the picks' weights:
 // w_j (1 - s_j) (grad_w_j - sum_i grad_w_i w_i), added through a row of LDS.
-template <int DT, int VEC, int NI>
+template <int DT, int G, int NI>
 __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
   typedef typename Row<DT>::T T;
-  extern __shared__ char lds[];
-  float* cnt = reinterpret_cast<float*>(lds);                                     // [E]
+  constexpr int kGroups = kThreads / G, R = back_rows(G);
+  extern __shared__ float picks[];  // [kGroups][R][E], zero between batches
+  __shared__ float box[2][G / 64 * R], far_box[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  float* extra = reinterpret_cast<float*>(lds) + (size_t)a.E * (1 + wv);          // [E] of this wave
+  const int grp = G == 64 ? wv : 0, c0 = (G == 64 ? lane : tid) * 4;
+  float* extra = picks + (size_t)grp * R * a.E;
   const int c = blockIdx.x;
   const int t_end = min(a.M, (c + 1) * a.chunk);
   int t0 = c * a.chunk;
-  for (int e = lane; e < a.E; e += 64) extra[e] = 0.0f;
   const float gl = a.grad_loss ? *a.grad_loss : 1.0f;
   const int filled = a.counts ? a.tokens[a.B] : 0;
+  bool fresh = true;
   for (int b = sequence_of(a, t0); b < a.B && t0 < t_end; ++b) {
     const int t1 = b == a.B - 1 ? t_end : min(offset_of(a, b + 1), t_end);
     if (t1 <= t0) continue;
-    __syncthreads();
-    if (a.counts)
-      for (int e = tid; e < a.E; e += kThreads) cnt[e] = (float)a.counts[(size_t)b * a.E + e];
-    const int n = a.counts ? a.tokens[b] : 0;
-    const float g = n > 0 && filled > 0
-                        ? (float)((double)gl * a.coef * a.E / ((double)a.k * n * (double)n * filled))
-                        : 0.0f;
-    __syncthreads();
-    for (int t = t0 + wv; t < t1; t += kWaves) {
-      T* dst = static_cast<T*>(a.out) + (size_t)t * a.E;
-      struct alignas(sizeof(T) * VEC) Pack {
-        T v[VEC];
-      };
-      if (a.mask && !a.mask[t]) {
+    Four<DT> next[R][NI];
+    auto fetch = [&](int t) {  // rows past the sequence's last one repeat it
+      if (a.counts)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int e = (i * 64 + lane) * VEC;
-          if (e < a.E) *reinterpret_cast<Pack*>(dst + e) = Pack{};
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+            next[r][i] =
+                load4<DT>(static_cast<const T*>(a.logits) + (size_t)min(t + r, t1 - 1) * a.E, c0 + i * G * 4, a.E,
+                                  i < NI - 1);
+    };
+    // picks: up to 16 of them, the batch's rows side by side in 16 lanes each of the
+    // group's first wave; more, a row in each of its first waves (or one after another)
+    const bool few = a.k <= 16;
+    constexpr int kTurns = G > 64 ? 1 : R;
+    const int seg = lane / 16;
+    auto row_of = [&](int i) { return few ? seg : G > 64 ? wv : i; };
+    // a batch's ids are two batches ahead, the logits that they name one
+    int id[kTurns], next_id[kTurns];
+    float gw[kTurns], next_gw[kTurns];
+    T xk[kTurns];
+    auto fetch_ids = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int r = row_of(i), j = few ? lane % 16 : lane;
+        next_id[i] = -1;
+        next_gw[i] = 0.0f;
+        if (r < R && (!few || (i == 0 && (G == 64 || wv == 0))) && j < a.k && t + r < t1 &&
+            (!a.mask || a.mask[t + r])) {
+          next_id[i] = a.ids[(size_t)(t + r) * a.k + j];
+          next_gw[i] = a.grad_w[(size_t)(t + r) * a.k + j];
         }
-        continue;
       }
-      const T* row = static_cast<const T*>(a.logits) + (size_t)t * a.E;
-      int id = -1;
-      float gw = 0.0f, xk = -__builtin_inff();
-      if (a.grad_w && lane < a.k) {
-        id = a.ids[(size_t)t * a.k + lane];
-        gw = a.grad_w[(size_t)t * a.k + lane];
-        if (id < 0 || id >= a.E) {
-          id = -1;
-          gw = 0.0f;
-        } else {
-          xk = Row<DT>::get(row[id]);
+    };
+    auto fetch_picks = [&](int t) {  // of the batch whose ids have come, and the next one's ids
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        id[i] = next_id[i] < a.E ? next_id[i] : -1;
+        gw[i] = id[i] >= 0 ? next_gw[i] : 0.0f;
+        xk[i] = Row<DT>::put(-__builtin_inff());
+        if (id[i] >= 0) xk[i] = static_cast<const T*>(a.logits)[(size_t)(t + row_of(i)) * a.E + id[i]];
+      }
+      fetch_ids(t + R * kGroups);
+    };
+    if (a.grad_w) fetch_ids(t0 + grp * R);
+    fetch(t0 + grp * R);
+    float cnt[NI][4] = {}, g = 0.0f;
+    if (a.counts) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (i < NI - 1 || c0 + i * G * 4 + v < a.E) cnt[i][v] = (float)a.counts[(size_t)b * a.E + c0 + i * G * 4 + v];
+      const int n = a.tokens[b];
+      if (n > 0 && filled > 0)
+        g = (float)((double)gl * a.coef * a.E / ((double)a.k * n * (double)n * filled));
+    }
+    if (a.grad_w) {
+      if (fresh) {
+        for (int i = tid; i < kGroups * R * a.E; i += kThreads) picks[i] = 0.0f;
+        __syncthreads();
+      }
+      fetch_picks(t0 + grp * R);
+    }
+    fresh = false;
+    for (int tb = t0; tb < t1; tb += R * kGroups) {
+      const int t = tb + grp * R;
+      const T* row = static_cast<const T*>(a.logits) + (size_t)min(t, t1 - 1) * a.E;
+      float d[R][NI][4], total[R], dot[R];
+      bool live[R];
+      int at[kTurns];  // the picks' places in LDS, -1 for none
+      float p[kTurns];
+      if (a.grad_w)
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          at[i] = id[i] >= 0 ? row_of(i) * a.E + id[i] : -1;
+          const float x = Row<DT>::get(xk[i]);
+          p[i] = few ? pick_grad<16>(x, gw[i]) : pick_grad<64>(x, gw[i]);
         }
-      }
-      float d[NI][VEC], cv[NI][VEC], dot = 0.0f, scale = 0.0f;
-      if (a.counts) {
-        float x[NI][VEC], s[NI][VEC], total = 0.0f;
-        load_row<DT, VEC, NI>(row, a.E, lane, x);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            s[i][v] = sigmoid(x[i][v], d[i][v]);
-            total += s[i][v];
-          }
-        total = wave_sum(total);
-        if (total < kTiny) {
-          shares_of_row<VEC, NI>(x);
+      for (int r = 0; r < R; ++r) {
+        live[r] = t + r < t1 && (!a.mask || a.mask[t + r]);
+        if (a.counts)
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) s[i][v] = d[i][v] = x[i][v];
-          scale = 1.0f;
-        } else {
-          scale = 1.0f / total;
+            for (int v = 0; v < 4; ++v) d[r][i][v] = Row<DT>::get(next[r][i].v[v]);
+      }
+      if (tb + R * kGroups < t1) {
+        if (a.grad_w) fetch_picks(t + R * kGroups);
+        fetch(t + R * kGroups);
+      }
+      if (a.grad_w)
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+          if (at[i] >= 0) atomicAdd(&extra[at[i]], p[i]);
+      if (a.counts) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          total[r] = dot[r] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float s = sigmoid(d[r][i][v], d[r][i][v]);
+              total[r] += s;
+              dot[r] = fmaf(cnt[i][v], s, dot[r]);
+            }
+          total[r] = wave_sum(total[r]);
+          dot[r] = wave_sum(dot[r]);
         }
+        if constexpr (G > 64) {
+          if (lane == 0)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+            for (int r = 0; r < R; ++r) {
+              box[0][wv * R + r] = total[r];
+              box[1][wv * R + r] = dot[r];
+            }
+        }
+      }
+      if constexpr (G > 64) __syncthreads();
+      else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (G > 64 && a.counts) {
+        sum_waves<G / 64, R>(box[0], total);
+        sum_waves<G / 64, R>(box[1], dot);
+      }
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const int e = (i * 64 + lane) * VEC + v;
-            cv[i][v] = e < a.E ? cnt[e] : 0.0f;
-            dot = fmaf(cv[i][v], s[i][v], dot);
+      for (int r = 0; r < R; ++r) {
+        if (t + r >= t1) continue;
+        float f = 0.0f, mean = 0.0f;
+        if (live[r] && a.counts) {
+          float scale = 1.0f;
+          if (total[r] < kTiny) {
+            far_shares<DT, G, NI>(row + (size_t)r * a.E, c0, a.E, far_box, d[r]);
+            dot[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) dot[r] = fmaf(cnt[i][v], d[r][i][v], dot[r]);
+            dot[r] = group_sum<G>(dot[r], far_box);
+          } else {
+            scale = 1.0f / total[r];
           }
-        dot = wave_sum(dot) * scale;
-      }
-      if (a.grad_w) {
-        // scores of the picks relative to exp(min(max x, 0)), so they never all underflow
-        const float m = fminf(wave_max(xk), 0.0f);
-        float w = 0.0f, rest = 0.0f;
-        if (id >= 0 && m > -__builtin_inff()) {
-          const float u = fast_exp(-__builtin_fabsf(xk));
-          const float r = fast_rcp(1.0f + u);
-          w = xk > 0.0f ? r : (xk != xk ? xk : fast_exp(xk - m) * r);  // s / exp(m)
-          rest = xk > 0.0f ? u * r : r;                                // 1 - s
+          f = g * scale;
+          mean = dot[r] * scale * f;
         }
-        const float sum = wave_sum(w);
-        w = sum > 0.0f || sum != sum ? w / sum : 0.0f;
-        const float mean = wave_sum(gw * w);
-        if (id >= 0) atomicAdd(&extra[id], w * rest * (gw - mean));
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // other lanes read it below
-      }
-      const float f = g * scale;
+        T* dst = static_cast<T*>(a.out) + (size_t)(t + r) * a.E;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int e = (i * 64 + lane) * VEC;
-        if (e < a.E) {
-          Pack o;
+        for (int i = 0; i < NI; ++i) {
+          float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const int col = c0 + i * G * 4;
+          if (live[r] && a.counts)
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const float add = a.grad_w ? extra[e + v] : 0.0f;
-            o.v[v] = Row<DT>::put(a.counts ? fmaf((cv[i][v] - dot) * f, d[i][v], add) : add);
-          }
-          *reinterpret_cast<Pack*>(dst + e) = o;
+            for (int v = 0; v < 4; ++v) o[v] = fmaf(cnt[i][v], f, -mean) * d[r][i][v];
+          if (live[r] && a.grad_w)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (i < NI - 1 || col + v < a.E) o[v] += extra[(size_t)r * a.E + col + v];
+          store4<DT>(dst, col, a.E, i < NI - 1, o);
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (id >= 0) extra[id] = 0.0f;
+      if constexpr (G > 64) __syncthreads();
+      else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (a.grad_w)
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+          if (at[i] >= 0) extra[at[i]] = 0.0f;
     }
     t0 = t1;
   }
 }
 
-constexpr int kMaxChunks = 1024;
-
-int choose_chunk(int M) {
-  int c = (M + kMaxChunks - 1) / kMaxChunks;
-  c = (c + kWaves - 1) / kWaves * kWaves;
-  return c < 2 * kWaves ? 2 * kWaves : c;
-}
-
 size_t align16(size_t v) { return (v + 15) & ~size_t(15); }
 
+// Threads that share a row: a wave while sixteen columns a lane hold it.  (With
+// four columns a thread and up to 1024 threads a row, the sums over the lanes
+// cost a quarter of the arithmetic and a barrier of sixteen waves held the loads
+// back: 8192 x 896 backward 19 us, 16384 x 4096 150.)
+int group_of(int E) { return E <= 1024 ? 64 : 256; }
+
+constexpr int kSingleBatches = 4;  // batches that one workgroup does alone
+constexpr int kSingleB = 64;
+constexpr int kTicketMax = 64;  // workgroups of the second kernel that may share a counter (40 ns each)
+
+// Tokens of a workgroup when `grid` of them run at once.
+int chunk_of(int M, int E, int rows, int grid) {
+  const int batch = rows * (kThreads / group_of(E)), each = (M + grid - 1) / grid;
+  return each <= batch ? batch : (each + batch - 1) / batch * batch;
+}
+
 struct Plan {
-  int chunk, chunks, tiles;
+  int chunk, chunks, tiles, waves;
+  bool single;
   size_t share, count, n, loss, ticket, total;
 };
 
 Plan plan_of(int M, int E, int B) {
   Plan p{};
-  p.chunk = choose_chunk(M);
+  const int alone = kSingleBatches * kRows * (kThreads / group_of(E));
+  p.single = M <= alone && B <= kSingleB;
+  p.chunk = p.single ? alone : chunk_of(M, E, kRows, 512);
   p.chunks = (M + p.chunk - 1) / p.chunk;
   p.tiles = (E + kTile - 1) / kTile;
-  const size_t pieces = (size_t)p.chunks + B;
+  // waves of the second kernel: sixteen for long sequences, four for many short ones
+  p.waves = p.chunks / B >= 64 ? 16 : 4;
+  const size_t all = (size_t)p.chunks + B;
   p.share = 0;
-  p.count = p.share + align16(pieces * E * 4);
-  p.n = p.count + align16(pieces * E * 4);
-  p.loss = p.n + align16(pieces * 4);
+  p.count = p.share + align16(all * E * 4);
+  p.n = p.count + align16(all * E * 4);
+  p.loss = p.n + align16(all * 4);
   p.ticket = p.loss + align16((size_t)B * p.tiles * 8);
   p.total = p.ticket + 16;
   return p;
@@ -495,45 +778,37 @@ bool valid_sizes(int M, int E, int k, int B) {
   return M >= 0 && E >= 1 && E <= 4096 && k >= 1 && k <= 64 && B >= 1 && B <= 65535;
 }
 
-enum { kPart, kBack };
+enum { kPart, kSingle, kBack };
 
-template <int WHAT, int DT, int VEC, int NI>
+template <int WHAT, int DT, int G, int NI>
 const void* one() {
-  if constexpr (WHAT == kPart) return reinterpret_cast<const void*>(k_balance_part<DT, VEC, NI>);
-  else return reinterpret_cast<const void*>(k_router_backward<DT, VEC, NI>);
+  if constexpr (WHAT == kBack) return reinterpret_cast<const void*>(k_router_backward<DT, G, NI>);
+  else return reinterpret_cast<const void*>(k_balance_part<DT, G, NI, WHAT == kSingle>);
 }
-
 template <int WHAT, int DT>
-const void* pick(int E, bool even) {
-  if (even) {
-    const int ni = (E + 127) / 128;
-    if (ni <= 1) return one<WHAT, DT, 2, 1>();
-    if (ni <= 2) return one<WHAT, DT, 2, 2>();
-    if (ni <= 3) return one<WHAT, DT, 2, 3>();
-    if (ni <= 4) return one<WHAT, DT, 2, 4>();
-    if (ni <= 6) return one<WHAT, DT, 2, 6>();
-    if (ni <= 7) return one<WHAT, DT, 2, 7>();
-    if (ni <= 8) return one<WHAT, DT, 2, 8>();
-    if (ni <= 12) return one<WHAT, DT, 2, 12>();
-    if (ni <= 16) return one<WHAT, DT, 2, 16>();
-    if (ni <= 24) return one<WHAT, DT, 2, 24>();
-    return one<WHAT, DT, 2, 32>();
+const void* kernel_of(int E) {
+  if (group_of(E) == 64) {
+    switch ((E + 255) / 256) {
+      case 1: return one<WHAT, DT, 64, 1>();
+      case 2: return one<WHAT, DT, 64, 2>();
+      case 3: return one<WHAT, DT, 64, 3>();
+      default: return one<WHAT, DT, 64, 4>();
+    }
   }
-  const int ni = (E + 63) / 64;
-  if (ni <= 2) return one<WHAT, DT, 1, 2>();
-  if (ni <= 8) return one<WHAT, DT, 1, 8>();
-  if (ni <= 24) return one<WHAT, DT, 1, 24>();
-  return one<WHAT, DT, 1, 64>();
+  switch ((E + 1023) / 1024) {
+    case 2: return one<WHAT, DT, 256, 2>();
+    case 3: return one<WHAT, DT, 256, 3>();
+    default: return one<WHAT, DT, 256, 4>();
+  }
 }
-
 template <int WHAT>
-const void* kernel_of(int dtype, int E, bool even) {
-  return dtype == MRS_DTYPE_F32 ? pick<WHAT, MRS_DTYPE_F32>(E, even) : pick<WHAT, MRS_DTYPE_BF16>(E, even);
+const void* kernel_of(int dtype, int E) {
+  return dtype == MRS_DTYPE_F32 ? kernel_of<WHAT, MRS_DTYPE_F32>(E) : kernel_of<WHAT, MRS_DTYPE_BF16>(E);
 }
 
-int launch(const void* fn, dim3 grid, size_t lds, BArgs& a, void* stream) {
+int launch(const void* fn, dim3 grid, int threads, size_t lds, BArgs& a, void* stream) {
   void* params[] = {&a};
-  return hipLaunchKernel(fn, grid, dim3(kThreads), params, lds, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+  return hipLaunchKernel(fn, grid, dim3(threads), params, lds, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? MRS_OK
              : MRS_ERR_LAUNCH;
 }
@@ -566,13 +841,12 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   a.k = k;
   a.B = B;
   a.chunk = p.chunk;
-  a.chunks = p.chunks;
   a.coef = coef;
   a.loss = loss;
   a.counts = counts;
   a.tokens = tokens;
   a.shares = shares;
-  if (M == 0) return launch(reinterpret_cast<const void*>(k_balance_none), dim3(1), 0, a, stream);
+  if (M == 0) return launch(reinterpret_cast<const void*>(k_balance_none), dim3(1), 256, 0, a, stream);
   if (!logits || !ids) return MRS_ERR_NULL_POINTER;
   const int size = logits_dtype == MRS_DTYPE_F32 ? 4 : 2;
   if (!aligned(logits, size) || !aligned(ids, 4) || !aligned(seq_offsets, 4)) return MRS_ERR_MISALIGNED;
@@ -584,10 +858,20 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   a.ws_n = reinterpret_cast<int32_t*>(ws + p.n);
   a.ws_loss = reinterpret_cast<double*>(ws + p.loss);
   a.ws_ticket = reinterpret_cast<uint32_t*>(ws + p.ticket);
-  const bool even = E % 2 == 0 && aligned(logits, 2 * size);
-  int rc = launch(kernel_of<kPart>(logits_dtype, E, even), dim3(p.chunks), (size_t)E * 8, a, stream);
-  if (rc == MRS_OK) rc = launch(reinterpret_cast<const void*>(k_balance_sum), dim3(p.tiles, B), 0, a, stream);
-  return rc;
+  const size_t lds = (size_t)E * 4 * (1 + kThreads / group_of(E));
+  if (p.single) return launch(kernel_of<kSingle>(logits_dtype, E), dim3(1), kThreads, lds, a, stream);
+  int rc = launch(kernel_of<kPart>(logits_dtype, E), dim3(p.chunks), kThreads, lds, a, stream);
+  if (rc != MRS_OK) return rc;
+  if ((int64_t)p.tiles * B <= kTicketMax)
+    return launch(reinterpret_cast<const void*>(k_balance_sum<true>), dim3(p.tiles, B), p.waves * 64, 0, a, stream);
+  rc = launch(reinterpret_cast<const void*>(k_balance_sum<false>), dim3(p.tiles, B), p.waves * 64, 0, a, stream);
+  if (rc != MRS_OK) return rc;
+  int tiles = p.tiles;
+  void* params[] = {&a, &tiles};
+  return hipLaunchKernel(reinterpret_cast<const void*>(k_balance_loss), dim3(1), dim3(1024), params, 0,
+                         reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? MRS_OK
+             : MRS_ERR_LAUNCH;
 }
 
 extern "C" int moe_router_backward(const void* logits, int logits_dtype, const int32_t* ids, const float* grad_w,
@@ -612,14 +896,13 @@ extern "C" int moe_router_backward(const void* logits, int logits_dtype, const i
   a.E = E;
   a.k = k;
   a.B = B;
-  a.chunk = choose_chunk(M);
-  a.chunks = (M + a.chunk - 1) / a.chunk;
+  a.chunk = chunk_of(M, E, back_rows(group_of(E)), E <= 1024 ? 1024 : 512);
   a.coef = coef;
   a.counts = const_cast<int32_t*>(counts);
   a.tokens = const_cast<int32_t*>(tokens);
   a.grad_w = grad_w;
   a.grad_loss = grad_loss;
   a.out = grad_logits;
-  const bool even = E % 2 == 0 && aligned(logits, 2 * size) && aligned(grad_logits, 2 * size);
-  return launch(kernel_of<kBack>(logits_dtype, E, even), dim3(a.chunks), (size_t)E * 4 * (1 + kWaves), a, stream);
+  const size_t lds = grad_w ? (size_t)back_rows(group_of(E)) * (kThreads / group_of(E)) * E * 4 : 0;
+  return launch(kernel_of<kBack>(logits_dtype, E), dim3((M + a.chunk - 1) / a.chunk), kThreads, lds, a, stream);
 }

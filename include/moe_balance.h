@@ -45,7 +45,7 @@ size_t moe_balance_workspace_bytes(int M, int E, int k, int B);
  *                aligned; never cleared between calls; calls that may overlap in
  *                time need distinct workspaces
  * The sums run in a fixed order: equal inputs give equal bits.  Asynchronous on
- * `stream`; two launches; allocates nothing.  Returns MRS_OK or a negative
+ * `stream`; one to three launches; allocates nothing.  Returns MRS_OK or a negative
  * MRS_ERR_* code before any launch.
  */
 int moe_balance_loss(const void* logits, int logits_dtype, const int32_t* ids, const int32_t* seq_offsets,
