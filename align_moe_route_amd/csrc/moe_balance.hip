@@ -111,15 +111,30 @@ constexpr int kThreads = 256;
 
 // Four columns from c of a row of E, as stored; columns past E read as -infinity,
 // whose score is zero.  Rows need no more alignment than their elements.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 template <int DT>
-struct __attribute__((packed, aligned(sizeof(typename Row<DT>::T)))) Four {
-  typename Row<DT>::T v[4];
+union Four;
+template <>
+union Four<MRS_DTYPE_F32> {
+  typedef u32x4_any Wide;
+  float v[4];
+  u32x4_any w;
+};
+template <>
+union Four<MRS_DTYPE_BF16> {
+  typedef u32x2_any Wide;
+  uint16_t v[4];
+  u32x2_any w;
 };
 // `inner`: of a thread's column groups all but the last lie inside the row.
 template <int DT>
 __device__ __forceinline__ Four<DT> load4(const typename Row<DT>::T* row, int c, int E, bool inner) {
-  if (inner || c + 4 <= E) return *reinterpret_cast<const Four<DT>*>(row + c);
   Four<DT> q;
+  if (inner || c + 4 <= E) {
+    q.w = *reinterpret_cast<const typename Four<DT>::Wide*>(row + c);
+    return q;
+  }
 #pragma unroll
   for (int v = 0; v < 4; ++v) q.v[v] = c + v < E ? row[c + v] : Row<DT>::put(-__builtin_inff());
   return q;
@@ -130,7 +145,7 @@ __device__ __forceinline__ void store4(typename Row<DT>::T* row, int c, int E, b
     Four<DT> q;
 #pragma unroll
     for (int v = 0; v < 4; ++v) q.v[v] = Row<DT>::put(x[v]);
-    *reinterpret_cast<Four<DT>*>(row + c) = q;
+    *reinterpret_cast<typename Four<DT>::Wide*>(row + c) = q.w;
   } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v)

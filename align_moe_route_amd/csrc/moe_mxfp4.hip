@@ -34,7 +34,8 @@ struct QArgs {
   void* values;
   int64_t rows, stride, groups;  // groups: eights of columns, rows * gpr
   int K, gpr;                    // gpr: groups per row, Kp / 8
-  uint32_t gpr_mul;              // ceil(2^32 / gpr)
+  uint32_t gpr_mul;              // ceil(2^32 / gpr): exact below 2^17 + 2^8
+  uint64_t gpr_mul64;            // floor(2^64 / gpr) + 1: exact below 2^49
 };
 
 template <int DT>
@@ -66,39 +67,42 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
 }
 
-// VEC: 16-byte accesses (rows of x aligned, K a multiple of 8).  Every lane of
-// a quad belongs to the same row (gpr is a multiple of 16) and all of them run.
-template <int DT, bool VEC, bool VALUES>
+// Eight values as stored.  Rows need no more alignment than their elements: the
+// wide global accesses accept that.
+template <typename T>
+union Eight {
+  T v[8];
+  u32x4 q[sizeof(T) / 2];
+};
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Every lane of a quad belongs to the same row (gpr is a multiple of 16) and all
+// of them run.
+template <int DT, bool VALUES>
 __global__ __launch_bounds__(kQThreads) void k_quantize(QArgs a) {
   typedef Elem<DT> El;
   typedef typename El::T T;
   const int64_t g0 = (int64_t)blockIdx.x * kQThreads;
-  const int64_t row0 = g0 / a.gpr;
+  const int64_t row0 = (int64_t)__umul64hi((uint64_t)g0, a.gpr_mul64);  // g0 / gpr
   const uint32_t in = (uint32_t)(g0 - row0 * a.gpr) + threadIdx.x;
   const uint32_t dr = __umulhi(in, a.gpr_mul);  // in / gpr
   const int64_t row = row0 + dr;
   const int g = (int)(in - dr * (uint32_t)a.gpr), c0 = g * 8;
   const bool live = row < a.rows;
   const T* src = static_cast<const T*>(a.x) + row * a.stride + c0;
-  T raw[8];
-  if (VEC) {
-    if (live && c0 < a.K) {
+  Eight<T> raw;
+  if (live && c0 + 8 <= a.K) {
 #pragma unroll
-      for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i)
-        reinterpret_cast<u32x4*>(raw)[i] = reinterpret_cast<const u32x4*>(src)[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = T(0);
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw.q[i] = reinterpret_cast<const u32x4_any*>(src)[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = live && c0 + i < a.K ? src[i] : T(0);
+    for (int i = 0; i < 8; ++i) raw.v[i] = live && c0 + i < a.K ? src[i] : T(0);
   }
   float v[8];
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[i] = El::get(raw[i]);
+    v[i] = El::get(raw.v[i]);
     top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
   top = quad_max(top);
@@ -127,30 +131,25 @@ __global__ __launch_bounds__(kQThreads) void k_quantize(QArgs a) {
     d[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2);
     d[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3);
     T* dst = static_cast<T*>(a.values) + row * a.K + c0;
-    T o[8];
+    Eight<T> o;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      o[i] = El::put(bad ? __uint_as_float(0x7FC00000u) : ldexpf(d[i / 2][i % 2], (int)X - 127));
-    if (VEC) {
-      if (c0 < a.K)
+      o.v[i] = El::put(bad ? __uint_as_float(0x7FC00000u) : ldexpf(d[i / 2][i % 2], (int)X - 127));
+    if (c0 + 8 <= a.K) {
 #pragma unroll
-        for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i)
-          reinterpret_cast<u32x4*>(dst)[i] = reinterpret_cast<u32x4*>(o)[i];
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<u32x4_any*>(dst)[i] = o.q[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c0 + i < a.K) dst[i] = o[i];
+        if (c0 + i < a.K) dst[i] = o.v[i];
     }
   }
 }
 
 template <int DT>
-const void* quant_kernel(bool vec, bool values) {
-  if (vec)
-    return values ? reinterpret_cast<const void*>(k_quantize<DT, true, true>)
-                  : reinterpret_cast<const void*>(k_quantize<DT, true, false>);
-  return values ? reinterpret_cast<const void*>(k_quantize<DT, false, true>)
-                : reinterpret_cast<const void*>(k_quantize<DT, false, false>);
+const void* quant_kernel(bool values) {
+  return values ? reinterpret_cast<const void*>(k_quantize<DT, true>)
+                : reinterpret_cast<const void*>(k_quantize<DT, false>);
 }
 
 // --------------------------------------------------------- grouped product
@@ -573,12 +572,11 @@ extern "C" int moe_mxfp4_quantize(const void* x, int dtype, int64_t rows, int K,
   const int gpr = (K + 127) / 128 * 16;
   if (rows > (int64_t(1) << 38) / gpr) return MRS_ERR_OVERFLOW;
   QArgs a{x, codes, scales, values, rows, row_stride, rows * gpr, K, gpr,
-          (uint32_t)(((uint64_t(1) << 32) + gpr - 1) / gpr)};
-  const bool vec = aligned(x, 16) && (!values || aligned(values, 16)) && K % 8 == 0 && row_stride * size % 16 == 0;
+          (uint32_t)(((uint64_t(1) << 32) + gpr - 1) / gpr), ~uint64_t(0) / gpr + 1};
   const int64_t grid = (a.groups + kQThreads - 1) / kQThreads;
-  const void* fn = dtype == MRS_DTYPE_F32    ? quant_kernel<MRS_DTYPE_F32>(vec, values != nullptr)
-                   : dtype == MRS_DTYPE_BF16 ? quant_kernel<MRS_DTYPE_BF16>(vec, values != nullptr)
-                                             : quant_kernel<MRS_DTYPE_F16>(vec, values != nullptr);
+  const void* fn = dtype == MRS_DTYPE_F32    ? quant_kernel<MRS_DTYPE_F32>(values != nullptr)
+                   : dtype == MRS_DTYPE_BF16 ? quant_kernel<MRS_DTYPE_BF16>(values != nullptr)
+                                             : quant_kernel<MRS_DTYPE_F16>(values != nullptr);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kQThreads), params, 0,
                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
