@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -558,14 +559,30 @@ class MXFP4(NamedTuple):
     scales: "torch.Tensor"  # uint8 [..., Kp / 32], 2^(byte - 127), 255 = NaN
 
 
+def _handle(stream, dev) -> int:
+    """The HIP stream handle of `stream`, by default of dev's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=4096)
+def _capacity(M: int, E: int, k: int, block: int):
+    return max_rows(M, E, k, block), max_blocks(M, E, k, block)
+
+
 def _check_mxfp4(q, dev, dims: int, name: str) -> int:
     """q holds contiguous 4-bit rows with `dims` dimensions on dev; returns Kp."""
     import torch
-    if not (isinstance(q, MXFP4) and all(isinstance(t, torch.Tensor) and t.device == dev and t.dtype == torch.uint8
-                                         and t.dim() == dims and t.is_contiguous() for t in q)):
+    ok = isinstance(q, MXFP4)
+    if ok:
+        for t in q:
+            ok = ok and (isinstance(t, torch.Tensor) and t.device == dev and t.dtype == torch.uint8 and t.dim() == dims
+                         and t.is_contiguous())
+    if not ok:
         raise ValueError(f"{name} must be an MXFP4 of contiguous uint8 tensors with {dims} dimensions on {dev}")
-    Kp = q.codes.shape[-1] * 2
-    if Kp == 0 or Kp % 128 or tuple(q.scales.shape) != tuple(q.codes.shape[:-1]) + (Kp // 32,):
+    shape = q.codes.shape
+    Kp = shape[-1] * 2
+    if Kp == 0 or Kp % 128 or q.scales.shape[:-1] != shape[:-1] or q.scales.shape[-1] * 32 != Kp:
         raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / 32] of the same rows, Kp a multiple of 128")
     return Kp
 
@@ -621,11 +638,10 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
         _check_tensor(values, dev, x.dtype, x.numel(), "values")
         if values.shape != x.shape:
             raise ValueError("values must have x's shape")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    handle = _handle(stream, dev)
     rc = int(lib().moe_mxfp4_quantize(x.data_ptr(), dts[x.dtype], rows, K, row_stride, out.codes.data_ptr(),
                                       out.scales.data_ptr(), values.data_ptr() if values is not None else None,
-                                      stream.cuda_stream))
+                                      handle))
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -651,7 +667,7 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
         raise ValueError("x and w disagree on K")
     E, N = w.codes.shape[:2]
     M = x.codes.shape[0] if tokens is None else int(tokens)
-    rows, blocks = max_rows(M, E, k, block), max_blocks(M, E, k, block)
+    rows, blocks = _capacity(M, E, k, block)
     if rows < 0:
         raise ValueError("invalid sizes or row capacity overflow")
     if tokens is not None and x.codes.shape[0] < rows:
@@ -664,13 +680,12 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
         raise ValueError("out must be a contiguous [max_rows, N] tensor of out_dtype on x's device")
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise NotImplementedError(f"y dtype {out.dtype} (bfloat16 or float32 only)")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    handle = _handle(stream, dev)
     rc = int(lib().moe_grouped_gemm_mxfp4(
         x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), sorted_ids.data_ptr(),
         expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, Kp, N, block,
         MRS_X_TOKENS if tokens is None else MRS_X_SORTED,
-        MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), stream.cuda_stream))
+        MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), handle))
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -714,6 +729,7 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
 def balance_workspace_bytes(M: int, E: int, k: int, B: int = 1) -> int:
     v = int(lib().moe_balance_workspace_bytes(M, E, k, B))
     if v == ctypes.c_size_t(-1).value:
@@ -747,16 +763,15 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
             _check_tensor(t, dev, dtype, 1, name)
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} must have shape {shape}")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    handle = _handle(stream, dev)
     if workspace is None:
-        workspace = _workspace(dev, stream.cuda_stream, nbytes)
+        workspace = _workspace(dev, handle, nbytes)
     else:
         _check_tensor(workspace, dev, None, 0, "workspace")
     rc = int(lib().moe_balance_loss(logits.data_ptr(), dt, ids.data_ptr(), _ptr(seq_offsets), _ptr(mask), M, E, k, B,
                                     float(coef), out.loss.data_ptr(), out.counts.data_ptr(), out.tokens.data_ptr(),
                                     out.shares.data_ptr(), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), stream.cuda_stream))
+                                    workspace.numel() * workspace.element_size(), handle))
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -789,13 +804,12 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
         _check_tensor(out, dev, logits.dtype, M * E, "out")
         if out.shape != logits.shape:
             raise ValueError("out must have the logits' shape")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    handle = _handle(stream, dev)
     rc = int(lib().moe_router_backward(logits.data_ptr(), dt, ids.data_ptr(), _ptr(grad_weights),
                                        _ptr(balance.counts) if balance is not None else None,
                                        _ptr(balance.tokens) if balance is not None else None, _ptr(grad_loss),
                                        _ptr(seq_offsets), _ptr(mask), M, E, k, B, float(coef), out.data_ptr(),
-                                       stream.cuda_stream))
+                                       handle))
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
