@@ -175,12 +175,15 @@ __device__ __forceinline__ void tile_of(int h, int ntn, int& rt, int& ct) {
   ct = j % ntn;
 }
 
-// Few rows an expert: the row tiles of one padding block (G of them) and one
-// column tile come one after another on one XCD; the pairs go to the XCDs in turn.
+// Few rows an expert: pairs of a padding block (G row tiles) and a column tile go
+// to the XCDs in turn, kPairs of them together, first row tiles first.  The later
+// row tiles are often padding only: pair by pair they fell to every G-th compute
+// unit and left it idle (one token, blocks of 32: 11.6 us).
+constexpr int kPairs = 16;
 __device__ __forceinline__ bool tile_of_block(int h, int G, int ntn, int nrt, int& rt, int& ct) {
   const int x = h % kXcds, j = h / kXcds;
-  const int u = j / G * kXcds + x;
-  rt = u / ntn * G + j % G;
+  const int u = (j / (G * kPairs) * kPairs + j % kPairs) * kXcds + x;
+  rt = u / ntn * G + j / kPairs % G;
   ct = u % ntn;
   return rt < nrt;
 }
@@ -205,13 +208,17 @@ __device__ __forceinline__ i32x8 frag(u32x4 q) {
 // lane l holds columns 32 (l / 16) .. + 31 of row l mod 16, which is one chunk
 // and one scale byte), U steps in flight at a time, and nothing goes through
 // LDS but the partial sums.  Padding rows load nothing.  Eight steps in flight
-// and 32 columns measured best: 64 tokens, 896 experts, K = 3584, N = 768 in
-// 219 us, 901 MB of weights at 4.1 TB/s (a 2 GiB copy moves 4.9); 16 columns
-// 235 us, 48 columns 235 us, four steps 238 us.
-constexpr int kRowsFN = 2, kRowsDeep = 8, kRowsCols = 16 * kRowsFN;
-template <typename Y>
+// and 32 columns measured best where there are workgroups enough: 64 tokens, 896
+// experts, K = 3584, N = 768 in 203 us, 901 MB of weights at 4.4 TB/s (a 2 GiB copy
+// moves 4.9); 16 columns 220 us, 48 columns 217 us, six steps 219 us, ten 220 us.
+// One token has 384 tiles of 32 columns: 16 columns keep all compute units busy
+// (9.0 us against 9.9).
+constexpr int kRowsDeep = 8;
+constexpr int kRowsNarrow = 1024;  // fewer tiles of 32 columns than this: tiles of 16
+
+template <typename Y, int FN>
 __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
-  constexpr int FN = kRowsFN, U = kRowsDeep;
+  constexpr int U = kRowsDeep;
   __shared__ f32x4 part[4][FN][64];
   int rt, ct;
   if (!tile_of_block((int)blockIdx.x, a.block / 16, a.ntn, a.nrt, rt, ct)) return;
@@ -239,34 +246,43 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
       wc[j] = a.wc + n * kb + q * 16;
       ws[j] = a.ws + n * ks;
     }
-    const int steps = a.K / 128;
-    for (int t0 = wv; t0 < steps; t0 += 4 * U) {
-      u32x4 xq[U], wq[U][FN];
-      int xe[U], we[U][FN];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = min(t0 + 4 * u, steps - 1);
-        xq[u] = u32x4{0u, 0u, 0u, 0u};
-        xe[u] = 0;
-        if (ok) {
-          xq[u] = *reinterpret_cast<const u32x4*>(xc + t * 64);
-          xe[u] = *reinterpret_cast<const int*>(xs + t * 4);
-        }
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          wq[u][j] = *reinterpret_cast<const u32x4*>(wc[j] + t * 64);
-          we[u][j] = *reinterpret_cast<const int*>(ws[j] + t * 4);
-        }
+    const int steps = a.K / 128, wave = __builtin_amdgcn_readfirstlane(wv);
+    u32x4 xq[U], wq[U][FN];
+    int xe[U], we[U][FN];
+    auto load = [&](int u, int t) {
+      xq[u] = u32x4{0u, 0u, 0u, 0u};
+      xe[u] = 0;
+      if (ok) {
+        xq[u] = *reinterpret_cast<const u32x4*>(xc + t * 64);
+        xe[u] = *reinterpret_cast<const int*>(xs + t * 4);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t0 + 4 * u < steps)
+      for (int j = 0; j < FN; ++j) {
+        wq[u][j] = *reinterpret_cast<const u32x4*>(wc[j] + t * 64);
+        we[u][j] = *reinterpret_cast<const int*>(ws[j] + t * 4);
+      }
+    };
+    auto multiply = [&](int u) {
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                frag(xq[u]), frag(wq[u][j]), acc[j], 4, 4, 0, (int)((uint32_t)xe[u] >> (8 * q)), 0,
-                (int)((uint32_t)we[u][j] >> (8 * q)));
+      for (int j = 0; j < FN; ++j)
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            frag(xq[u]), frag(wq[u][j]), acc[j], 4, 4, 0, (int)((uint32_t)xe[u] >> (8 * q)), 0,
+            (int)((uint32_t)we[u][j] >> (8 * q)));
+    };
+    int t = wave;
+    for (; t + 4 * (U - 1) < steps; t += 4 * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(u, t + 4 * u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) multiply(u);
     }
+    const int left = (steps - t + 3) / 4;  // of this wave, fewer than U
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (u < left) load(u, t + 4 * u);
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (u < left) multiply(u);
   }
 #pragma unroll
   for (int j = 0; j < FN; ++j) part[wv][j][lane] = acc[j];
@@ -549,12 +565,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
 }
 
 template <typename Y>
-const void* product_kernel(int bm) {
+const void* product_kernel(int bm, int bn) {
   switch (bm) {
     case 128: return reinterpret_cast<const void*>(k_product_tile<Y, 128>);
     case 64: return reinterpret_cast<const void*>(k_product_tile<Y, 64>);
     case 32: return reinterpret_cast<const void*>(k_product_tile<Y, 32>);
-    default: return reinterpret_cast<const void*>(k_product_rows<Y>);
+    default:
+      return bn == 16 ? reinterpret_cast<const void*>(k_product_rows<Y, 1>)
+                      : reinterpret_cast<const void*>(k_product_rows<Y, 2>);
   }
 }
 
@@ -607,19 +625,19 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
   if (block % 32 == 0 && routes > 16 * used) {
     bm = block % 128 == 0 && routes > 64 * used ? 128 : (block % 64 == 0 && routes > 32 * used ? 64 : 32);
   }
-  const int bn = bm == 16 ? kRowsCols : kCols;
+  const int bn = bm > 16 ? kCols : used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32;
   const int64_t nrt = row_limit / bm, ntn = ((int64_t)N + bn - 1) / bn;
   int64_t grid;
   if (bm == 16) {  // whole rounds of pairs (padding block, column tile)
     const int64_t pairs = row_limit / block * ntn;
-    grid = (pairs + kXcds - 1) / kXcds * kXcds * (block / 16);
+    grid = (pairs + kXcds * kPairs - 1) / (kXcds * kPairs) * (kXcds * kPairs) * (block / 16);
   } else {
     grid = (nrt + kXcds * kRunRows - 1) / (kXcds * kRunRows) * kRunRows * kXcds * ntn;
   }
   if (grid > INT32_MAX) return MRS_ERR_OVERFLOW;
   PArgs a{x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, y,
           M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn};
-  const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm) : product_kernel<float>(bm);
+  const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm, bn) : product_kernel<float>(bm, bn);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(bm == 16 ? 256 : kTileThreads), params, 0,
                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
