@@ -207,14 +207,14 @@ __device__ __forceinline__ i32x8 frag(u32x4 q) {
 // straight into the matrix operand's registers (v_mfma_scale_f32_16x16x128:
 // lane l holds columns 32 (l / 16) .. + 31 of row l mod 16, which is one chunk
 // and one scale byte), U steps in flight at a time, and nothing goes through
-// LDS but the partial sums.  Padding rows load nothing.  Eight steps in flight
-// and 32 columns measured best where there are workgroups enough: 64 tokens, 896
-// experts, K = 3584, N = 768 in 203 us, 901 MB of weights at 4.4 TB/s (a 2 GiB copy
-// moves 4.9); 16 columns 220 us, 48 columns 217 us, six steps 219 us, ten 220 us.
-// One token has 384 tiles of 32 columns: 16 columns keep all compute units busy
-// (9.0 us against 9.9).
+// LDS but the partial sums.  Padding rows load nothing.  896 experts, top-16, K =
+// 3584, N = 768, blocks of 32: one token in 9.0 us, 24 MB at 2.6 TB/s, of which 3.4
+// us pass with a single step (the launch, the metadata, one round trip).  Eight
+// steps in flight measured best (64 tokens 203 us, six or ten 220 us).
 constexpr int kRowsDeep = 8;
-constexpr int kRowsNarrow = 1024;  // fewer tiles of 32 columns than this: tiles of 16
+// Fewer tiles of 32 columns than this: tiles of 16 (one token, 384 tiles: 9.6 and
+// 11.7 us; two tokens, 768 tiles: 17.2 and 16.0 us).
+constexpr int kRowsNarrow = 512;
 
 template <typename Y, int FN>
 __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
@@ -312,7 +312,8 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
 // and bounded the kernel.  8192 tokens, 896 experts, top-16, K = 3584, N = 768 in
 // 450 us: 1.5 GB that must move at 3.4 TB/s; with the experts' rows read again
 // from the L2's misses and y written, 2.0 GB at 4.5 TB/s (a 2 GiB copy: 4.9), which
-// bounds it now (without the multiplications it takes 410 us).
+// bounds it now (without the multiplications it takes 410 us).  64 tokens of the
+// same experts in blocks of 16: 901 MB of weights in 177 us, 5.1 TB/s.
 constexpr int kFN = 2, kNW = 4;  // 32-column operands a wave, waves
 constexpr int kCols = kNW * kFN * 32, kTileThreads = kNW * 64;
 
@@ -348,12 +349,16 @@ __device__ __forceinline__ void stage_scales(Scale8* dst, int left, F src) {
   }
 }
 
+// Rows that a tile of BM multiplies: one of 16 fills half an operand, the other
+// half repeats row 0 of x and is not stored.
+constexpr int tile_rows(int BM) { return BM < 32 ? 32 : BM; }
+
 template <int BM>
 struct Tile {
-  u32x4 x[BM * 8], w[kCols * 8];
-  Scale8 sx[BM * kScaleSteps], sw[kCols * kScaleSteps];
-  uint32_t row[BM];        // row of x
-  uint32_t mask[BM / 32];  // rows that hold a route
+  static constexpr int kRows = tile_rows(BM);
+  u32x4 x[kRows * 8], w[kCols * 8];
+  Scale8 sx[kRows * kScaleSteps], sw[kCols * kScaleSteps];
+  uint32_t row[kRows];  // row of x
 };
 
 constexpr int kWP = kFN * 32 * 8 / 64;  // weight chunks a lane stages in a step
@@ -376,12 +381,13 @@ struct Weights {
 
 __device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
-// `live`: the leading 32-row parts of the tile that hold a route
+// `has`: a bit for each row that holds a route; `live`: the leading 32-row parts
+// of the tile that have one
 template <typename Y, int BM>
-__device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int live, const Weights& w, WeightRegs& wr,
-                                          Tile<BM>& l) {
-  constexpr int FM = BM / 32;
-  constexpr int XP = BM * 8 / kTileThreads;  // x chunks a thread stages in a step
+__device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const uint64_t (&has)[2], int live,
+                                          const Weights& w, WeightRegs& wr, Tile<BM>& l) {
+  constexpr int TR = tile_rows(BM), FM = TR / 32;
+  constexpr int XP = TR * 8 / kTileThreads;  // x chunks a thread stages in a step
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int lr = lane & 31, lh = lane >> 5;
   const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
@@ -414,7 +420,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int li
     uint32_t kv = (uint32_t)ks;
     asm volatile("" : "+s"(kv));
     const int left = (int)kv / 4 - t * 2;  // words left in a row
-    stage_scales<BM>(l.sx, left, [&](int r) { return a.xs + (size_t)l.row[r] * kv + t * 8; });
+    stage_scales<TR>(l.sx, left, [&](int r) { return a.xs + (size_t)l.row[r] * kv + t * 8; });
     if (weights)
       stage_scales<kCols>(l.sw, left, [&](int r) { return w.scales + (size_t)min(r, w.last) * kv + t * 8; });
   };
@@ -493,8 +499,8 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int li
   char* stage = reinterpret_cast<char*>(&l) + wv * 32 * kPad;
   const int n1 = n0 + wv * kFN * 32;
 #pragma unroll
-  for (int i = 0; i < BM / 32; ++i) {
-    const uint32_t rows = l.mask[i];
+  for (int i = 0; i < FM; ++i) {
+    const uint32_t rows = (uint32_t)(has[i / 2] >> (i % 2 * 32));
     Y* y = static_cast<Y*>(a.y) + (size_t)(r0 + i * 32) * a.N;
     if (wide) {
 #pragma unroll
@@ -511,7 +517,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int li
         const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
         const int n = n1 + c * (16 / (int)sizeof(Y));
         const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
-        if (n < a.N) *reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n) = o;
+        if (n < a.N && (BM >= 32 || r < BM)) *reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n) = o;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     } else {
@@ -523,7 +529,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, int li
           for (int v = 0; v < 16; ++v) {
             const int r = 8 * (v / 4) + 4 * lh + v % 4;
             const float o = (rows >> r) & 1u ? acc[i][j][v] : 0.0f;
-            put_y(y + (size_t)r * a.N + n, o);
+            if (BM >= 32 || r < BM) put_y(y + (size_t)r * a.N + n, o);
           }
       }
     }
@@ -540,40 +546,79 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   const int r0 = rt * BM, n0 = ct * kCols;
   const int npp = min(*a.npp, a.row_limit);
   const int e = __builtin_amdgcn_readfirstlane(a.eob[r0 / a.block]);
-  const int s = tid < BM ? a.sid[r0 + tid] : -1;
+  int s[2];  // slots of rows lane and 64 + lane, in every wave
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s[i] = i * 64 + lane < BM ? a.sid[r0 + i * 64 + lane] : -1;
   if (r0 + BM > npp || e < 0 || e >= a.E) return;  // npp is a multiple of block and BM divides block
+  bool ok[2];
+  uint64_t has[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ok[i] = s[i] >= 0 && s[i] < a.M * a.k;
+    has[i] = __ballot(ok[i]);
+  }
+  if (!(has[0] | has[1])) {  // padding only: no weights are read
+    const int cols = min(kCols, a.N - n0);
+    for (int i = tid; i < BM * cols; i += kTileThreads)
+      put_y(static_cast<Y*>(a.y) + (size_t)(r0 + i / cols) * a.N + n0 + i % cols, 0.0f);
+    return;
+  }
   const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
   const Weights w{a.wc + ((size_t)e * a.N + n0) * kb, a.ws + ((size_t)e * a.N + n0) * ks,
                   wv * kFN * 32 + lane / 8, a.N - 1 - n0, (uint32_t)kb};
   WeightRegs wr;
   w.load(wr, tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0));
   stage_scales<kCols>(l.sw, (int)ks / 4, [&](int r) { return w.scales + (size_t)min(r, w.last) * ks; });
-  const bool ok = s >= 0 && s < a.M * a.k;
-  if (tid < BM) {
-    l.row[tid] = ok ? (a.sorted ? r0 + tid : s / a.k) : 0;
-    const uint64_t m = __ballot(ok);
-    if (lane % 32 == 0) l.mask[tid / 32] = (uint32_t)(lane ? m >> 32 : m);
+  if (tid < l.kRows) {  // the first two waves, lane tid mod 64
+    const bool mine = ok[wv & 1];
+    const int slot = s[wv & 1];
+    l.row[tid] = mine ? (a.sorted ? r0 + tid : slot / a.k) : 0;
   }
   __syncthreads();
   // a segment's routes come first: the last 32 rows that hold one bound the work
-  int live = 1;
-#pragma unroll
-  for (int i = 1; i < BM / 32; ++i)
-    if (l.mask[i]) live = i + 1;
-  live = __builtin_amdgcn_readfirstlane(live);
-  tile_body<Y, BM>(a, r0, n0, live, w, wr, l);
+  int live = has[1] >> 32 ? 4 : has[1] ? 3 : has[0] >> 32 ? 2 : 1;
+  // opaque: knowing that the first part is live the compiler merges its block
+  // with the step's loads and spills inside the loop (1.5 ms in place of 0.45)
+  asm volatile("" : "+s"(live));
+  tile_body<Y, BM>(a, r0, n0, has, live, w, wr, l);
 }
 
 template <typename Y>
 const void* product_kernel(int bm, int bn) {
+  if (bn == 16) return reinterpret_cast<const void*>(k_product_rows<Y, 1>);
+  if (bn == 32) return reinterpret_cast<const void*>(k_product_rows<Y, 2>);
   switch (bm) {
     case 128: return reinterpret_cast<const void*>(k_product_tile<Y, 128>);
     case 64: return reinterpret_cast<const void*>(k_product_tile<Y, 64>);
     case 32: return reinterpret_cast<const void*>(k_product_tile<Y, 32>);
-    default:
-      return bn == 16 ? reinterpret_cast<const void*>(k_product_rows<Y, 1>)
-                      : reinterpret_cast<const void*>(k_product_rows<Y, 2>);
+    default: return reinterpret_cast<const void*>(k_product_tile<Y, 16>);
   }
+}
+
+// Tile sizes from the expected load.  Strips are the weights' tiles of 256 columns
+// over the experts that get a route; a workgroup of the tile kernel streams one.
+// With few of them and few rows the rows kernel's smaller tiles fill the chip (us,
+// rows kernel / tile kernel; 896 experts, top-16, K = 3584, N = 768, blocks of 32):
+// 1 token, 48 strips 9.6 / 22.6; 3 tokens, 144 strips 21.5 / 23.2; 4 tokens, 192
+// strips 26.8 / 24.3.  It reads the weights again for every 16 rows: 64 experts,
+// K = 1024, N = 512, 128 strips, 5 rows an expert 8.5 / 8.2, 10 rows 11.7 / 8.3;
+// 8 strips, 16 rows 4.2 / 7.9, 128 rows 9.9 / 8.2.
+//
+// The tile kernel takes the largest tile that divides the block (a part of 32 rows
+// without a route costs nothing but its zeros; 256 experts, K = 3584, blocks of
+// 128, 4 / 64 / 192 rows an expert: tiles of 128 99 / 111 / 149 us, of 64 107 / 129 /
+// 203, of 32 159 / 189 / 307), smaller ones where 128 workgroups would not come
+// together (8 experts, 512 tokens: tiles of 32 8.2 us, 64 10.2, 128 14.1).
+struct Shape {
+  int bm, bn;
+};
+Shape shape_of(int64_t routes, int64_t used, int N, int block) {
+  const int64_t cols = (N + kCols - 1) / kCols, strips = used * cols;
+  if (strips < 192 && strips * routes <= 768 * used)
+    return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32};
+  int bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
+  while (strips < 192 && bm > 32 && routes / bm * cols < 128) bm /= 2;
+  return {bm, kCols};
 }
 
 }  // namespace
@@ -621,14 +666,11 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
       !aligned(sorted_ids, 4) || !aligned(expert_of_block, 4) || !aligned(num_post_pad, 4) || !aligned(y, 4))
     return MRS_ERR_MISALIGNED;
   const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E;
-  int bm = 16;
-  if (block % 32 == 0 && routes > 16 * used) {
-    bm = block % 128 == 0 && routes > 64 * used ? 128 : (block % 64 == 0 && routes > 32 * used ? 64 : 32);
-  }
-  const int bn = bm > 16 ? kCols : used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32;
+  const Shape shape = shape_of(routes, used, N, block);
+  const int bm = shape.bm, bn = shape.bn;
   const int64_t nrt = row_limit / bm, ntn = ((int64_t)N + bn - 1) / bn;
   int64_t grid;
-  if (bm == 16) {  // whole rounds of pairs (padding block, column tile)
+  if (bn < kCols) {  // whole rounds of pairs (padding block, column tile)
     const int64_t pairs = row_limit / block * ntn;
     grid = (pairs + kXcds * kPairs - 1) / (kXcds * kPairs) * (kXcds * kPairs) * (block / 16);
   } else {
@@ -639,7 +681,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
           M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn};
   const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm, bn) : product_kernel<float>(bm, bn);
   void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(bm == 16 ? 256 : kTileThreads), params, 0,
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), params, 0,
                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? MRS_OK
              : MRS_ERR_LAUNCH;

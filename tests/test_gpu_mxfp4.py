@@ -146,6 +146,15 @@ SHAPES = [  # M, E, k, K, N, block, drop, skew
     (150, 3, 1, 4500, 40, 64, 0, 0),
     (70, 2, 1, 6200, 264, 32, 0, 0.5),
     (9, 3, 1, 9000, 33, 48, 0, 0),
+    # many experts with few rows: whole strips of weights, tiles of 16 to 128 rows
+    # most of which are padding
+    (70, 200, 2, 256, 40, 16, 0.1, 0),
+    (70, 200, 2, 384, 264, 48, 0, 0),
+    (90, 220, 3, 128, 24, 64, 0.5, 0),
+    (60, 250, 4, 300, 270, 128, 0.2, 0.5),
+    (100, 130, 2, 640, 300, 256, 0, 0),
+    (2, 60, 20, 700, 80, 16, 0, 0),     # 32-column tiles of the few-rows kernel
+    (2, 90, 40, 520, 200, 32, 0, 0),
 ]
 
 
