@@ -813,3 +813,50 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
+
+
+@functools.lru_cache(maxsize=1)
+def _route_train_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class RouteTrain(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, bias, sizes, coef, seq_offsets, mask):
+            out = route_sort(logits, bias, *sizes)
+            bal = balance_loss(logits, out.ids, coef, seq_offsets=seq_offsets, mask=mask)
+            ctx.save_for_backward(logits, out.ids, bal.counts, bal.tokens, seq_offsets, mask)
+            ctx.coef = coef
+            ctx.set_materialize_grads(False)
+            rest = (out.ids, out.sorted_ids, out.expert_of_block, out.num_post_pad, bal.counts, bal.tokens, bal.shares)
+            ctx.mark_non_differentiable(*rest)
+            return (out.weights, bal.loss) + rest
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad_weights, grad_loss, *_):
+            logits, ids, counts, tokens, seq_offsets, mask = ctx.saved_tensors
+            if grad_weights is None and grad_loss is None:
+                return (None,) * 6
+            balance = None if grad_loss is None else BalanceOutput(None, counts, tokens, None)
+            grad = router_backward(logits, ids, balance=balance, coef=ctx.coef, seq_offsets=seq_offsets, mask=mask,
+                                   grad_weights=None if grad_weights is None else grad_weights.float().contiguous(),
+                                   grad_loss=None if grad_loss is None else grad_loss.float().contiguous())
+            return (grad,) + (None,) * 5
+
+    return RouteTrain
+
+
+def route_sort_train(logits, bias, k: int, n_group: int, topk_group: int, block: int, *, balance_coef: float = 0.0,
+                     seq_offsets=None, mask=None):
+    """route_sort and balance_loss under autograd: (RouteSortOutput, BalanceOutput)
+    whose `weights` and `loss` carry gradients to logits (router_backward; the
+    selection and the counts are constants, the bias gets no gradient).
+
+    logits, bias and sizes as for route_sort, coefficient, seq_offsets and mask as
+    for balance_loss; padding tokens (mask) are routed as any other but take part
+    in neither the loss nor the gradients.  To capture a training step in a graph
+    call balance_loss and router_backward themselves."""
+    w, loss, ids, sid, eob, npp, counts, tokens, shares = _route_train_function().apply(
+        logits, bias, (k, n_group, topk_group, block), float(balance_coef), seq_offsets, mask)
+    return RouteSortOutput(ids, w, sid, eob, npp), BalanceOutput(loss, counts, tokens, shares)
