@@ -1,16 +1,23 @@
 // Balance loss, per-expert counts and the router's gradient, MI355X (gfx950,
 // CDNA4, wave64).  Definitions and argument contracts: include/moe_balance.h.
 //
-// Both directions read each row of logits once: a wave (up to 1024 experts) or a
-// workgroup of four takes a row, up to sixteen columns of it to a thread, the
-// next rows on their way meanwhile; a thread keeps its columns (their running
-// shares, or their counts) in registers throughout.
+// Both directions read each row of logits once: sixteen lanes (up to 256
+// experts), a wave (up to 1024) or four waves take a row, up to sixteen columns of
+// it to a thread, the next rows on their way meanwhile; a thread keeps its columns
+// (their running shares, or their counts) in registers throughout.
 // Forward: a workgroup walks a chunk of tokens; its column sums and its LDS
 // histogram of the ids go to the workspace as one piece per (chunk, sequence),
 // and a second kernel adds the pieces up in their order (one workgroup alone
 // finishes a small batch itself).  Backward: the row's counts-weighted mean comes
 // from the same pass, and the picks' gradient joins in FP32 before the one
 // rounding.
+//
+// Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s):
+// forward 16384 x 4096 FP32, 37 sequences, in 66 us (276 MB, 4.2 TB/s; the pieces
+// add 37 MB and two small launches 16 us), 65536 x 512 FP32 in 31 us; backward 118
+// and 55 us (541 and 273 MB, 4.6 and 5.0 TB/s).  8192 x 896 BF16 takes 15.5 us
+// forward, 8 of them the second launch's chain of round trips, and 13 us backward
+// (30 MB; 6 us of arithmetic, the rest latency); 131072 x 128 BF16 20 and 24 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -74,6 +81,24 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
   return v;
+}
+
+// Reductions over segments of S lanes, the same bits in each lane of a segment.
+template <int S>
+__device__ __forceinline__ float seg_sum(float v) {
+  if constexpr (S == 64) return wave_sum(v);
+  v += dpp<0x128, 0xF>(0.0f, v);  // rows of 16 lanes rotated by 8, 4, 2, 1
+  v += dpp<0x124, 0xF>(0.0f, v);
+  v += dpp<0x122, 0xF>(0.0f, v);
+  return v + dpp<0x121, 0xF>(0.0f, v);
+}
+template <int S>
+__device__ __forceinline__ float seg_max(float v) {
+  if constexpr (S == 64) return wave_max(v);
+  v = fmaxf(v, dpp<0x128, 0xF>(0.0f, v));
+  v = fmaxf(v, dpp<0x124, 0xF>(0.0f, v));
+  v = fmaxf(v, dpp<0x122, 0xF>(0.0f, v));
+  return fmaxf(v, dpp<0x121, 0xF>(0.0f, v));
 }
 
 __device__ __forceinline__ float fast_rcp(float v) { return __builtin_amdgcn_rcpf(v); }
@@ -171,10 +196,10 @@ __device__ __forceinline__ int sequence_of(const BArgs& a, int t) {
 }
 
 // Sum or maximum over a group, the same bits in each of its threads.  `box` holds
-// a word for each of the group's waves; every thread of the workgroup calls it.
+// a word for each of the group's waves; every thread of a group calls it together.
 template <int G>
 __device__ __forceinline__ float group_sum(float v, float* box) {
-  v = wave_sum(v);
+  v = seg_sum<G < 64 ? G : 64>(v);
   if constexpr (G > 64) {
     if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -187,7 +212,7 @@ __device__ __forceinline__ float group_sum(float v, float* box) {
 }
 template <int G>
 __device__ __forceinline__ float group_max(float v, float* box) {
-  v = wave_max(v);
+  v = seg_max<G < 64 ? G : 64>(v);
   if constexpr (G > 64) {
     if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -253,22 +278,23 @@ __device__ __forceinline__ float loss_of(const BArgs& a, double total, int fille
   return filled > 0 ? (float)((double)a.coef * total * a.E / ((double)a.k * filled)) : 0.0f;
 }
 
-constexpr int kRows = 2;  // rows of a group in flight
+constexpr int kPartRows = 2;  // rows of a group in flight in the forward pass
 
-// Piece c + b holds chunk c's part of sequence b: along the tokens every next
-// (chunk, sequence) pair raises c or b, so no two pairs share a piece.  SINGLE:
-// the grid is one workgroup, which writes the results itself.
+// Threads of a workgroup in the forward pass.
+__host__ __device__ constexpr int part_threads(int G) { return G < 256 ? 512 : 256; }
+
 template <int DT, int G, int NI, bool SINGLE>
-__global__ __launch_bounds__(kThreads) void k_balance_part(BArgs a) {
+__global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
   typedef typename Row<DT>::T T;
-  constexpr int kGroups = kThreads / G, R = kRows;
+  constexpr int kThreads = part_threads(G), kGroups = kThreads / G, R = kPartRows;
+  constexpr int kSeg = G < 64 ? G : 64;
   extern __shared__ int32_t hist[];                     // [E]
   float* share = reinterpret_cast<float*>(hist + a.E);  // [kGroups][E]
-  __shared__ float box[2][G / 64 * R], far_box[4];
+  __shared__ float box[2][G > 64 ? G / 64 * R : 1], far_box[4];
   __shared__ int live_tokens;
-  __shared__ double loss_part[4];
+  __shared__ double loss_part[kThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = G == 64 ? wv : 0, c0 = (G == 64 ? lane : tid) * 4;
+  const int grp = G == 64 ? wv : tid / G, c0 = tid % G * 4;
   const int c = blockIdx.x;
   if (!SINGLE && c == 0 && tid == 0) *a.ws_ticket = 0u;
   const int t_end = min(a.M, (c + 1) * a.chunk);
@@ -319,7 +345,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(BArgs a) {
             s[r][i][v] = sigmoid(s[r][i][v]);
             total[r] += s[r][i][v];
           }
-        total[r] = wave_sum(total[r]);
+        total[r] = seg_sum<kSeg>(total[r]);
       }
       if constexpr (G > 64) {
         if (lane == 0)
@@ -343,7 +369,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(BArgs a) {
           for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(s[r][i][v], inv, acc[i][v]);
       }
     }
-    if (kGroups > 1 && lane == 0) atomicAdd(&live_tokens, n);
+    if (kGroups > 1 && tid % G == 0) atomicAdd(&live_tokens, n);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -382,7 +408,8 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(BArgs a) {
     if (lane == 0) loss_part[wv] = loss;
     __syncthreads();
     if (tid == 0) {
-      loss = ((loss_part[0] + loss_part[1]) + loss_part[2]) + loss_part[3];
+      loss = loss_part[0];
+      for (int w = 1; w < kThreads / 64; ++w) loss += loss_part[w];
       a.loss[0] = loss_of(a, loss, filled);
       a.tokens[a.B] = filled;
     }
@@ -518,25 +545,7 @@ __global__ __launch_bounds__(256) void k_balance_none(BArgs a) {
 // Rows of a group in flight in the backward pass: one keeps three workgroups of
 // 896 experts on a compute unit that two do not (8192 x 896: 18 and 26 us); a
 // workgroup's barriers want two (16384 x 4096: 139 and 133 us).
-__host__ __device__ constexpr int back_rows(int G) { return G == 64 ? 1 : 2; }
-
-// Reductions over segments of S lanes, the same bits in each lane of a segment.
-template <int S>
-__device__ __forceinline__ float seg_sum(float v) {
-  if constexpr (S == 64) return wave_sum(v);
-  v += dpp<0x128, 0xF>(0.0f, v);  // rows of 16 lanes rotated by 8, 4, 2, 1
-  v += dpp<0x124, 0xF>(0.0f, v);
-  v += dpp<0x122, 0xF>(0.0f, v);
-  return v + dpp<0x121, 0xF>(0.0f, v);
-}
-template <int S>
-__device__ __forceinline__ float seg_max(float v) {
-  if constexpr (S == 64) return wave_max(v);
-  v = fmaxf(v, dpp<0x128, 0xF>(0.0f, v));
-  v = fmaxf(v, dpp<0x124, 0xF>(0.0f, v));
-  v = fmaxf(v, dpp<0x122, 0xF>(0.0f, v));
-  return fmaxf(v, dpp<0x121, 0xF>(0.0f, v));
-}
+__host__ __device__ constexpr int back_rows(int G) { return G < 256 ? 1 : 2; }
 
 // The gradient that a row's routing weights give the logit of this lane's pick:
 // xk its logit (-infinity: no pick), gw its weight's gradient.
@@ -559,11 +568,11 @@ __device__ __forceinline__ float pick_grad(float xk, float gw) {
 template <int DT, int G, int NI>
 __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
   typedef typename Row<DT>::T T;
-  constexpr int kGroups = kThreads / G, R = back_rows(G);
+  constexpr int kGroups = kThreads / G, R = back_rows(G), kSeg = G < 64 ? G : 64;
   extern __shared__ float picks[];  // [kGroups][R][E], zero between batches
-  __shared__ float box[2][G / 64 * R], far_box[4];
+  __shared__ float box[2][G > 64 ? G / 64 * R : 1], far_box[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = G == 64 ? wv : 0, c0 = (G == 64 ? lane : tid) * 4;
+  const int grp = G == 64 ? wv : tid / G, c0 = tid % G * 4;
   float* extra = picks + (size_t)grp * R * a.E;
   const int c = blockIdx.x;
   const int t_end = min(a.M, (c + 1) * a.chunk);
@@ -586,10 +595,11 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
                                   i < NI - 1);
     };
     // picks: up to 16 of them, the batch's rows side by side in 16 lanes each of the
-    // group's first wave; more, a row in each of its first waves (or one after another)
-    const bool few = a.k <= 16;
+    // group's first wave (groups of 16 have a row and no more picks); more, a row in
+    // each of its first waves (or one after another)
+    const bool few = G == 16 || a.k <= 16;
     constexpr int kTurns = G > 64 ? 1 : R;
-    const int seg = lane / 16;
+    const int seg = G == 16 ? 0 : lane / 16;
     auto row_of = [&](int i) { return few ? seg : G > 64 ? wv : i; };
     // a batch's ids are two batches ahead, the logits that they name one
     int id[kTurns], next_id[kTurns];
@@ -601,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
         const int r = row_of(i), j = few ? lane % 16 : lane;
         next_id[i] = -1;
         next_gw[i] = 0.0f;
-        if (r < R && (!few || (i == 0 && (G == 64 || wv == 0))) && j < a.k && t + r < t1 &&
+        if (r < R && (!few || (i == 0 && (G <= 64 || wv == 0))) && j < a.k && t + r < t1 &&
             (!a.mask || a.mask[t + r])) {
           next_id[i] = a.ids[(size_t)(t + r) * a.k + j];
           next_gw[i] = a.grad_w[(size_t)(t + r) * a.k + j];
@@ -682,8 +692,8 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
               total[r] += s;
               dot[r] = fmaf(cnt[i][v], s, dot[r]);
             }
-          total[r] = wave_sum(total[r]);
-          dot[r] = wave_sum(dot[r]);
+          total[r] = seg_sum<kSeg>(total[r]);
+          dot[r] = seg_sum<kSeg>(dot[r]);
         }
         if constexpr (G > 64) {
           if (lane == 0)
@@ -696,9 +706,11 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
       }
       if constexpr (G > 64) __syncthreads();
       else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (G > 64 && a.counts) {
-        sum_waves<G / 64, R>(box[0], total);
-        sum_waves<G / 64, R>(box[1], dot);
+      if constexpr (G > 64) {
+        if (a.counts) {
+          sum_waves<G / 64, R>(box[0], total);
+          sum_waves<G / 64, R>(box[1], dot);
+        }
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -748,19 +760,23 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
 
 size_t align16(size_t v) { return (v + 15) & ~size_t(15); }
 
-// Threads that share a row: a wave while sixteen columns a lane hold it.  (With
-// four columns a thread and up to 1024 threads a row, the sums over the lanes
-// cost a quarter of the arithmetic and a barrier of sixteen waves held the loads
-// back: 8192 x 896 backward 19 us, 16384 x 4096 150.)
-int group_of(int E) { return E <= 1024 ? 64 : 256; }
+// Threads that share a row: sixteen lanes while sixteen columns a lane hold it,
+// then a wave, then four.  (With four columns a thread and up to 1024 threads a
+// row, the sums over the lanes cost a quarter of the arithmetic and a barrier of
+// sixteen waves held the loads back: 8192 x 896 backward 19 us, 16384 x 4096 150.)
+// A whole wave for 128 experts left half its lanes idle and paid its sums per row:
+// 131072 x 128 forward 50 us against 20, backward 64 against 24.  Sixteen lanes have
+// no room for more than sixteen picks, a lane each.
+int group_of(int E, bool picks, int k) { return E <= 256 && !(picks && k > 16) ? 16 : E <= 1024 ? 64 : 256; }
+int columns_of(int E, int G) { return (E + 4 * G - 1) / (4 * G); }
 
 constexpr int kSingleBatches = 4;  // batches that one workgroup does alone
 constexpr int kSingleB = 64;
 constexpr int kTicketMax = 64;  // workgroups of the second kernel that may share a counter (40 ns each)
 
 // Tokens of a workgroup when `grid` of them run at once.
-int chunk_of(int M, int E, int rows, int grid) {
-  const int batch = rows * (kThreads / group_of(E)), each = (M + grid - 1) / grid;
+int chunk_of(int M, int batch, int grid) {
+  const int each = (M + grid - 1) / grid;
   return each <= batch ? batch : (each + batch - 1) / batch * batch;
 }
 
@@ -772,9 +788,10 @@ struct Plan {
 
 Plan plan_of(int M, int E, int B) {
   Plan p{};
-  const int alone = kSingleBatches * kRows * (kThreads / group_of(E));
+  const int G = group_of(E, false, 0), batch = kPartRows * (part_threads(G) / G), alone = kSingleBatches * batch;
   p.single = M <= alone && B <= kSingleB;
-  p.chunk = p.single ? alone : chunk_of(M, E, kRows, 512);
+  // a workgroup for each compute unit: eight waves, or twice four
+  p.chunk = p.single ? alone : chunk_of(M, batch, G < 256 ? 256 : 512);
   p.chunks = (M + p.chunk - 1) / p.chunk;
   p.tiles = (E + kTile - 1) / kTile;
   // waves of the second kernel: sixteen for long sequences, four for many short ones
@@ -801,24 +818,35 @@ const void* one() {
   else return reinterpret_cast<const void*>(k_balance_part<DT, G, NI, WHAT == kSingle>);
 }
 template <int WHAT, int DT>
-const void* kernel_of(int E) {
-  if (group_of(E) == 64) {
-    switch ((E + 255) / 256) {
-      case 1: return one<WHAT, DT, 64, 1>();
+const void* kernel_of(int E, int G) {
+  const int ni = columns_of(E, G);
+  if (G == 16) {
+    switch (ni) {
+      case 1: return one<WHAT, DT, 16, 1>();
+      case 2: return one<WHAT, DT, 16, 2>();
+      case 3: return one<WHAT, DT, 16, 3>();
+      default: return one<WHAT, DT, 16, 4>();
+    }
+  }
+  if (G == 64) {
+    switch (ni) {
+      case 1:
+        if constexpr (WHAT == kBack) return one<WHAT, DT, 64, 1>();  // more than sixteen picks
+        [[fallthrough]];
       case 2: return one<WHAT, DT, 64, 2>();
       case 3: return one<WHAT, DT, 64, 3>();
       default: return one<WHAT, DT, 64, 4>();
     }
   }
-  switch ((E + 1023) / 1024) {
+  switch (ni) {
     case 2: return one<WHAT, DT, 256, 2>();
     case 3: return one<WHAT, DT, 256, 3>();
     default: return one<WHAT, DT, 256, 4>();
   }
 }
 template <int WHAT>
-const void* kernel_of(int dtype, int E) {
-  return dtype == MRS_DTYPE_F32 ? kernel_of<WHAT, MRS_DTYPE_F32>(E) : kernel_of<WHAT, MRS_DTYPE_BF16>(E);
+const void* kernel_of(int dtype, int E, int G) {
+  return dtype == MRS_DTYPE_F32 ? kernel_of<WHAT, MRS_DTYPE_F32>(E, G) : kernel_of<WHAT, MRS_DTYPE_BF16>(E, G);
 }
 
 int launch(const void* fn, dim3 grid, int threads, size_t lds, BArgs& a, void* stream) {
@@ -873,9 +901,10 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   a.ws_n = reinterpret_cast<int32_t*>(ws + p.n);
   a.ws_loss = reinterpret_cast<double*>(ws + p.loss);
   a.ws_ticket = reinterpret_cast<uint32_t*>(ws + p.ticket);
-  const size_t lds = (size_t)E * 4 * (1 + kThreads / group_of(E));
-  if (p.single) return launch(kernel_of<kSingle>(logits_dtype, E), dim3(1), kThreads, lds, a, stream);
-  int rc = launch(kernel_of<kPart>(logits_dtype, E), dim3(p.chunks), kThreads, lds, a, stream);
+  const int G = group_of(E, false, k), threads = part_threads(G);
+  const size_t lds = (size_t)E * 4 * (1 + threads / G);
+  if (p.single) return launch(kernel_of<kSingle>(logits_dtype, E, G), dim3(1), threads, lds, a, stream);
+  int rc = launch(kernel_of<kPart>(logits_dtype, E, G), dim3(p.chunks), threads, lds, a, stream);
   if (rc != MRS_OK) return rc;
   if ((int64_t)p.tiles * B <= kTicketMax)
     return launch(reinterpret_cast<const void*>(k_balance_sum<true>), dim3(p.tiles, B), p.waves * 64, 0, a, stream);
@@ -911,13 +940,14 @@ extern "C" int moe_router_backward(const void* logits, int logits_dtype, const i
   a.E = E;
   a.k = k;
   a.B = B;
-  a.chunk = chunk_of(M, E, back_rows(group_of(E)), E <= 1024 ? 1024 : 512);
+  const int G = group_of(E, grad_w != nullptr, k);
+  a.chunk = chunk_of(M, back_rows(G) * (kThreads / G), G < 256 ? 1024 : 512);
   a.coef = coef;
   a.counts = const_cast<int32_t*>(counts);
   a.tokens = const_cast<int32_t*>(tokens);
   a.grad_w = grad_w;
   a.grad_loss = grad_loss;
   a.out = grad_logits;
-  const size_t lds = grad_w ? (size_t)back_rows(group_of(E)) * (kThreads / group_of(E)) * E * 4 : 0;
-  return launch(kernel_of<kBack>(logits_dtype, E), dim3((M + a.chunk - 1) / a.chunk), kThreads, lds, a, stream);
+  const size_t lds = grad_w ? (size_t)back_rows(G) * (kThreads / G) * E * 4 : 0;
+  return launch(kernel_of<kBack>(logits_dtype, E, G), dim3((M + a.chunk - 1) / a.chunk), kThreads, lds, a, stream);
 }

@@ -62,6 +62,9 @@ SHAPES = [  # M, E, k, B, masked, dtype
     (777, 897, 16, 3, 0.2, "f32"), (300, 1030, 3, 7, 0, "f32"), (64, 4096, 64, 5, 0.5, "f32"),
     (130, 4095, 16, 2, 0, "bf16"), (9000, 96, 6, 300, 0.1, "bf16"), (20, 16, 2, 60, 0.4, "f32"),
     (2048, 640, 8, 1, 0.9, "bf16"), (700, 3000, 8, 2, 0, "f32"), (41, 500, 4, 1, 0, "f32"), (50, 1600, 4, 3, 0, "bf16"),
+    # sixteen lanes a row (one to four column groups, whole and cut) and more picks than lanes
+    (333, 61, 7, 5, 0.2, "bf16"), (1500, 128, 8, 1, 0, "bf16"), (700, 190, 16, 40, 0.1, "f32"), (260, 256, 2, 2, 0, "f32"),
+    (90, 100, 17, 3, 0.1, "f32"), (50, 64, 64, 1, 0, "bf16"), (77, 256, 33, 2, 0.3, "bf16"), (5000, 3, 2, 7, 0.1, "bf16"),
 ]
 
 
@@ -113,7 +116,7 @@ def test_backward_terms(grad_w, balance, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("E", [48, 129, 896])
+@pytest.mark.parametrize("E", [48, 129, 300, 896, 1500])
 def test_extreme_rows(E, dtype):
     """Rows of the type's lowest value, infinities, far-off rows whose scores
     underflow, and NaN or infinities in masked rows."""
