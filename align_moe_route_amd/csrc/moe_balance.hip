@@ -810,6 +810,9 @@ bool valid_sizes(int M, int E, int k, int B) {
   return M >= 0 && E >= 1 && E <= 4096 && k >= 1 && k <= 64 && B >= 1 && B <= 65535;
 }
 
+// Token and route numbers, and a chunk past the last token, in 32 bits.
+bool fits(int M, int k) { return M <= (1 << 30) && (int64_t)M * k <= INT32_MAX; }
+
 enum { kPart, kSingle, kBack };
 
 template <int WHAT, int DT, int G, int NI>
@@ -859,7 +862,7 @@ int launch(const void* fn, dim3 grid, int threads, size_t lds, BArgs& a, void* s
 }  // namespace
 
 extern "C" size_t moe_balance_workspace_bytes(int M, int E, int k, int B) {
-  if (!valid_sizes(M, E, k, B)) return (size_t)-1;
+  if (!valid_sizes(M, E, k, B) || !fits(M, k)) return (size_t)-1;
   return plan_of(M, E, B).total;
 }
 
@@ -870,6 +873,7 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   if (!valid_sizes(M, E, k, B) || (!seq_offsets && B != 1) ||
       (logits_dtype != MRS_DTYPE_F32 && logits_dtype != MRS_DTYPE_BF16))
     return MRS_ERR_INVALID_ARG;
+  if (!fits(M, k)) return MRS_ERR_OVERFLOW;
   if (!loss || !counts || !tokens || !shares) return MRS_ERR_NULL_POINTER;
   if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(shares, 4))
     return MRS_ERR_MISALIGNED;
@@ -925,6 +929,7 @@ extern "C" int moe_router_backward(const void* logits, int logits_dtype, const i
   if (!valid_sizes(M, E, k, B) || (!seq_offsets && B != 1) ||
       (logits_dtype != MRS_DTYPE_F32 && logits_dtype != MRS_DTYPE_BF16))
     return MRS_ERR_INVALID_ARG;
+  if (!fits(M, k)) return MRS_ERR_OVERFLOW;
   if (M == 0) return MRS_OK;
   if (!logits || !ids || !grad_logits || (counts && !tokens)) return MRS_ERR_NULL_POINTER;
   const int size = logits_dtype == MRS_DTYPE_F32 ? 4 : 2;

@@ -39,7 +39,8 @@ size_t moe_balance_workspace_bytes(int M, int E, int k, int B);
  *                nondecreasing from 0 to M (read on the device; other values
  *                are clamped to [0, M] and give unspecified results)
  *   mask         NULL (every token counts) or uint8[M]
- *   M >= 0, 1 <= E <= 4096, 1 <= k <= 64, 1 <= B <= 65535
+ *   0 <= M <= 2^30, 1 <= E <= 4096, 1 <= k <= 64, M k < 2^31, 1 <= B <= 65535
+ *                (MRS_ERR_OVERFLOW for more tokens or routes)
  *   loss float[1], counts int32[B, E], tokens int32[B + 1], shares float[B, E] (written)
  *   workspace    device scratch of moe_balance_workspace_bytes() bytes, 16-byte
  *                aligned; never cleared between calls; calls that may overlap in

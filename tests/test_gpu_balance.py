@@ -214,3 +214,23 @@ def test_replayed_from_a_graph():
         wgrad = amr.router_backward(gx, gi, grad_weights=gw, balance=want, coef=0.1, seq_offsets=go, mask=gm)
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want)) and torch.equal(grad, wgrad)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens' gradients, and the shares of a constant matrix."""
+    M, E, k = 600000, 4096, 2
+    x = torch.zeros(M, E, dtype=torch.bfloat16, device="cuda")
+    ids = torch.randint(0, E, (M, k), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0))
+    out = amr.balance_loss(x, ids, 1.0)
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    assert torch.equal(out.counts[0].long(), counts) and out.tokens.tolist() == [M, 1]
+    # equal shares; the chunks' sums add up to 2400 equal terms in FP32
+    assert bool(((out.shares * E - 1).abs() <= 2600 * ob.U).all())
+    assert abs(out.loss.item() - 1.0) <= 2700 * ob.U
+    x[-5:] = torch.randn(5, E, device="cuda").bfloat16()
+    gw = torch.randn(M, k, device="cuda")
+    got = amr.router_backward(x, ids, grad_weights=gw)
+    x64, i5 = x[-5:].double().cpu().numpy(), ids[-5:].cpu().numpy()
+    ref, size = ob.backward(x64, i5, 1.0, 1.0, gw[-5:].cpu().numpy())
+    err = ob.grad_bound(np.abs(x64).max(), E) * size + ob.FLUSH
+    assert (np.abs(got[-5:].double().cpu().numpy() - ref) <= err + 2.0 ** -8 * (np.abs(ref) + err)).all()

@@ -245,3 +245,32 @@ def test_quantize_and_product_replayed_from_a_graph():
         want = amr.grouped_gemm_mxfp4(amr.mxfp4_quantize(x), *args, out=torch.zeros_like(y))
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """Rows and weights whose byte offsets pass 2^32: the last rows, the last experts."""
+    K, rows = 65536, 70000
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, K, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").bfloat16()
+    q = amr.mxfp4_quantize(x)
+    codes, scales, _ = om.quantize(x[-3:].double().cpu().numpy())
+    assert np.array_equal(q.codes[-3:].cpu().numpy(), codes) and np.array_equal(q.scales[-3:].cpu().numpy(), scales)
+    assert not bool(q.codes[:-3].any())
+    del x, q
+    E, N, K, M, k = 3000, 256, 16384, 40, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    wc = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    ws = torch.randint(124, 131, (E, N, K // 32), dtype=torch.uint8, device="cuda", generator=g)
+    rng = np.random.default_rng(2)
+    xc, xs = random_rows(rng, (M,), K)
+    for block in (16, 64):  # the few-rows and the tile kernel
+        ids = np.stack([np.sort(rng.choice(np.arange(E - (20 if block == 16 else 4), E), k, replace=False))
+                        for _ in range(M)]).astype(np.int32)
+        out = amr.sort_from_ids(torch.from_numpy(ids).cuda(), E, block)
+        y = amr.grouped_gemm_mxfp4(amr.MXFP4(*to_gpu(xc, xs)), amr.MXFP4(wc, ws), out.sorted_ids, out.expert_of_block,
+                                   out.num_post_pad, k, block, out_dtype=torch.float32)
+        npp = int(out.num_post_pad.item())
+        lo = E - 20
+        ref, ab = om.product(xc, xs, wc[lo:].cpu().numpy(), ws[lo:].cpu().numpy(), out.sorted_ids.cpu().numpy(),
+                             out.expert_of_block.cpu().numpy() - lo, npp, M, k, block)
+        assert (np.abs(y[:npp].double().cpu().numpy() - ref) <= om.tolerance(ref, ab, K, False)).all()

@@ -46,7 +46,8 @@ def balance(logits=P, dt=0, ids=P, off=None, mask=None, M=4, E=8, k=2, B=1, loss
 
 SIZES = [(dict(M=-1), -1), (dict(E=0), -1), (dict(E=4097), -1), (dict(k=0), -1), (dict(k=65), -1), (dict(B=0), -1),
          (dict(B=2), -1), (dict(B=65536, off=P), -1), (dict(dt=2), -1), (dict(logits=None), -2), (dict(ids=None), -2),
-         (dict(logits=P + 2), -3), (dict(logits=P + 1, dt=1), -3), (dict(ids=P + 2), -3), (dict(off=P + 2), -3)]
+         (dict(logits=P + 2), -3), (dict(logits=P + 1, dt=1), -3), (dict(ids=P + 2), -3), (dict(off=P + 2), -3),
+         (dict(M=(1 << 30) + 1, k=1), -5), (dict(M=1 << 28, k=8), -5)]
 
 
 @pytest.mark.parametrize("kw,code", SIZES + [
