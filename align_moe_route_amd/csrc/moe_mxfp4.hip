@@ -161,17 +161,17 @@ struct PArgs {
   int M, k, E, K, N, block, sorted;
   int row_limit;  // rows the metadata can hold: (max_rows / block) * block
   int nrt, ntn;   // row tiles, column tiles
+  int run;        // consecutive row tiles of an XCD
 };
 
-// Workgroup h goes to XCD h mod 8; runs of kRunRows consecutive row tiles go to
-// the XCDs in turn, the column tiles of a row tile one after another, so an
-// expert's row tiles read its weights, and a row tile's column tiles its rows,
-// from one L2 at about the same time.
+// Workgroup h goes to XCD h mod 8; runs of `run` consecutive row tiles go to the
+// XCDs in turn, the column tiles of a row tile one after another, so an expert's
+// row tiles read its weights, and a row tile's column tiles its rows, from one L2
+// at about the same time.
 constexpr int kXcds = 8;
-constexpr int kRunRows = 8;
-__device__ __forceinline__ void tile_of(int h, int ntn, int& rt, int& ct) {
+__device__ __forceinline__ void tile_of(int h, int run, int ntn, int& rt, int& ct) {
   const int x = h % kXcds, j = h / kXcds, i = j / ntn;
-  rt = (i / kRunRows * kXcds + x) * kRunRows + i % kRunRows;
+  rt = (i / run * kXcds + x) * run + i % run;
   ct = j % ntn;
 }
 
@@ -540,7 +540,7 @@ template <typename Y, int BM>
 __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   __shared__ Tile<BM> l;
   int rt, ct;
-  tile_of((int)blockIdx.x, a.ntn, rt, ct);
+  tile_of((int)blockIdx.x, a.run, a.ntn, rt, ct);
   if (rt >= a.nrt) return;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int r0 = rt * BM, n0 = ct * kCols;
@@ -609,16 +609,24 @@ const void* product_kernel(int bm, int bn) {
 // 128, 4 / 64 / 192 rows an expert: tiles of 128 99 / 111 / 149 us, of 64 107 / 129 /
 // 203, of 32 159 / 189 / 307), smaller ones where 128 workgroups would not come
 // together (8 experts, 512 tokens: tiles of 32 8.2 us, 64 10.2, 128 14.1).
+//
+// Runs of row tiles: eight or more for each XCD, so that none has much more than
+// another (us with runs of 8 / with this rule: 2048 tokens, 64 experts, top-8 45.5 /
+// 34.0; 8192 tokens, 8 experts, top-2, blocks of 256 53.6 / 47.9), powers of two up
+// to 16 (8192 tokens, 896 experts: 428, runs of 23 446).
 struct Shape {
-  int bm, bn;
+  int bm, bn, run;
 };
 Shape shape_of(int64_t routes, int64_t used, int N, int block) {
   const int64_t cols = (N + kCols - 1) / kCols, strips = used * cols;
   if (strips < 192 && strips * routes <= 768 * used)
-    return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32};
+    return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32, 1};
   int bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
   while (strips < 192 && bm > 32 && routes / bm * cols < 128) bm /= 2;
-  return {bm, kCols};
+  const int64_t tiles = routes / bm + used / 2;  // an expert's last tile is half full
+  int run = 1;
+  while (run < 16 && run * 128 <= tiles) run *= 2;
+  return {bm, kCols, run};
 }
 
 }  // namespace
@@ -674,11 +682,11 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
     const int64_t pairs = row_limit / block * ntn;
     grid = (pairs + kXcds * kPairs - 1) / (kXcds * kPairs) * (kXcds * kPairs) * (block / 16);
   } else {
-    grid = (nrt + kXcds * kRunRows - 1) / (kXcds * kRunRows) * kRunRows * kXcds * ntn;
+    grid = (nrt + kXcds * shape.run - 1) / (kXcds * shape.run) * shape.run * kXcds * ntn;
   }
   if (grid > INT32_MAX) return MRS_ERR_OVERFLOW;
   PArgs a{x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, y,
-          M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn};
+          M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn, shape.run};
   const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm, bn) : product_kernel<float>(bm, bn);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), params, 0,
