@@ -352,6 +352,10 @@ __device__ __forceinline__ void stage_scales(Scale8* dst, int left, F src) {
 // Rows that a tile of BM multiplies: one of 16 fills half an operand, the other
 // half repeats row 0 of x and is not stored.
 constexpr int tile_rows(int BM) { return BM < 32 ? 32 : BM; }
+// Steps in flight while one is multiplied: two where the registers allow it (2048
+// tokens, 256 experts, top-8, K = 3584, N = 768, blocks of 64: 109 us with one, 98
+// with two; 512 tokens in blocks of 128 of the same, tiles of 128 rows: two spill).
+constexpr int deep_of(int BM) { return BM < 128 ? 2 : 1; }
 
 template <int BM>
 struct Tile {
@@ -385,7 +389,8 @@ __device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F7
 // of the tile that have one
 template <typename Y, int BM>
 __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const uint64_t (&has)[2], int live,
-                                          const Weights& w, WeightRegs& wr, Tile<BM>& l) {
+                                          const Weights& w, WeightRegs (&wr)[deep_of(BM)], Tile<BM>& l) {
+  constexpr int kDeep = deep_of(BM);
   constexpr int TR = tile_rows(BM), FM = TR / 32;
   constexpr int XP = TR * 8 / kTileThreads;  // x chunks a thread stages in a step
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -403,16 +408,18 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
   const uint8_t* xsrc[XP];
 #pragma unroll
   for (int p = 0; p < XP; ++p) xsrc[p] = a.xc + (size_t)l.row[(tid + p * kTileThreads) / 8] * kb;
-  u32x4 xr[XP];
-  auto load_x = [&](int t) {
+  typedef u32x4 RowRegs[XP];
+  RowRegs xr[kDeep];
+  auto load = [&](RowRegs& x, WeightRegs& q, int t) {
+    w.load(q, at(t));
 #pragma unroll
-    for (int p = 0; p < XP; ++p) xr[p] = *reinterpret_cast<const u32x4*>(xsrc[p] + at(t));
+    for (int p = 0; p < XP; ++p) x[p] = *reinterpret_cast<const u32x4*>(xsrc[p] + at(t));
   };
-  auto store = [&]() {
+  auto store = [&](const RowRegs& x, const WeightRegs& q) {
 #pragma unroll
-    for (int p = 0; p < XP; ++p) l.x[swz((tid + p * kTileThreads) / 8, tid % 8)] = xr[p];
+    for (int p = 0; p < XP; ++p) l.x[swz((tid + p * kTileThreads) / 8, tid % 8)] = x[p];
 #pragma unroll
-    for (int p = 0; p < kWP; ++p) l.w[swz(wv * kFN * 32 + lane / 8 + p * 8, tid % 8)] = wr[p];
+    for (int p = 0; p < kWP; ++p) l.w[swz(wv * kFN * 32 + lane / 8 + p * 8, tid % 8)] = q[p];
   };
   auto load_scales = [&](int t, bool weights) {
     // opaque, or the addresses of the runs after the first are made ahead of the
@@ -425,9 +432,11 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
       stage_scales<kCols>(l.sw, left, [&](int r) { return w.scales + (size_t)min(r, w.last) * kv + t * 8; });
   };
 
-  load_x(0);
+#pragma unroll
+  for (int p = 0; p < XP; ++p) xr[0][p] = *reinterpret_cast<const u32x4*>(xsrc[p] + at(0));
   load_scales(0, false);
-  store();
+  if constexpr (kDeep == 2) load(xr[1], wr[1], min(1, steps - 1));
+  store(xr[0], wr[0]);
   wait_memory();  // the scales are in LDS
   __syncthreads();
   __builtin_amdgcn_sched_barrier(0);
@@ -437,16 +446,16 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
 #pragma unroll
     for (int j = 0; j < kFN; ++j) acc[i][j] = f32x16{};
 
-  for (int t = 0; t < steps; ++t) {
-    const int next = min(t + 1, steps - 1);
+  // step t, whose operands are in LDS: those of step t + kDeep go into the
+  // registers that step t's have left
+  auto step = [&](int t, RowRegs& x, WeightRegs& q) {
     if (t > 0 && t % kScaleSteps == 0) {  // past the last step's barrier
       load_scales(t, true);
       wait_memory();
       __syncthreads();
     }
     const uint32_t keep = half && t == steps - 1 ? 0u : ~0u;
-    w.load(wr, at(next));
-    load_x(next);
+    load(x, q, min(t + kDeep, steps - 1));
     // scale of columns 64 g + 32 lh ..: byte 2 (g mod 2) of the word g / 2 shifted by 8 lh
     Scale8 we[kFN];
 #pragma unroll
@@ -484,8 +493,18 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
       }
     }
     __syncthreads();
-    store();
+  };
+  for (int t = 0;;) {
+    step(t, xr[0], wr[0]);
+    if (++t == steps) break;
+    store(xr[kDeep - 1], wr[kDeep - 1]);
     __syncthreads();
+    if constexpr (kDeep == 2) {
+      step(t, xr[1], wr[1]);
+      if (++t == steps) break;
+      store(xr[0], wr[0]);
+      __syncthreads();
+    }
   }
 
   // Result register v of lane l: row 8 (v / 4) + 4 (l / 32) + v mod 4, column
@@ -566,8 +585,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
   const Weights w{a.wc + ((size_t)e * a.N + n0) * kb, a.ws + ((size_t)e * a.N + n0) * ks,
                   wv * kFN * 32 + lane / 8, a.N - 1 - n0, (uint32_t)kb};
-  WeightRegs wr;
-  w.load(wr, tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0));
+  WeightRegs wr[deep_of(BM)];
+  w.load(wr[0], tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0));
   stage_scales<kCols>(l.sw, (int)ks / 4, [&](int r) { return w.scales + (size_t)min(r, w.last) * ks; });
   if (tid < l.kRows) {  // the first two waves, lane tid mod 64
     const bool mine = ok[wv & 1];
