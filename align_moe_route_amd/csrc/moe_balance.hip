@@ -13,8 +13,8 @@
 // rounding.
 //
 // Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s):
-// forward 16384 x 4096 FP32, 37 sequences, in 66 us (276 MB, 4.2 TB/s; the pieces
-// add 37 MB and two small launches 16 us), 65536 x 512 FP32 in 31 us; backward 118
+// forward 16384 x 4096 FP32, 37 sequences, in 61 us (276 MB, 4.5 TB/s; the pieces
+// add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 31 us; backward 118
 // and 55 us (541 and 273 MB, 4.6 and 5.0 TB/s).  8192 x 896 BF16 takes 15.5 us
 // forward, 8 of them the second launch's chain of round trips, and 13 us backward
 // (30 MB; 6 us of arithmetic, the rest latency); 131072 x 128 BF16 20 and 24 us.
@@ -416,8 +416,6 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
   }
 }
 
-constexpr int kTile = 32;  // experts a workgroup of the second kernel adds up, a half wave to a piece
-
 // The tiles' parts of the loss, in their order, by one workgroup.
 __device__ __forceinline__ void finish(const BArgs& a, int tiles, double* sh, int* nn) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, waves = blockDim.x / 64;
@@ -446,17 +444,21 @@ __device__ __forceinline__ void finish(const BArgs& a, int tiles, double* sh, in
   }
 }
 
-// A half wave adds every (half waves)-th piece, eight at a time in flight.
-// TICKET: the workgroup that finishes last adds up the loss, else a third
-// launch does.
-template <bool TICKET>
-__global__ __launch_bounds__(1024) void k_balance_sum(BArgs a) {
-  __shared__ double sh[32][kTile + 1];
-  __shared__ int ct[32][kTile + 1], nn[16];
+// A workgroup adds up 2^lcols experts of a sequence, 2^lwalkers threads to an
+// expert, each every (walkers)-th piece, eight at a time in flight.  TICKET: the
+// workgroup that finishes last adds up the loss, else a third launch does.  LONG:
+// 32 walkers and 32 experts, known to the compiler (8192 x 896 forward 15.5 us, as
+// arguments 16.0).
+template <bool TICKET, bool LONG>
+__global__ __launch_bounds__(1024) void k_balance_sum(BArgs a, int lcols, int lwalkers) {
+  if constexpr (LONG) lcols = lwalkers = 5;
+  __shared__ double sh[1024 + 32];
+  __shared__ int ct[1024 + 32], nn[16];
   __shared__ bool last;
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int halves = blockDim.x / 32, half = tid / 32, l = tid % 32, tiles = gridDim.x, b = blockIdx.y;
-  const int e = blockIdx.x * kTile + l, ec = min(e, a.E - 1);
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x / 64;
+  const int cols = 1 << lcols, walkers = 1 << lwalkers, walker = tid >> lcols, l = tid & (cols - 1);
+  const int tiles = gridDim.x, b = blockIdx.y;
+  const int ec = min((int)blockIdx.x * cols + l, a.E - 1);
   const int t0 = offset_of(a, b), t1 = b == a.B - 1 ? a.M : offset_of(a, b + 1);
   int first = 0, end = 0;
   if (t1 > t0) {
@@ -466,63 +468,61 @@ __global__ __launch_bounds__(1024) void k_balance_sum(BArgs a) {
   double s = 0.0;
   int count = 0, n = 0;
   for (int p = first + tid; p < end; p += blockDim.x) n += a.ws_n[p];
-  for (int p0 = first + half; p0 < end; p0 += 8 * halves) {
+  for (int p0 = first + walker; p0 < end; p0 += 8 * walkers) {
     float f[8];
     int i[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const size_t at = (size_t)min(p0 + u * halves, end - 1) * a.E + ec;
+      const size_t at = (size_t)min(p0 + u * walkers, end - 1) * a.E + ec;
       f[u] = a.ws_share[at];
       i[u] = a.ws_count[at];
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (p0 + u * halves < end) {
+      if (p0 + u * walkers < end) {
         s += (double)f[u];
         count += i[u];
       }
   }
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m, 64);
-  sh[half][l] = s;
-  ct[half][l] = count;
+  sh[walker * (cols + 1) + l] = s;
+  ct[walker * (cols + 1) + l] = count;
   if (lane == 0) nn[wv] = n;
   __syncthreads();
-  // the halves of a column lie side by side now, for a butterfly
-  const int h = tid % halves, col = tid / halves, ecol = blockIdx.x * kTile + col;
-  s = sh[h][col];
-  count = ct[h][col];
-  for (int m = halves / 2; m >= 1; m >>= 1) {
+  // the walkers of a column lie side by side now, for a butterfly
+  const int h = tid & (walkers - 1), col = tid >> lwalkers, ecol = blockIdx.x * cols + col;
+  s = sh[h * (cols + 1) + col];
+  count = ct[h * (cols + 1) + col];
+  for (int m = walkers / 2; m >= 1; m >>= 1) {
     s += __shfl_xor(s, m, 64);
     count += __shfl_xor(count, m, 64);
   }
   n = nn[0];
-  for (int w = 1; w < halves / 2; ++w) n += nn[w];
+  for (int w = 1; w < waves; ++w) n += nn[w];
   const double share = n > 0 ? s / n : 0.0;
-  if (h == 0 && ecol < a.E) {
+  const bool mine = h == 0 && ecol < a.E;
+  if (mine) {
     a.counts[(size_t)b * a.E + ecol] = count;
     a.shares[(size_t)b * a.E + ecol] = (float)share;
   }
+  double part = wave_sum(mine && n > 0 ? (double)count * share / n : 0.0);
   __syncthreads();
-  if (h == 0) sh[0][col] = ecol < a.E && n > 0 ? (double)count * share / n : 0.0;
+  if (lane == 0) sh[wv] = part;
   __syncthreads();
-  if (tid < 32) {
-    double part = sh[0][tid];
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) part += __shfl_xor(part, m, 32);
-    if (tid == 0) {
-      a.ws_loss[(size_t)b * tiles + blockIdx.x] = part;
-      if (blockIdx.x == 0) a.tokens[b] = n;
-      if constexpr (TICKET) {
-        __threadfence();
-        last = atomicAdd(a.ws_ticket, 1u) == (uint32_t)tiles * (uint32_t)a.B - 1u;
-        __threadfence();
-      }
+  if (tid == 0) {
+    for (int w = 1; w < waves; ++w) part += sh[w];
+    a.ws_loss[(size_t)b * tiles + blockIdx.x] = part;
+    if (blockIdx.x == 0) a.tokens[b] = n;
+    if constexpr (TICKET) {
+      __threadfence();
+      last = atomicAdd(a.ws_ticket, 1u) == (uint32_t)tiles * (uint32_t)a.B - 1u;
+      __threadfence();
     }
   }
   if constexpr (TICKET) {
     __syncthreads();
-    if (last) finish(a, tiles, &sh[0][0], nn);
+    if (last) finish(a, tiles, sh, nn);
   }
 }
 
@@ -772,7 +772,10 @@ int columns_of(int E, int G) { return (E + 4 * G - 1) / (4 * G); }
 
 constexpr int kSingleBatches = 4;  // batches that one workgroup does alone
 constexpr int kSingleB = 64;
-constexpr int kTicketMax = 64;  // workgroups of the second kernel that may share a counter (40 ns each)
+// Workgroups of the second kernel that may share a counter, 40 ns each, in place of
+// a third launch (65536 x 64, 64 sequences: with 64 of them 18.9 us, with the launch
+// 17.8; 65536 x 128, 16 sequences, 32 of them: 17.2 and 18.2).
+constexpr int kTicketMax = 32;
 
 // Tokens of a workgroup when `grid` of them run at once.
 int chunk_of(int M, int batch, int grid) {
@@ -781,7 +784,7 @@ int chunk_of(int M, int batch, int grid) {
 }
 
 struct Plan {
-  int chunk, chunks, tiles, waves;
+  int chunk, chunks, lcols, lwalkers, tiles;
   bool single;
   size_t share, count, n, loss, ticket, total;
 };
@@ -793,9 +796,24 @@ Plan plan_of(int M, int E, int B) {
   // a workgroup for each compute unit: eight waves, or twice four
   p.chunk = p.single ? alone : chunk_of(M, batch, G < 256 ? 256 : 512);
   p.chunks = (M + p.chunk - 1) / p.chunk;
-  p.tiles = (E + kTile - 1) / kTile;
-  // waves of the second kernel: sixteen for long sequences, four for many short ones
-  p.waves = p.chunks / B >= 64 ? 16 : 4;
+  const int pieces = p.chunks / B;  // of a sequence
+  // Threads of the second kernel: 32 walkers of 32 experts for long sequences (1024
+  // threads), else 256 threads, 8 walkers or 4 when each of eight would get less than
+  // four pieces of an average sequence (us, 8 / 4 walkers: 16384 x 4096, 37 equal
+  // sequences 67 / 61; 8192 x 896, 128 of them 26.7 / 23.2, and where one of these has
+  // 90 % of the tokens 32.1 / 30.5).  2 walkers only shorten a launch of many
+  // workgroups, one sequence's chain of pieces takes the longer (4 / 2 walkers: 16384
+  // x 4096, 200 sequences 84 / 72, with one of 95 % 95 / 91; the 8192 x 896 above 23.2
+  // / 22.0 and 30.5 / 33.5).
+  p.lcols = 5;
+  p.lwalkers = pieces >= 64 ? 5 : 3;
+  p.tiles = (E + 31) / 32;
+  while (p.lwalkers < 5 && p.lwalkers > 1 && (1 << p.lcols) < E && pieces < 4 << p.lwalkers &&
+         (p.lwalkers > 2 || (int64_t)p.tiles * B > 4096)) {
+    ++p.lcols;
+    --p.lwalkers;
+    p.tiles = (E + (1 << p.lcols) - 1) >> p.lcols;
+  }
   const size_t all = (size_t)p.chunks + B;
   p.share = 0;
   p.count = p.share + align16(all * E * 4);
@@ -852,6 +870,14 @@ const void* kernel_of(int dtype, int E, int G) {
   return dtype == MRS_DTYPE_F32 ? kernel_of<WHAT, MRS_DTYPE_F32>(E, G) : kernel_of<WHAT, MRS_DTYPE_BF16>(E, G);
 }
 
+const void* sum_kernel(bool ticket, bool many) {
+  if (ticket)
+    return many ? reinterpret_cast<const void*>(k_balance_sum<true, true>)
+                : reinterpret_cast<const void*>(k_balance_sum<true, false>);
+  return many ? reinterpret_cast<const void*>(k_balance_sum<false, true>)
+              : reinterpret_cast<const void*>(k_balance_sum<false, false>);
+}
+
 int launch(const void* fn, dim3 grid, int threads, size_t lds, BArgs& a, void* stream) {
   void* params[] = {&a};
   return hipLaunchKernel(fn, grid, dim3(threads), params, lds, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
@@ -877,7 +903,7 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   if (!loss || !counts || !tokens || !shares) return MRS_ERR_NULL_POINTER;
   if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(shares, 4))
     return MRS_ERR_MISALIGNED;
-  const Plan p = plan_of(M, E, B);
+  Plan p = plan_of(M, E, B);
   BArgs a{};
   a.logits = logits;
   a.ids = ids;
@@ -910,10 +936,12 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, const int3
   if (p.single) return launch(kernel_of<kSingle>(logits_dtype, E, G), dim3(1), threads, lds, a, stream);
   int rc = launch(kernel_of<kPart>(logits_dtype, E, G), dim3(p.chunks), threads, lds, a, stream);
   if (rc != MRS_OK) return rc;
-  if ((int64_t)p.tiles * B <= kTicketMax)
-    return launch(reinterpret_cast<const void*>(k_balance_sum<true>), dim3(p.tiles, B), p.waves * 64, 0, a, stream);
-  rc = launch(reinterpret_cast<const void*>(k_balance_sum<false>), dim3(p.tiles, B), p.waves * 64, 0, a, stream);
-  if (rc != MRS_OK) return rc;
+  const bool ticket = (int64_t)p.tiles * B <= kTicketMax;
+  void* sum_params[] = {&a, &p.lcols, &p.lwalkers};
+  if (hipLaunchKernel(sum_kernel(ticket, p.lwalkers == 5), dim3(p.tiles, B), dim3(1 << (p.lcols + p.lwalkers)), sum_params,
+                      0, reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+    return MRS_ERR_LAUNCH;
+  if (ticket) return MRS_OK;
   int tiles = p.tiles;
   void* params[] = {&a, &tiles};
   return hipLaunchKernel(reinterpret_cast<const void*>(k_balance_loss), dim3(1), dim3(1024), params, 0,

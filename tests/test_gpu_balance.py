@@ -65,6 +65,8 @@ SHAPES = [  # M, E, k, B, masked, dtype
     # sixteen lanes a row (one to four column groups, whole and cut) and more picks than lanes
     (333, 61, 7, 5, 0.2, "bf16"), (1500, 128, 8, 1, 0, "bf16"), (700, 190, 16, 40, 0.1, "f32"), (260, 256, 2, 2, 0, "f32"),
     (90, 100, 17, 3, 0.1, "f32"), (50, 64, 64, 1, 0, "bf16"), (77, 256, 33, 2, 0.3, "bf16"), (5000, 3, 2, 7, 0.1, "bf16"),
+    # many short sequences of a wide router: two walkers a column in the second kernel
+    (2000, 4000, 4, 70, 0.1, "bf16"),
 ]
 
 
