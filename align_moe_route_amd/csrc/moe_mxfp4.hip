@@ -162,6 +162,7 @@ struct PArgs {
   int row_limit;  // rows the metadata can hold: (max_rows / block) * block
   int nrt, ntn;   // row tiles, column tiles
   int run;        // consecutive row tiles of an XCD
+  bool large;     // the weights are larger than the 256 MB cache in front of the memory
 };
 
 // Workgroup h goes to XCD h mod 8; runs of `run` consecutive row tiles go to the
@@ -310,10 +311,10 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
 // present one is multiplied.  Reading the weights straight into operand
 // registers, every lane another row, kept the address unit busy 87 % of the time
 // and bounded the kernel.  8192 tokens, 896 experts, top-16, K = 3584, N = 768 in
-// 450 us: 1.5 GB that must move at 3.4 TB/s; with the experts' rows read again
-// from the L2's misses and y written, 2.0 GB at 4.5 TB/s (a 2 GiB copy: 4.9), which
+// 435 us: 1.6 GB that must move at 3.7 TB/s; with the experts' rows read again
+// from the L2's misses and y written, 2.2 GB at 5.0 TB/s (a 2 GiB copy: 4.9), which
 // bounds it now (without the multiplications it takes 410 us).  64 tokens of the
-// same experts in blocks of 16: 901 MB of weights in 177 us, 5.1 TB/s.
+// same experts in blocks of 16: 901 MB of weights in 165 us, 5.5 TB/s.
 constexpr int kFN = 2, kNW = 4;  // 32-column operands a wave, waves
 constexpr int kCols = kNW * kFN * 32, kTileThreads = kNW * 64;
 
@@ -357,6 +358,11 @@ constexpr int tile_rows(int BM) { return BM < 32 ? 32 : BM; }
 // with two; 512 tokens in blocks of 128 of the same, tiles of 128 rows: two spill).
 constexpr int deep_of(int BM) { return BM < 128 ? 2 : 1; }
 
+// Whether weights that one row tile alone reads are loaded past the L2 (another
+// copy of the loop, which tiles of 64 rows and more have no registers for).
+template <int BM>
+constexpr bool kOnce = BM <= 32;
+
 template <int BM>
 struct Tile {
   static constexpr int kRows = tile_rows(BM);
@@ -373,12 +379,19 @@ struct Weights {
   const uint8_t *codes, *scales;  // of the tile's first column
   int row, last;                  // this lane's first row, the last row that exists
   uint32_t kb;                    // bytes of a row
-  __device__ __forceinline__ void load(WeightRegs& q, int o) const {  // o: byte of the row
+  // o: byte of the row.  ONCE: no other row tile reads these weights, and the L2 need
+  // not keep them (896 experts, blocks of 16: 64 tokens 168 -> 158 us, 512 tokens 251 ->
+  // 241; so loaded where row tiles share them, 2048 tokens and 256 experts 176 -> 220; nor
+  // where all experts' fit the cache in front of the memory, which may have them from
+  // the call before: 50 MB 13.6 -> 14.7).
+  template <bool ONCE>
+  __device__ __forceinline__ void load(WeightRegs& q, int o) const {
 #pragma unroll
     for (int p = 0; p < kWP; ++p) {
       int r = row + p * 8;
       asm volatile("" : "+v"(r));  // opaque: eight row addresses kept over the loop spill
-      q[p] = *reinterpret_cast<const u32x4*>(codes + ((uint32_t)min(r, last) * kb + (uint32_t)o));
+      const u32x4* at = reinterpret_cast<const u32x4*>(codes + ((uint32_t)min(r, last) * kb + (uint32_t)o));
+      q[p] = ONCE ? __builtin_nontemporal_load(at) : *at;
     }
   }
 };
@@ -387,7 +400,7 @@ __device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F7
 
 // `has`: a bit for each row that holds a route; `live`: the leading 32-row parts
 // of the tile that have one
-template <typename Y, int BM>
+template <typename Y, int BM, bool ONCE>
 __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const uint64_t (&has)[2], int live,
                                           const Weights& w, WeightRegs (&wr)[deep_of(BM)], Tile<BM>& l) {
   constexpr int kDeep = deep_of(BM);
@@ -411,7 +424,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
   typedef u32x4 RowRegs[XP];
   RowRegs xr[kDeep];
   auto load = [&](RowRegs& x, WeightRegs& q, int t) {
-    w.load(q, at(t));
+    w.template load<ONCE>(q, at(t));
 #pragma unroll
     for (int p = 0; p < XP; ++p) x[p] = *reinterpret_cast<const u32x4*>(xsrc[p] + at(t));
   };
@@ -536,7 +549,10 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
         const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
         const int n = n1 + c * (16 / (int)sizeof(Y));
         const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
-        if (n < a.N && (BM >= 32 || r < BM)) *reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n) = o;
+                // not kept in the L2, which the rows and weights need (8192 tokens, 896 experts:
+        // 447 -> 435 us; 64 tokens, 256 experts, blocks of 128: 93.5 -> 87)
+        if (n < a.N && (BM >= 32 || r < BM))
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n));
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     } else {
@@ -564,7 +580,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int r0 = rt * BM, n0 = ct * kCols;
   const int npp = min(*a.npp, a.row_limit);
-  const int e = __builtin_amdgcn_readfirstlane(a.eob[r0 / a.block]);
+  const int blk = r0 / a.block, e = __builtin_amdgcn_readfirstlane(a.eob[blk]);
+  // the only row tile of its expert?  A block of several tiles counts as shared.
+  int before = e, after = e;
+  if constexpr (kOnce<BM>) {
+    before = blk > 0 ? a.eob[blk - 1] : -1;
+    after = r0 + a.block < a.row_limit ? a.eob[blk + 1] : -1;
+  }
   int s[2];  // slots of rows lane and 64 + lane, in every wave
 #pragma unroll
   for (int i = 0; i < 2; ++i) s[i] = i * 64 + lane < BM ? a.sid[r0 + i * 64 + lane] : -1;
@@ -586,7 +608,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   const Weights w{a.wc + ((size_t)e * a.N + n0) * kb, a.ws + ((size_t)e * a.N + n0) * ks,
                   wv * kFN * 32 + lane / 8, a.N - 1 - n0, (uint32_t)kb};
   WeightRegs wr[deep_of(BM)];
-  w.load(wr[0], tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0));
+  const bool once = kOnce<BM> && a.large && BM == a.block && before != e && (r0 + BM >= npp || after != e);
+  const int o0 = tid % 8 * 16 - (a.K == 128 && tid % 8 >= 4 ? 64 : 0);
+  if (once) w.template load<kOnce<BM>>(wr[0], o0);
+  else w.template load<false>(wr[0], o0);
   stage_scales<kCols>(l.sw, (int)ks / 4, [&](int r) { return w.scales + (size_t)min(r, w.last) * ks; });
   if (tid < l.kRows) {  // the first two waves, lane tid mod 64
     const bool mine = ok[wv & 1];
@@ -599,7 +624,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
   // opaque: knowing that the first part is live the compiler merges its block
   // with the step's loads and spills inside the loop (1.5 ms in place of 0.45)
   asm volatile("" : "+s"(live));
-  tile_body<Y, BM>(a, r0, n0, has, live, w, wr, l);
+  if (once) tile_body<Y, BM, kOnce<BM>>(a, r0, n0, has, live, w, wr, l);
+  else tile_body<Y, BM, false>(a, r0, n0, has, live, w, wr, l);
 }
 
 template <typename Y>
@@ -705,7 +731,8 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
   }
   if (grid > INT32_MAX) return MRS_ERR_OVERFLOW;
   PArgs a{x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, y,
-          M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn, shape.run};
+          M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn, shape.run,
+          (int64_t)E * N * K / 2 > 256 << 20};
   const void* fn = y_dtype == MRS_DTYPE_BF16 ? product_kernel<uint16_t>(bm, bn) : product_kernel<float>(bm, bn);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), params, 0,

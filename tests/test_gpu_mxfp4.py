@@ -274,3 +274,33 @@ def test_offsets_past_32_bits():
         ref, ab = om.product(xc, xs, wc[lo:].cpu().numpy(), ws[lo:].cpu().numpy(), out.sorted_ids.cpu().numpy(),
                              out.expert_of_block.cpu().numpy() - lo, npp, M, k, block)
         assert (np.abs(y[:npp].double().cpu().numpy() - ref) <= om.tolerance(ref, ab, K, False)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 32])
+def test_weights_larger_than_the_caches(block, dtype):
+    """More than 256 MB of weights: an expert's only row tile reads them past the
+    L2, experts with several share them; both, side by side."""
+    E, N, K, M, k, used = 300, 260, 7900, 150, 2, 16
+    print(f"[gpu] mxfp4 product of large weights block={block} {dtype}", flush=True)
+    Kp = (K + 127) // 128 * 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wc = torch.randint(0, 256, (E, N, Kp // 2), dtype=torch.uint8, device="cuda", generator=g)
+    wc[:, :, K // 2:] = 0
+    ws = torch.randint(124, 131, (E, N, Kp // 32), dtype=torch.uint8, device="cuda", generator=g)
+    assert wc.numel() > 256 << 20
+    rng = np.random.default_rng(block)
+    xc, xs = random_rows(rng, (M,), K)
+    p = 0.8 ** np.arange(used)
+    ids = np.stack([np.sort(rng.choice(np.arange(E - used, E), k, replace=False, p=p / p.sum()))
+                    for _ in range(M)]).astype(np.int32)
+    tiles = (np.bincount(ids.ravel(), minlength=E)[-used:] + block - 1) // block
+    assert (tiles == 1).any() and (tiles > 1).any()
+    out = amr.sort_from_ids(torch.from_numpy(ids).cuda(), E, block)
+    y = amr.grouped_gemm_mxfp4(amr.MXFP4(*to_gpu(xc, xs)), amr.MXFP4(wc, ws), out.sorted_ids, out.expert_of_block,
+                               out.num_post_pad, k, block,
+                               out_dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    npp, lo = int(out.num_post_pad.item()), E - used
+    ref, ab = om.product(xc, xs, wc[lo:].cpu().numpy(), ws[lo:].cpu().numpy(), out.sorted_ids.cpu().numpy(),
+                         out.expert_of_block.cpu().numpy() - lo, npp, M, k, block)
+    assert (np.abs(y[:npp].double().cpu().numpy() - ref) <= om.tolerance(ref, ab, K, dtype == "bf16")).all()
