@@ -14,9 +14,9 @@
 //
 // Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s):
 // forward 16384 x 4096 FP32, 37 sequences, in 61 us (276 MB, 4.5 TB/s; the pieces
-// add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 31 us; backward 118
-// and 55 us (541 and 273 MB, 4.6 and 5.0 TB/s).  8192 x 896 BF16 takes 15.5 us
-// forward, 8 of them the second launch's chain of round trips, and 13 us backward
+// add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 31 us; backward 102
+// and 48 us (541 and 273 MB, 5.3 and 5.7 TB/s).  8192 x 896 BF16 takes 15.5 us
+// forward, 8 of them the second launch's chain of round trips, and 11.5 us backward
 // (30 MB; 6 us of arithmetic, the rest latency); 131072 x 128 BF16 20 and 24 us.
 
 #include <hip/hip_runtime.h>
@@ -545,11 +545,6 @@ __global__ __launch_bounds__(256) void k_balance_none(BArgs a) {
   if (threadIdx.x == 0) a.loss[0] = 0.0f;
 }
 
-// Rows of a group in flight in the backward pass: one keeps three workgroups of
-// 896 experts on a compute unit that two do not (8192 x 896: 18 and 26 us); a
-// workgroup's barriers want two (16384 x 4096: 139 and 133 us).
-__host__ __device__ constexpr int back_rows(int G) { return G < 256 ? 1 : 2; }
-
 // The gradient that a row's routing weights give the logit of this lane's pick:
 // xk its logit (-infinity: no pick), gw its weight's gradient.
 template <int S>
@@ -567,72 +562,61 @@ __device__ __forceinline__ float pick_grad(float xk, float gw) {
 
 // d/dx of the balance loss of row t: g_b s' / S * (count[b,e] - sum_e' count[b,e'] p[e']),
 // g_b = grad_loss coef E / (k n_b^2 B'); of the picks' weights:
-// w_j (1 - s_j) (grad_w_j - sum_i grad_w_i w_i), added through a row of LDS.
+// w_j (1 - s_j) (grad_w_j - sum_i grad_w_i w_i), added through a row of LDS.  One
+// row a group is in flight: with two, fewer workgroups fit (16384 x 4096 FP32 109 and
+// 102 us, 8192 x 896 BF16 12.4 and 11.7).
 template <int DT, int G, int NI>
 __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
   typedef typename Row<DT>::T T;
-  constexpr int kGroups = kThreads / G, R = back_rows(G), kSeg = G < 64 ? G : 64;
-  extern __shared__ float picks[];  // [kGroups][R][E], zero between batches
-  __shared__ float box[2][G > 64 ? G / 64 * R : 1], far_box[4];
+  constexpr int kGroups = kThreads / G, kSeg = G < 64 ? G : 64;
+  extern __shared__ float picks[];  // [kGroups][E], zero between rows
+  __shared__ float box[2][G > 64 ? G / 64 : 1], far_box[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = G == 64 ? wv : tid / G, c0 = tid % G * 4;
-  float* extra = picks + (size_t)grp * R * a.E;
+  float* extra = picks + (size_t)grp * a.E;
   const int c = blockIdx.x;
   const int t_end = min(a.M, (c + 1) * a.chunk);
   int t0 = c * a.chunk;
   const float gl = a.grad_loss ? *a.grad_loss : 1.0f;
   const int filled = a.counts ? a.tokens[a.B] : 0;
+  // picks: up to 16 of them, in the first 16 lanes of the group's first wave
+  // (groups of 16 have no more picks); more, in the whole wave
+  const bool few = G == 16 || a.k <= 16;
+  const int j = few ? lane % 16 : lane;
+  const bool picker = j < a.k && (G > 64 ? wv == 0 : true) && (!few || G == 16 || lane < 16);
   bool fresh = true;
   for (int b = sequence_of(a, t0); b < a.B && t0 < t_end; ++b) {
     const int t1 = b == a.B - 1 ? t_end : min(offset_of(a, b + 1), t_end);
     if (t1 <= t0) continue;
-    Four<DT> next[R][NI];
+    Four<DT> next[NI];
     auto fetch = [&](int t) {  // rows past the sequence's last one repeat it
       if (a.counts)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int i = 0; i < NI; ++i)
-            next[r][i] =
-                load4<DT>(static_cast<const T*>(a.logits) + (size_t)min(t + r, t1 - 1) * a.E, c0 + i * G * 4, a.E,
-                                  i < NI - 1);
+        for (int i = 0; i < NI; ++i)
+          next[i] = load4<DT>(static_cast<const T*>(a.logits) + (size_t)min(t, t1 - 1) * a.E, c0 + i * G * 4, a.E,
+                              i < NI - 1);
     };
-    // picks: up to 16 of them, the batch's rows side by side in 16 lanes each of the
-    // group's first wave (groups of 16 have a row and no more picks); more, a row in
-    // each of its first waves (or one after another)
-    const bool few = G == 16 || a.k <= 16;
-    constexpr int kTurns = G > 64 ? 1 : R;
-    const int seg = G == 16 ? 0 : lane / 16;
-    auto row_of = [&](int i) { return few ? seg : G > 64 ? wv : i; };
-    // a batch's ids are two batches ahead, the logits that they name one
-    int id[kTurns], next_id[kTurns];
-    float gw[kTurns], next_gw[kTurns];
-    T xk[kTurns];
+    // a row's ids are two rows ahead, the logits that they name one
+    int id, next_id;
+    float gw, next_gw;
+    T xk;
     auto fetch_ids = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const int r = row_of(i), j = few ? lane % 16 : lane;
-        next_id[i] = -1;
-        next_gw[i] = 0.0f;
-        if (r < R && (!few || (i == 0 && (G <= 64 || wv == 0))) && j < a.k && t + r < t1 &&
-            (!a.mask || a.mask[t + r])) {
-          next_id[i] = a.ids[(size_t)(t + r) * a.k + j];
-          next_gw[i] = a.grad_w[(size_t)(t + r) * a.k + j];
-        }
+      next_id = -1;
+      next_gw = 0.0f;
+      if (picker && t < t1 && (!a.mask || a.mask[t])) {
+        next_id = a.ids[(size_t)t * a.k + j];
+        next_gw = a.grad_w[(size_t)t * a.k + j];
       }
     };
-    auto fetch_picks = [&](int t) {  // of the batch whose ids have come, and the next one's ids
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        id[i] = next_id[i] < a.E ? next_id[i] : -1;
-        gw[i] = id[i] >= 0 ? next_gw[i] : 0.0f;
-        xk[i] = Row<DT>::put(-__builtin_inff());
-        if (id[i] >= 0) xk[i] = static_cast<const T*>(a.logits)[(size_t)(t + row_of(i)) * a.E + id[i]];
-      }
-      fetch_ids(t + R * kGroups);
+    auto fetch_picks = [&](int t) {  // of the row whose ids have come, and the next one's ids
+      id = next_id < a.E ? next_id : -1;
+      gw = id >= 0 ? next_gw : 0.0f;
+      xk = Row<DT>::put(-__builtin_inff());
+      if (id >= 0) xk = static_cast<const T*>(a.logits)[(size_t)t * a.E + id];
+      fetch_ids(t + kGroups);
     };
-    if (a.grad_w) fetch_ids(t0 + grp * R);
-    fetch(t0 + grp * R);
+    if (a.grad_w) fetch_ids(t0 + grp);
+    fetch(t0 + grp);
     float cnt[NI][4] = {}, g = 0.0f;
     if (a.counts) {
 #pragma unroll
@@ -646,116 +630,100 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
     }
     if (a.grad_w) {
       if (fresh) {
-        for (int i = tid; i < kGroups * R * a.E; i += kThreads) picks[i] = 0.0f;
+        for (int i = tid; i < kGroups * a.E; i += kThreads) picks[i] = 0.0f;
         __syncthreads();
       }
-      fetch_picks(t0 + grp * R);
+      fetch_picks(t0 + grp);
     }
     fresh = false;
-    for (int tb = t0; tb < t1; tb += R * kGroups) {
-      const int t = tb + grp * R;
+    for (int tb = t0; tb < t1; tb += kGroups) {
+      const int t = tb + grp;
       const T* row = static_cast<const T*>(a.logits) + (size_t)min(t, t1 - 1) * a.E;
-      float d[R][NI][4], total[R], dot[R];
-      bool live[R];
-      int at[kTurns];  // the picks' places in LDS, -1 for none
-      float p[kTurns];
-      if (a.grad_w)
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-          at[i] = id[i] >= 0 ? row_of(i) * a.E + id[i] : -1;
-          const float x = Row<DT>::get(xk[i]);
-          p[i] = few ? pick_grad<16>(x, gw[i]) : pick_grad<64>(x, gw[i]);
-        }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        live[r] = t + r < t1 && (!a.mask || a.mask[t + r]);
-        if (a.counts)
-#pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) d[r][i][v] = Row<DT>::get(next[r][i].v[v]);
+      float d[NI][4], total = 0.0f, dot = 0.0f, p = 0.0f;
+      int at = -1;  // the pick's place in LDS
+      if (a.grad_w) {
+        at = id;
+        const float x = Row<DT>::get(xk);
+        p = few ? pick_grad<16>(x, gw) : pick_grad<64>(x, gw);
       }
-      if (tb + R * kGroups < t1) {
-        if (a.grad_w) fetch_picks(t + R * kGroups);
-        fetch(t + R * kGroups);
-      }
-      if (a.grad_w)
+      const bool live = t < t1 && (!a.mask || a.mask[t]);
+      if (a.counts)
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i)
-          if (at[i] >= 0) atomicAdd(&extra[at[i]], p[i]);
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) d[i][v] = Row<DT>::get(next[i].v[v]);
+      if (tb + kGroups < t1) {
+        if (a.grad_w) fetch_picks(t + kGroups);
+        fetch(t + kGroups);
+      }
+      if (at >= 0) atomicAdd(&extra[at], p);
       if (a.counts) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          total[r] = dot[r] = 0.0f;
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float s = sigmoid(d[r][i][v], d[r][i][v]);
-              total[r] += s;
-              dot[r] = fmaf(cnt[i][v], s, dot[r]);
-            }
-          total[r] = seg_sum<kSeg>(total[r]);
-          dot[r] = seg_sum<kSeg>(dot[r]);
-        }
+          for (int v = 0; v < 4; ++v) {
+            const float s = sigmoid(d[i][v], d[i][v]);
+            total += s;
+            dot = fmaf(cnt[i][v], s, dot);
+          }
+        total = seg_sum<kSeg>(total);
+        dot = seg_sum<kSeg>(dot);
         if constexpr (G > 64) {
-          if (lane == 0)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              box[0][wv * R + r] = total[r];
-              box[1][wv * R + r] = dot[r];
-            }
+          if (lane == 0) {
+            box[0][wv] = total;
+            box[1][wv] = dot;
+          }
         }
       }
-      if constexpr (G > 64) __syncthreads();
-      else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if constexpr (G > 64) {
+        __syncthreads();
         if (a.counts) {
-          sum_waves<G / 64, R>(box[0], total);
-          sum_waves<G / 64, R>(box[1], dot);
-        }
-      }
+          total = dot = 0.0f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (t + r >= t1) continue;
+          for (int w = 0; w < G / 64; ++w) {
+            total += box[0][w];
+            dot += box[1][w];
+          }
+        }
+      } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      if (t < t1) {
         float f = 0.0f, mean = 0.0f;
-        if (live[r] && a.counts) {
+        if (live && a.counts) {
           float scale = 1.0f;
-          if (total[r] < kTiny) {
-            far_shares<DT, G, NI>(row + (size_t)r * a.E, c0, a.E, far_box, d[r]);
-            dot[r] = 0.0f;
+          if (total < kTiny) {
+            far_shares<DT, G, NI>(row, c0, a.E, far_box, d);
+            dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
-              for (int v = 0; v < 4; ++v) dot[r] = fmaf(cnt[i][v], d[r][i][v], dot[r]);
-            dot[r] = group_sum<G>(dot[r], far_box);
+              for (int v = 0; v < 4; ++v) dot = fmaf(cnt[i][v], d[i][v], dot);
+            dot = group_sum<G>(dot, far_box);
           } else {
-            scale = 1.0f / total[r];
+            scale = 1.0f / total;
           }
           f = g * scale;
-          mean = dot[r] * scale * f;
+          mean = dot * scale * f;
         }
-        T* dst = static_cast<T*>(a.out) + (size_t)(t + r) * a.E;
+        T* dst = static_cast<T*>(a.out) + (size_t)t * a.E;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           const int col = c0 + i * G * 4;
-          if (live[r] && a.counts)
+          if (live && a.counts)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o[v] = fmaf(cnt[i][v], f, -mean) * d[r][i][v];
-          if (live[r] && a.grad_w)
+            for (int v = 0; v < 4; ++v) o[v] = fmaf(cnt[i][v], f, -mean) * d[i][v];
+          if (live && a.grad_w)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              if (i < NI - 1 || col + v < a.E) o[v] += extra[(size_t)r * a.E + col + v];
+              if (i < NI - 1 || col + v < a.E) o[v] += extra[col + v];
           store4<DT>(dst, col, a.E, i < NI - 1, o);
         }
       }
       if constexpr (G > 64) __syncthreads();
       else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (a.grad_w)
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i)
-          if (at[i] >= 0) extra[at[i]] = 0.0f;
+      if (at >= 0) extra[at] = 0.0f;
     }
     t0 = t1;
   }
@@ -977,13 +945,13 @@ extern "C" int moe_router_backward(const void* logits, int logits_dtype, const i
   a.k = k;
   a.B = B;
   const int G = group_of(E, grad_w != nullptr, k);
-  a.chunk = chunk_of(M, back_rows(G) * (kThreads / G), G < 256 ? 1024 : 512);
+  a.chunk = chunk_of(M, kThreads / G, 1024);  // four workgroups a compute unit
   a.coef = coef;
   a.counts = const_cast<int32_t*>(counts);
   a.tokens = const_cast<int32_t*>(tokens);
   a.grad_w = grad_w;
   a.grad_loss = grad_loss;
   a.out = grad_logits;
-  const size_t lds = grad_w ? (size_t)back_rows(G) * (kThreads / G) * E * 4 : 0;
+  const size_t lds = grad_w ? (size_t)(kThreads / G) * E * 4 : 0;
   return launch(kernel_of<kBack>(logits_dtype, E, G), dim3((M + a.chunk - 1) / a.chunk), kThreads, lds, a, stream);
 }
