@@ -203,6 +203,30 @@ __device__ __forceinline__ void put_y(uint16_t* y, float v) {
   *y = v != v ? (uint16_t)0x7FC0u : (uint16_t)(r >> 16);
 }
 
+// Whether 16-byte chunks of y's rows are whole and aligned.
+template <typename Y>
+__device__ __forceinline__ bool wide_rows(const PArgs& a) {
+  return a.N % (16 / sizeof(Y)) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+}
+
+// Zeros in a workgroup's tile of BM rows x BN columns, 256 threads.
+template <typename Y, int BM, int BN>
+__device__ __forceinline__ void zero_tile(const PArgs& a, int r0, int n0) {
+  const int tid = threadIdx.x;
+  Y* y = static_cast<Y*>(a.y) + (size_t)r0 * a.N + n0;
+  if (wide_rows<Y>(a)) {
+    constexpr int kChunk = 16 / sizeof(Y), kRow = BN / kChunk;  // values of a chunk, chunks of a row
+    const int c = tid % kRow * kChunk;
+    if (n0 + c < a.N)
+      for (int r = tid / kRow; r < BM; r += 256 / kRow)
+        __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4*>(y + (size_t)r * a.N + c));
+  } else {
+    const int c = tid % BN;
+    if (n0 + c < a.N)
+      for (int r = tid / BN; r < BM; r += 256 / BN) put_y(y + (size_t)r * a.N + c, 0.0f);
+  }
+}
+
 __device__ __forceinline__ i32x8 frag(u32x4 q) {
   const i32x4 v = __builtin_bit_cast(i32x4, q);
   return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -238,10 +262,14 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
   if (r0 >= npp || e < 0 || e >= a.E) return;
   const bool ok = s >= 0 && s < a.M * a.k;
   const uint32_t rows = (uint32_t)__ballot(ok) & 0xFFFFu;
+  if (!rows) {  // padding only
+    zero_tile<Y, 16, 16 * FN>(a, r0, n0);
+    return;
+  }
   f32x4 acc[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) acc[j] = f32x4{};
-  if (rows) {
+  {
     const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
     const size_t xr = ok ? (size_t)(a.sorted ? r0 + r16 : s / a.k) : 0;
     const uint8_t* xc = a.xc + xr * kb + q * 16;
@@ -320,7 +348,7 @@ __global__ __launch_bounds__(256) void k_product_rows(PArgs a) {
 // 435 us: 1.6 GB that must move at 3.7 TB/s; with the experts' rows read again
 // from the L2's misses and y written, 2.2 GB at 5.0 TB/s (a 2 GiB copy: 4.9), which
 // bounds it now (without the multiplications it takes 410 us).  64 tokens of the
-// same experts in blocks of 16: 901 MB of weights in 165 us, 5.5 TB/s.
+// same experts in blocks of 16: 901 MB of weights in 150 us, 6.0 TB/s.
 constexpr int kFN = 2, kNW = 4;  // 32-column operands a wave, waves
 constexpr int kCols = kNW * kFN * 32, kTileThreads = kNW * 64;
 
@@ -360,8 +388,9 @@ __device__ __forceinline__ void stage_scales(Scale8* dst, int left, F src) {
 // half repeats row 0 of x and is not stored.
 constexpr int tile_rows(int BM) { return BM < 32 ? 32 : BM; }
 // Steps in flight while one is multiplied: two where the registers allow it (2048
-// tokens, 256 experts, top-8, K = 3584, N = 768, blocks of 64: 109 us with one, 98
-// with two; 512 tokens in blocks of 128 of the same, tiles of 128 rows: two spill).
+// tokens, 256 experts, top-8, K = 3584, N = 768, blocks of 64: 109 us with one, 92
+// with two; tiles of 128 rows spill with two, tiles of 32 are slower with three, 223
+// against 213).
 constexpr int deep_of(int BM) { return BM < 128 ? 2 : 1; }
 
 // Whether weights that one row tile alone reads are loaded past the L2 (another
@@ -386,7 +415,7 @@ struct Weights {
   int row, last;                  // this lane's first row, the last row that exists
   uint32_t kb;                    // bytes of a row
   // o: byte of the row.  ONCE: no other row tile reads these weights, and the L2 need
-  // not keep them (896 experts, blocks of 16: 64 tokens 168 -> 158 us, 512 tokens 251 ->
+  // not keep them (896 experts, blocks of 16: 64 tokens 177 -> 165 us, 512 tokens 251 ->
   // 241; so loaded where row tiles share them, 2048 tokens and 256 experts 176 -> 220; nor
   // where all experts' fit the cache in front of the memory, which may have them from
   // the call before: 50 MB 13.6 -> 14.7).
@@ -513,13 +542,27 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
     }
     __syncthreads();
   };
-  for (int t = 0;;) {
+  int t = 0;
+  if constexpr (kDeep == 2) {
+    // no way out of the middle: with one, the compiler waits in every step for loads
+    // that only the last one has in flight
+    for (; t + 2 < steps; t += 2) {
+      step(t, xr[0], wr[0]);
+      store(xr[1], wr[1]);
+      __syncthreads();
+      step(t + 1, xr[1], wr[1]);
+      store(xr[0], wr[0]);
+      __syncthreads();
+    }
     step(t, xr[0], wr[0]);
-    if (++t == steps) break;
-    store(xr[kDeep - 1], wr[kDeep - 1]);
-    __syncthreads();
-    if constexpr (kDeep == 2) {
-      step(t, xr[1], wr[1]);
+    if (t + 1 < steps) {
+      store(xr[1], wr[1]);
+      __syncthreads();
+      step(t + 1, xr[1], wr[1]);
+    }
+  } else {
+    for (;;) {
+      step(t, xr[0], wr[0]);
       if (++t == steps) break;
       store(xr[0], wr[0]);
       __syncthreads();
@@ -532,8 +575,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
   // chunks of y's rows.
   constexpr int kRow = kFN * 32 * sizeof(Y), kPad = kRow + 16;  // bytes of a row in LDS
   static_assert(kNW * 32 * kPad <= (int)(sizeof(l.x) + sizeof(l.w)), "the results fit");
-  // 16-byte chunks stay inside the row and are aligned
-  const bool wide = a.N % (16 / sizeof(Y)) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  const bool wide = wide_rows<Y>(a);
   char* stage = reinterpret_cast<char*>(&l) + wv * 32 * kPad;
   const int n1 = n0 + wv * kFN * 32;
 #pragma unroll
@@ -605,9 +647,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_tile(PArgs a) {
     has[i] = __ballot(ok[i]);
   }
   if (!(has[0] | has[1])) {  // padding only: no weights are read
-    const int cols = min(kCols, a.N - n0);
-    for (int i = tid; i < BM * cols; i += kTileThreads)
-      put_y(static_cast<Y*>(a.y) + (size_t)(r0 + i / cols) * a.N + n0 + i % cols, 0.0f);
+    zero_tile<Y, BM, kCols>(a, r0, n0);
     return;
   }
   const size_t kb = (size_t)a.K / 2, ks = (size_t)a.K / 32;
@@ -649,34 +689,43 @@ const void* product_kernel(int bm, int bn) {
 // Tile sizes from the expected load.  Strips are the weights' tiles of 256 columns
 // over the experts that get a route; a workgroup of the tile kernel streams one.
 // With few of them and few rows the rows kernel's smaller tiles fill the chip (us,
-// rows kernel / tile kernel; 896 experts, top-16, K = 3584, N = 768, blocks of 32):
-// 1 token, 48 strips 9.6 / 22.6; 3 tokens, 144 strips 21.5 / 23.2; 4 tokens, 192
-// strips 26.8 / 24.3.  It reads the weights again for every 16 rows: 64 experts,
-// K = 1024, N = 512, 128 strips, 5 rows an expert 8.5 / 8.2, 10 rows 11.7 / 8.3;
-// 8 strips, 16 rows 4.2 / 7.9, 128 rows 9.9 / 8.2.
+// rows kernel / tile kernel; K = 3584, N = 768, blocks of 32): 1 token of 896 experts,
+// top-16, 48 strips 8.9 / 16.6; 2 tokens, 96 strips 14.5 / 18.0; 3 tokens, 144 strips
+// 20.3 / 20.0.  It reads the weights again for every 16 rows: 8 experts, 24 strips, 16
+// rows an expert 9.7 / 15.7, 64 rows 19.4 / 16.5.  And a block's row tiles that have
+// padding only are workgroups too, 1 ns each, while the tile kernel's time is its
+// steps': one token as above in blocks of 128 13.9 / 15.8, of 256 19.6 / 15.9; 64 experts,
+// K = 2048, 2 tokens, top-8, blocks of 64 9.7 / 10.5, of 128 12.7 / 10.5; K = 1024, N = 512,
+// 4 tokens, top-4, blocks of 64 5.9 / 7.6, of 256 13.0 / 7.6.
 //
 // The tile kernel takes the largest tile that divides the block (a part of 32 rows
-// without a route costs nothing but its zeros; 256 experts, K = 3584, blocks of
-// 128, 4 / 64 / 192 rows an expert: tiles of 128 99 / 111 / 149 us, of 64 107 / 129 /
-// 203, of 32 159 / 189 / 307), smaller ones where 128 workgroups would not come
-// together (8 experts, 512 tokens: tiles of 32 8.2 us, 64 10.2, 128 14.1).
+// without a route costs no multiplications; 256 experts, K = 3584, blocks of 128, 64 /
+// 128 / 192 rows an expert: tiles of 128 100 / 124 / 154 us, of 64 96 / 129 / 173, of 32
+// 117 / 165 / 220), but none of 128 for fewer than 48 rows, of which most of the steps'
+// loads would be padding's (16 rows 97 / 87 / 91; blocks of 256 107 / 100 / 98), and
+// smaller ones where 128 workgroups would not come together (8 experts, 512 tokens:
+// tiles of 32 8.2 us, 64 10.2, 128 14.1).
 //
 // Runs of row tiles: eight or more for each XCD, so that none has much more than
 // another (us with runs of 8 / with this rule: 2048 tokens, 64 experts, top-8 45.5 /
 // 34.0; 8192 tokens, 8 experts, top-2, blocks of 256 53.6 / 47.9), powers of two up
-// to 16 (8192 tokens, 896 experts: 428, runs of 23 446).
+// to 16 (8192 tokens, 896 experts: 428, runs of 23 446), and whole blocks, or the tiles that
+// have routes, the first of each block, fall to some of the XCDs only (64 experts, K =
+// 1024, 16 rows an expert, blocks of 128 12.8 / 10.0, of 256 22 / 11).
 struct Shape {
   int bm, bn, run;
 };
-Shape shape_of(int64_t routes, int64_t used, int N, int block) {
+Shape shape_of(int64_t routes, int64_t used, int K, int N, int block) {
   const int64_t cols = (N + kCols - 1) / kCols, strips = used * cols;
-  if (strips < 192 && strips * routes <= 768 * used)
+  if (strips < 192 && strips * routes <= 768 * used && strips * (block / 16) <= 160 + K / 16)
     return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32, 1};
-  int bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
+  int bm = block % 128 == 0 && routes > 48 * used ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
   while (strips < 192 && bm > 32 && routes / bm * cols < 128) bm /= 2;
   const int64_t tiles = routes / bm + used / 2;  // an expert's last tile is half full
   int run = 1;
   while (run < 16 && run * 128 <= tiles) run *= 2;
+  const int each = block / bm;  // row tiles of a block
+  run = (run + each - 1) / each * each;
   return {bm, kCols, run};
 }
 
@@ -725,7 +774,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
       !aligned(sorted_ids, 4) || !aligned(expert_of_block, 4) || !aligned(num_post_pad, 4) || !aligned(y, 4))
     return MRS_ERR_MISALIGNED;
   const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E;
-  const Shape shape = shape_of(routes, used, N, block);
+  const Shape shape = shape_of(routes, used, K, N, block);
   const int bm = shape.bm, bn = shape.bn;
   const int64_t nrt = row_limit / bm, ntn = ((int64_t)N + bn - 1) / bn;
   int64_t grid;
