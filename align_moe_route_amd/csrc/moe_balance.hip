@@ -13,9 +13,9 @@
 // rounding.
 //
 // Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s):
-// forward 16384 x 4096 FP32, 37 sequences, in 61 us (276 MB, 4.5 TB/s; the pieces
-// add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 31 us; backward 102
-// and 48 us (541 and 273 MB, 5.3 and 5.7 TB/s).  8192 x 896 BF16 takes 15.5 us
+// forward 16384 x 4096 FP32, 37 sequences, in 60 us (276 MB, 4.6 TB/s; the pieces
+// add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 30 us; backward 99
+// and 47 us (541 and 273 MB, 5.5 and 5.8 TB/s).  8192 x 896 BF16 takes 15.5 us
 // forward, 8 of them the second launch's chain of round trips, and 11.5 us backward
 // (30 MB; 6 us of arithmetic, the rest latency); 131072 x 128 BF16 20 and 24 us.
 
@@ -307,7 +307,10 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
     const int t1 = max(t0, b == a.B - 1 ? t_end : min(offset_of(a, b + 1), t_end));
     if (!SINGLE && t1 == t0) continue;
     Four<DT> next[R][NI];
+    int next_mask[R];  // with its row: a load to wait for would drain those in flight
     auto fetch = [&](int t) {  // rows past the sequence's last one repeat it
+#pragma unroll
+      for (int r = 0; r < R; ++r) next_mask[r] = a.mask ? a.mask[min(t + r, t1 - 1)] : 1;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -320,8 +323,8 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
     if (tid == 0) live_tokens = 0;
     __syncthreads();
     for (int i = tid; i < (t1 - t0) * a.k; i += kThreads) {
-      const int id = a.ids[(size_t)t0 * a.k + i];
-      if (id >= 0 && id < a.E && (!a.mask || a.mask[t0 + i / a.k])) atomicAdd(&hist[id], 1);
+      const int id = a.ids[(size_t)t0 * a.k + i], mask = a.mask ? a.mask[t0 + i / a.k] : 1;
+      if (id >= 0 && id < a.E && mask) atomicAdd(&hist[id], 1);
     }
     float acc[NI][4] = {};
     int n = 0, turn = 0;
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
       bool live[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        live[r] = t + r < t1 && (!a.mask || a.mask[t + r]);
+        live[r] = t + r < t1 && next_mask[r];
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -560,6 +563,14 @@ __device__ __forceinline__ float pick_grad(float xk, float gw) {
   return w * rest * (gw - seg_sum<S>(gw * w));
 }
 
+// Token t's mask, 1 without one: a load either way, since a constant in its place
+// waits for the loads in flight before it is written over the last one's register
+// (16384 x 4096 FP32 without a mask 101 us, with the constant 108).
+__device__ __forceinline__ int mask_of(const BArgs& a, int t) {
+  const uint8_t* p = a.mask ? a.mask + t : reinterpret_cast<const uint8_t*>(a.ids);
+  return *p | (a.mask ? 0 : 1);
+}
+
 // d/dx of the balance loss of row t: g_b s' / S * (count[b,e] - sum_e' count[b,e'] p[e']),
 // g_b = grad_loss coef E / (k n_b^2 B'); of the picks' weights:
 // w_j (1 - s_j) (grad_w_j - sum_i grad_w_i w_i), added through a row of LDS.  One
@@ -597,25 +608,29 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
                               i < NI - 1);
     };
     // a row's ids are two rows ahead, the logits that they name one
+    int mask, next_mask;  // of the same rows: a load to wait for would drain those in flight
     int id, next_id;
     float gw, next_gw;
     T xk;
     auto fetch_ids = [&](int t) {
+      next_mask = mask_of(a, min(t, t1 - 1));
       next_id = -1;
-      next_gw = 0.0f;
-      if (picker && t < t1 && (!a.mask || a.mask[t])) {
+      if (a.grad_w && picker && t < t1) {
         next_id = a.ids[(size_t)t * a.k + j];
         next_gw = a.grad_w[(size_t)t * a.k + j];
       }
     };
     auto fetch_picks = [&](int t) {  // of the row whose ids have come, and the next one's ids
-      id = next_id < a.E ? next_id : -1;
-      gw = id >= 0 ? next_gw : 0.0f;
-      xk = Row<DT>::put(-__builtin_inff());
-      if (id >= 0) xk = static_cast<const T*>(a.logits)[(size_t)t * a.E + id];
+      mask = next_mask;
+      if (a.grad_w) {
+        id = mask && next_id < a.E ? next_id : -1;
+        gw = id >= 0 ? next_gw : 0.0f;
+        xk = Row<DT>::put(-__builtin_inff());
+        if (id >= 0) xk = static_cast<const T*>(a.logits)[(size_t)t * a.E + id];
+      }
       fetch_ids(t + kGroups);
     };
-    if (a.grad_w) fetch_ids(t0 + grp);
+    fetch_ids(t0 + grp);
     fetch(t0 + grp);
     float cnt[NI][4] = {}, g = 0.0f;
     if (a.counts) {
@@ -633,8 +648,8 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
         for (int i = tid; i < kGroups * a.E; i += kThreads) picks[i] = 0.0f;
         __syncthreads();
       }
-      fetch_picks(t0 + grp);
     }
+    fetch_picks(t0 + grp);
     fresh = false;
     for (int tb = t0; tb < t1; tb += kGroups) {
       const int t = tb + grp;
@@ -646,14 +661,14 @@ __global__ __launch_bounds__(kThreads) void k_router_backward(BArgs a) {
         const float x = Row<DT>::get(xk);
         p = few ? pick_grad<16>(x, gw) : pick_grad<64>(x, gw);
       }
-      const bool live = t < t1 && (!a.mask || a.mask[t]);
+      const bool live = t < t1 && mask;
       if (a.counts)
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int v = 0; v < 4; ++v) d[i][v] = Row<DT>::get(next[i].v[v]);
       if (tb + kGroups < t1) {
-        if (a.grad_w) fetch_picks(t + kGroups);
+        fetch_picks(t + kGroups);
         fetch(t + kGroups);
       }
       if (at >= 0) atomicAdd(&extra[at], p);
