@@ -239,7 +239,7 @@ __device__ __forceinline__ i32x8 frag(u32x4 q) {
 // lane l holds columns 32 (l / 16) .. + 31 of row l mod 16, which is one chunk
 // and one scale byte), U steps in flight at a time, and nothing goes through
 // LDS but the partial sums.  Padding rows load nothing.  896 experts, top-16, K =
-// 3584, N = 768, blocks of 32: one token in 9.0 us, 24 MB at 2.6 TB/s, of which 3.4
+// 3584, N = 768, blocks of 32: one token in 8.8 us, 24 MB at 2.7 TB/s, of which 3.4
 // us pass with a single step (the launch, the metadata, one round trip).  Eight
 // steps in flight measured best (64 tokens 203 us, six or ten 220 us).
 constexpr int kRowsDeep = 8;
@@ -709,9 +709,12 @@ const void* product_kernel(int bm, int bn) {
 // Runs of row tiles: eight or more for each XCD, so that none has much more than
 // another (us with runs of 8 / with this rule: 2048 tokens, 64 experts, top-8 45.5 /
 // 34.0; 8192 tokens, 8 experts, top-2, blocks of 256 53.6 / 47.9), powers of two up
-// to 16 (8192 tokens, 896 experts: 428, runs of 23 446), and whole blocks, or the tiles that
-// have routes, the first of each block, fall to some of the XCDs only (64 experts, K =
-// 1024, 16 rows an expert, blocks of 128 12.8 / 10.0, of 256 22 / 11).
+// to 16 (8192 tokens, 896 experts: 428, runs of 23 446).  Whole blocks, or the
+// tiles that have routes, the first of each block, fall to some of the XCDs only (64
+// experts, K = 1024, 16 rows an expert, blocks of 128 12.8 / 10.0, of 256 22 / 11) and an
+// expert's weights are read by all of them (8 experts, 250 rows each, blocks of 256 16.5
+// / 13.8); but not those of fewer experts than XCDs with routes in most of a block's
+// tiles, which would keep to a few XCDs (2 experts, blocks of 1024 34 / 21.5).
 struct Shape {
   int bm, bn, run;
 };
@@ -724,8 +727,8 @@ Shape shape_of(int64_t routes, int64_t used, int K, int N, int block) {
   const int64_t tiles = routes / bm + used / 2;  // an expert's last tile is half full
   int run = 1;
   while (run < 16 && run * 128 <= tiles) run *= 2;
-  const int each = block / bm;  // row tiles of a block
-  run = (run + each - 1) / each * each;
+  const int64_t each = block / bm, live = (routes / used + bm - 1) / bm;  // tiles of a block, with routes
+  if (used >= kXcds || 2 * live <= each) run = (int)((run + each - 1) / each * each);
   return {bm, kCols, run};
 }
 
