@@ -597,7 +597,7 @@ __device__ __forceinline__ void tile_body(const PArgs& a, int r0, int n0, const 
         const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
         const int n = n1 + c * (16 / (int)sizeof(Y));
         const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
-                // not kept in the L2, which the rows and weights need (8192 tokens, 896 experts:
+        // not kept in the L2, which the rows and weights need (8192 tokens, 896 experts:
         // 447 -> 435 us; 64 tokens, 256 experts, blocks of 128: 93.5 -> 87)
         if (n < a.N && (BM >= 32 || r < BM))
           __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(y + (size_t)r * a.N + n));
