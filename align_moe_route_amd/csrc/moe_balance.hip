@@ -757,7 +757,7 @@ int group_of(int E, bool picks, int k) { return E <= 256 && !(picks && k > 16) ?
 int columns_of(int E, int G) { return (E + 4 * G - 1) / (4 * G); }
 
 constexpr int kSingleBatches = 4;  // batches that one workgroup does alone
-constexpr int kSingleB = 64;
+constexpr int kSingleB = 4;  // 64 x 64: one workgroup 7.0 us for 3 sequences, 11.9 for 6, several 10.4
 // Workgroups of the second kernel that may share a counter, 40 ns each, in place of
 // a third launch (65536 x 64, 64 sequences: with 64 of them 18.9 us, with the launch
 // 17.8; 65536 x 128, 16 sequences, 32 of them: 17.2 and 18.2).
@@ -781,6 +781,11 @@ Plan plan_of(int M, int E, int B) {
   p.single = M <= alone && B <= kSingleB;
   // a workgroup for each compute unit: eight waves, or twice four
   p.chunk = p.single ? alone : chunk_of(M, batch, G < 256 ? 256 : 512);
+  // a workgroup takes its sequences one after another, 2 us each: fewer rows where
+  // they are short (256 x 256, 8 sequences 19.3 -> 13.4 us; 901 x 190, 49 of them 28 ->
+  // 15.8; 2000 x 64, 200 of them 32.5 -> 15.1)
+  if (!p.single && p.chunk == batch)
+    while (p.chunk > 4 && p.chunk > M / B / 4 && M / p.chunk < 512) p.chunk /= 2;
   p.chunks = (M + p.chunk - 1) / p.chunk;
   const int pieces = p.chunks / B;  // of a sequence
   // Threads of the second kernel: 32 walkers of 32 experts for long sequences (1024
