@@ -763,10 +763,16 @@ constexpr int kSingleB = 4;  // 64 x 64: one workgroup 7.0 us for 3 sequences, 1
 // 17.8; 65536 x 128, 16 sequences, 32 of them: 17.2 and 18.2).
 constexpr int kTicketMax = 32;
 
-// Tokens of a workgroup when `grid` of them run at once.
-int chunk_of(int M, int batch, int grid) {
+// Tokens of a workgroup when `grid` of them run at once.  It takes its sequences one
+// after another, 2 us each: fewer rows where they are short (forward 256 x 256, 8
+// sequences 19.3 -> 13.4 us; 901 x 190, 49 of them 28 -> 15.8; 2000 x 64, 200 of them 32.5 ->
+// 15.1; backward the last two 12.8 -> 8.6 and 11.8 -> 7.8).
+int chunk_of(int M, int B, int batch, int grid) {
   const int each = (M + grid - 1) / grid;
-  return each <= batch ? batch : (each + batch - 1) / batch * batch;
+  if (each > batch) return (each + batch - 1) / batch * batch;
+  int chunk = batch;
+  while (chunk > 4 && chunk > M / B / 4 && M / chunk < grid) chunk /= 2;
+  return chunk;
 }
 
 struct Plan {
@@ -780,12 +786,7 @@ Plan plan_of(int M, int E, int B) {
   const int G = group_of(E, false, 0), batch = kPartRows * (part_threads(G) / G), alone = kSingleBatches * batch;
   p.single = M <= alone && B <= kSingleB;
   // a workgroup for each compute unit: eight waves, or twice four
-  p.chunk = p.single ? alone : chunk_of(M, batch, G < 256 ? 256 : 512);
-  // a workgroup takes its sequences one after another, 2 us each: fewer rows where
-  // they are short (256 x 256, 8 sequences 19.3 -> 13.4 us; 901 x 190, 49 of them 28 ->
-  // 15.8; 2000 x 64, 200 of them 32.5 -> 15.1)
-  if (!p.single && p.chunk == batch)
-    while (p.chunk > 4 && p.chunk > M / B / 4 && M / p.chunk < 512) p.chunk /= 2;
+  p.chunk = p.single ? alone : chunk_of(M, B, batch, G < 256 ? 256 : 512);
   p.chunks = (M + p.chunk - 1) / p.chunk;
   const int pieces = p.chunks / B;  // of a sequence
   // Threads of the second kernel: 32 walkers of 32 experts for long sequences (1024
@@ -965,7 +966,7 @@ extern "C" int moe_router_backward(const void* logits, int logits_dtype, const i
   a.k = k;
   a.B = B;
   const int G = group_of(E, grad_w != nullptr, k);
-  a.chunk = chunk_of(M, kThreads / G, 1024);  // four workgroups a compute unit
+  a.chunk = chunk_of(M, B, kThreads / G, 1024);  // four workgroups a compute unit
   a.coef = coef;
   a.counts = const_cast<int32_t*>(counts);
   a.tokens = const_cast<int32_t*>(tokens);
