@@ -521,9 +521,8 @@ __global__ __launch_bounds__(1024) void k_balance_sum(BArgs a, int lcols, int lw
     a.ws_loss[(size_t)b * tiles + blockIdx.x] = part;
     if (blockIdx.x == 0) a.tokens[b] = n;
     if constexpr (TICKET) {
-      __threadfence();
-      last = atomicAdd(a.ws_ticket, 1u) == (uint32_t)tiles * (uint32_t)a.B - 1u;
-      __threadfence();
+      last = __hip_atomic_fetch_add(a.ws_ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             (uint32_t)tiles * (uint32_t)a.B - 1u;
     }
   }
   if constexpr (TICKET) {
