@@ -9,6 +9,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -173,7 +174,8 @@ def _workspace(device, stream_handle: int, nbytes: int):
     streams may overlap in time and each stream gets buffers of its own.  An
     outgrown buffer is kept, not freed, since a captured graph may still hold
     its address; sizes are powers of two, so a stream's buffers add up to less
-    than twice the largest."""
+    than twice the largest.  A buffer is allocated and filled on its own stream:
+    on another one the fill could run beside the kernels that use the buffer."""
     import torch
     bufs = _ws_cache.setdefault((str(device), int(stream_handle)), [])
     if bufs and bufs[-1].numel() >= nbytes:
@@ -181,7 +183,12 @@ def _workspace(device, stream_handle: int, nbytes: int):
     size = 256
     while size < nbytes:
         size *= 2
-    bufs.append(torch.zeros(size, dtype=torch.uint8, device=device))
+    own = contextlib.nullcontext()
+    if torch.device(device).type == "cuda":
+        own = torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=device) if stream_handle else
+                                torch.cuda.default_stream(device))
+    with own:
+        bufs.append(torch.zeros(size, dtype=torch.uint8, device=device))
     return bufs[-1]
 
 
@@ -565,6 +572,35 @@ def _handle(stream, dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
+def _foreign(stream, dev):
+    """`stream` where it is not dev's current stream, else None."""
+    return None if stream.cuda_stream == _handle(None, dev) else stream
+
+
+def _allocate(foreign, dev, make):
+    """make()'s tensors, which a call on the stream `foreign` writes: out of that
+    stream's memory (a block that the current stream's work still reads is not
+    written), and not given back before the current stream, where they go, is
+    through with them."""
+    import torch
+    if foreign is None:
+        return make()
+    with torch.cuda.stream(foreign):
+        made = make()
+    current = torch.cuda.current_stream(dev)
+    for t in made:
+        t.record_stream(current)
+    return made
+
+
+def _hold(foreign, *tensors):
+    """The memory of what a call on the stream `foreign` reads or writes is not
+    given back before that stream has passed the call."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(foreign)
+
+
 def _empty(shape, dtype, dev):
     """A contiguous tensor.  With the strides given, torch takes 1.3 us in place of
     1.7, which shows in calls of a token or two."""
@@ -605,7 +641,9 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     stride (a slice of a wider buffer's columns is fine).
     values: optional contiguous tensor of x's shape and type that takes the
     values the 4-bit rows stand for (for training with rounded values).
-    out: optional MXFP4 to write into, codes [..., Kp / 2], scales [..., Kp / 32]."""
+    out: optional MXFP4 to write into, codes [..., Kp / 2], scales [..., Kp / 32].
+    stream: the stream to run on, by default the current one; on another the
+    caller orders it after what made the inputs and before what reads the results."""
     import torch
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() >= 1):
         raise ValueError("x must be a GPU tensor of at least one dimension")
@@ -634,8 +672,10 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
             raise ValueError("x's rows must not overlap")
     dev = x.device
     Kp = (K + 127) // 128 * 128
+    foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = MXFP4(_empty((*lead, Kp // 2), torch.uint8, dev), _empty((*lead, Kp // 32), torch.uint8, dev))
+        out = _allocate(foreign, dev, lambda: MXFP4(_empty((*lead, Kp // 2), torch.uint8, dev),
+                                                    _empty((*lead, Kp // 32), torch.uint8, dev)))
     else:
         _check_mxfp4(out, dev, x.dim(), "out")
         if out.codes.shape != (*lead, Kp // 2):
@@ -648,6 +688,8 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     rc = int(lib().moe_mxfp4_quantize(x.data_ptr(), dts[x.dtype], rows, K, row_stride, out.codes.data_ptr(),
                                       out.scales.data_ptr(), values.data_ptr() if values is not None else None,
                                       handle))
+    if foreign is not None:
+        _hold(foreign, x, *out, values)
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -663,7 +705,8 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
     given, x holds max_rows rows in sorted order and row(r) = r (a later product
     on the rows an earlier one wrote).  w: 4-bit rows [E, N].  block: a multiple
     of 16.  out_dtype: bfloat16 (default) or float32.  Returns y [max_rows, N];
-    rows at or past num_post_pad are left as they were."""
+    rows at or past num_post_pad are left as they were.  stream: as for
+    mxfp4_quantize."""
     import torch
     if not (isinstance(x, MXFP4) and isinstance(x.codes, torch.Tensor) and x.codes.is_cuda):
         raise ValueError("x must be an MXFP4 of GPU tensors")
@@ -679,8 +722,9 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
     if tokens is not None and x.codes.shape[0] < rows:
         raise ValueError(f"x must hold at least {rows} rows in sorted order")
     _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = _empty((max(rows, 1), N), out_dtype or torch.bfloat16, dev)
+        out, = _allocate(foreign, dev, lambda: (_empty((max(rows, 1), N), out_dtype or torch.bfloat16, dev),))
     elif not (isinstance(out, torch.Tensor) and out.device == dev and out.is_contiguous() and out.dim() == 2
               and out.shape[1] == N and out.shape[0] >= rows and (out_dtype is None or out.dtype == out_dtype)):
         raise ValueError("out must be a contiguous [max_rows, N] tensor of out_dtype on x's device")
@@ -692,6 +736,8 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
         expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, Kp, N, block,
         MRS_X_TOKENS if tokens is None else MRS_X_SORTED,
         MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), handle))
+    if foreign is not None:
+        _hold(foreign, *x, *w, sorted_ids, expert_of_block, num_post_pad, out)
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -751,14 +797,17 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
     logits: [M, E] float32 or bfloat16, ids: [M, k] int32 as route_sort returns
     them (ids outside [0, E) are dropped routes).  seq_offsets: int32 [B + 1],
     the loss is the mean over the sequences; mask: bool or uint8 [M], zero for
-    padding tokens.  workspace: as for route_sort (balance_workspace_bytes)."""
+    padding tokens.  workspace: as for route_sort (balance_workspace_bytes);
+    stream: as for mxfp4_quantize."""
     import torch
     dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
     dev = logits.device
     nbytes = balance_workspace_bytes(M, E, k, B)
+    foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = BalanceOutput(_empty((1,), torch.float32, dev), _empty((B, E), torch.int32, dev),
-                            _empty((B + 1,), torch.int32, dev), _empty((B, E), torch.float32, dev))
+        out = _allocate(foreign, dev, lambda: BalanceOutput(
+            _empty((1,), torch.float32, dev), _empty((B, E), torch.int32, dev),
+            _empty((B + 1,), torch.int32, dev), _empty((B, E), torch.float32, dev)))
     else:
         for t, dtype, shape, name in ((out.loss, torch.float32, (1,), "out.loss"),
                                       (out.counts, torch.int32, (B, E), "out.counts"),
@@ -776,6 +825,8 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
                                     float(coef), out.loss.data_ptr(), out.counts.data_ptr(), out.tokens.data_ptr(),
                                     out.shares.data_ptr(), workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), handle))
+    if foreign is not None:
+        _hold(foreign, logits, ids, seq_offsets, mask, *out, workspace)
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
@@ -787,7 +838,7 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
     `balance` (what balance_loss returned for the same logits, ids, seq_offsets
     and mask) is given, times grad_loss (float32 [1], default 1), plus that of
     the routing weights when grad_weights ([M, k] float32) is given.  Returns
-    [M, E] of the logits' type."""
+    [M, E] of the logits' type.  stream: as for mxfp4_quantize."""
     import torch
     dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
     dev = logits.device
@@ -802,8 +853,9 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
                 raise ValueError(f"{name} must have shape {shape}")
     if grad_loss is not None:
         _check_tensor(grad_loss, dev, torch.float32, 1, "grad_loss")
+    foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = torch.empty_like(logits)
+        out, = _allocate(foreign, dev, lambda: (torch.empty_like(logits),))
     else:
         _check_tensor(out, dev, logits.dtype, M * E, "out")
         if out.shape != logits.shape:
@@ -814,6 +866,9 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
                                        _ptr(balance.tokens) if balance is not None else None, _ptr(grad_loss),
                                        _ptr(seq_offsets), _ptr(mask), M, E, k, B, float(coef), out.data_ptr(),
                                        handle))
+    if foreign is not None:
+        _hold(foreign, logits, ids, grad_weights, grad_loss, seq_offsets, mask, out,
+              *(() if balance is None else (balance.counts, balance.tokens)))
     if rc != MRS_OK:
         raise RouteSortError(rc)
     return out
