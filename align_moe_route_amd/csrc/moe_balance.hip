@@ -556,7 +556,7 @@ __device__ __forceinline__ float pick_grad(float xk, float gw) {
   const float u = fast_exp(-__builtin_fabsf(xk)), q = fast_rcp(1.0f + u);
   float w = xk > 0.0f ? q : (xk != xk ? xk : fast_exp(xk - m) * q);  // s / exp(m)
   const float rest = xk > 0.0f ? u * q : q;                          // 1 - s
-  if (m == -__builtin_inff()) w = 0.0f;
+  if (m == -__builtin_inff()) w = xk != xk ? xk : 0.0f;  // the maximum passes NaN over
   const float sum = seg_sum<S>(w);
   w = sum > 0.0f || sum != sum ? w / sum : 0.0f;
   return w * rest * (gw - seg_sum<S>(gw * w));
