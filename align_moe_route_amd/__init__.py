@@ -56,6 +56,7 @@ EXPORTED = [
     "moe_grouped_gemm_mxfp4",
     "moe_balance_workspace_bytes",
     "moe_balance_loss",
+    "moe_route_far_weights",
     "moe_router_backward",
 ]
 
@@ -119,6 +120,8 @@ def lib() -> ctypes.CDLL:
     L.moe_balance_workspace_bytes.restype = sz
     L.moe_balance_loss.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]
     L.moe_balance_loss.restype = i32
+    L.moe_route_far_weights.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp]
+    L.moe_route_far_weights.restype = i32
     L.moe_router_backward.argtypes = [vp, i32] + [vp] * 7 + [i32] * 4 + [f32, vp, vp]
     L.moe_router_backward.restype = i32
     _lib = L
@@ -883,6 +886,12 @@ def _route_train_function():
         @staticmethod
         def forward(ctx, logits, bias, sizes, coef, seq_offsets, mask):
             out = route_sort(logits, bias, *sizes)
+            rc = int(lib().moe_route_far_weights(logits.data_ptr(),
+                                                 MRS_DTYPE_F32 if logits.dtype == torch.float32 else MRS_DTYPE_BF16,
+                                                 out.ids.data_ptr(), *logits.shape, sizes[0], out.weights.data_ptr(),
+                                                 _handle(None, logits.device)))
+            if rc != MRS_OK:
+                raise RouteSortError(rc)
             bal = balance_loss(logits, out.ids, coef, seq_offsets=seq_offsets, mask=mask)
             ctx.save_for_backward(logits, out.ids, bal.counts, bal.tokens, seq_offsets, mask)
             ctx.coef = coef
@@ -914,7 +923,10 @@ def route_sort_train(logits, bias, k: int, n_group: int, topk_group: int, block:
 
     logits, bias and sizes as for route_sort, coefficient, seq_offsets and mask as
     for balance_loss; padding tokens (mask) are routed as any other but take part
-    in neither the loss nor the gradients.  To capture a training step in a graph
+    in neither the loss nor the gradients.  Tokens whose picked logits all lie below
+    -87 (rows of the type's lowest value, say) get the weights that the gradient is
+    the gradient of, in place of the route's infinite or NaN quotients of vanished
+    scores (moe_route_far_weights).  To capture a training step in a graph
     call balance_loss and router_backward themselves."""
     w, loss, ids, sid, eob, npp, counts, tokens, shares = _route_train_function().apply(
         logits, bias, (k, n_group, topk_group, block), float(balance_coef), seq_offsets, mask)

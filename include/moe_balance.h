@@ -54,6 +54,26 @@ int moe_balance_loss(const void* logits, int logits_dtype, const int32_t* ids, c
                      int32_t* tokens, float* shares, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * moe_route_far_weights -- the routing weights of tokens so far off that FP32
+ * scores cannot hold them, in place of those of moe_route_sort.
+ *
+ * For each token t whose kept picks' logits (ids[t,j] in [0, E)) all lie below
+ * -87, where the scores are subnormal or zero and their FP32 quotient is coarse,
+ * infinite or NaN:
+ *     weights[t,j] = exp(x_j - max_i x_i) / sum_i exp(x_i - max_i x_i),
+ *                    x_j = logits[t, ids[t,j]]
+ * which is the limit that moe_router_backward differentiates: 0 for a dropped
+ * pick, 0 for all where every pick is -infinity, NaN for all where one is NaN (a
+ * NaN does not count as a logit of -87 or more).  Other tokens' weights are not
+ * written.
+ *   logits, logits_dtype, ids, M, E, k   as for moe_balance_loss
+ *   weights      float[M, k], as moe_route_sort wrote them
+ * Asynchronous on `stream`; one launch (none for M == 0); allocates nothing.
+ */
+int moe_route_far_weights(const void* logits, int logits_dtype, const int32_t* ids, int M, int E, int k,
+                          float* weights, void* stream);
+
+/*
  * moe_router_backward -- grad_logits = d(total) / d(logits), where total has
  *   grad_loss as its derivative by the balance loss (counts are constants), and
  *   grad_w[t, j] as its derivative by the routing weights
