@@ -152,6 +152,9 @@ __global__ __launch_bounds__(kQThreads) void k_quantize(QArgs a) {
   }
 }
 
+// A launch has to have fewer than 2^32 threads, and each takes one group.
+constexpr int64_t kQLaunch = int64_t(1) << 31;  // groups of one launch, in whole rows
+
 template <int DT>
 const void* quant_kernel(bool values) {
   return values ? reinterpret_cast<const void*>(k_quantize<DT, true>)
@@ -745,17 +748,22 @@ extern "C" int moe_mxfp4_quantize(const void* x, int dtype, int64_t rows, int K,
   if (!aligned(x, size) || !aligned(codes, 4) || (values && !aligned(values, size))) return MRS_ERR_MISALIGNED;
   const int gpr = (K + 127) / 128 * 16;
   if (rows > (int64_t(1) << 38) / gpr) return MRS_ERR_OVERFLOW;
-  QArgs a{x, codes, scales, values, rows, row_stride, rows * gpr, K, gpr,
-          (uint32_t)(((uint64_t(1) << 32) + gpr - 1) / gpr), ~uint64_t(0) / gpr + 1};
-  const int64_t grid = (a.groups + kQThreads - 1) / kQThreads;
   const void* fn = dtype == MRS_DTYPE_F32    ? quant_kernel<MRS_DTYPE_F32>(values != nullptr)
                    : dtype == MRS_DTYPE_BF16 ? quant_kernel<MRS_DTYPE_BF16>(values != nullptr)
                                              : quant_kernel<MRS_DTYPE_F16>(values != nullptr);
-  void* params[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kQThreads), params, 0,
-                         reinterpret_cast<hipStream_t>(stream)) == hipSuccess
-             ? MRS_OK
-             : MRS_ERR_LAUNCH;
+  const int64_t most = kQLaunch / gpr;
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = rows - r < most ? rows - r : most;
+    QArgs a{static_cast<const char*>(x) + r * row_stride * size, codes + r * gpr * 4, scales + r * (gpr / 4),
+            values ? static_cast<char*>(values) + r * K * size : nullptr, n, row_stride, n * gpr, K, gpr,
+            (uint32_t)(((uint64_t(1) << 32) + gpr - 1) / gpr), ~uint64_t(0) / gpr + 1};
+    const int64_t grid = (a.groups + kQThreads - 1) / kQThreads;
+    void* params[] = {&a};
+    if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kQThreads), params, 0, reinterpret_cast<hipStream_t>(stream)) !=
+        hipSuccess)
+      return MRS_ERR_LAUNCH;
+  }
+  return MRS_OK;
 }
 
 extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,

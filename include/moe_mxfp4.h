@@ -41,8 +41,9 @@ enum { MRS_DTYPE_F16 = 2 };
  *   values      NULL, or [rows, K] contiguous of x's type (written): the values
  *               that codes and scales stand for (all exact in x's type); NaN in
  *               a block with X = 255
- * Asynchronous on `stream`; one launch (none for rows == 0); allocates nothing.
- * Returns MRS_OK or a negative MRS_ERR_* code before any launch;
+ * Asynchronous on `stream`; one launch for up to 2^31 groups of eight columns
+ * (rows * Kp / 8; none for rows == 0), one more for each further 2^31; allocates
+ * nothing.  Returns MRS_OK or a negative MRS_ERR_* code before any launch;
  * MRS_ERR_OVERFLOW when rows * Kp / 8 exceeds 2^38.
  */
 int moe_mxfp4_quantize(const void* x, int dtype, int64_t rows, int K, int64_t row_stride, uint8_t* codes,
