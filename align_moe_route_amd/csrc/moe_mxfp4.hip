@@ -795,7 +795,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
   } else {
     grid = (nrt + kXcds * shape.run - 1) / (kXcds * shape.run) * shape.run * kXcds * ntn;
   }
-  if (grid > INT32_MAX) return MRS_ERR_OVERFLOW;
+  if (grid * 256 > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   PArgs a{x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, y,
           M, k, E, K, N, block, x_rows == MRS_X_SORTED, (int)row_limit, (int)nrt, (int)ntn, shape.run,
           (int64_t)E * N * K / 2 > 256 << 20};

@@ -80,7 +80,9 @@ enum {
  * reaches every result that it takes part in and no padding row.  Rows of a
  * block whose expert id lies outside [0, E) are not written.
  * Asynchronous on `stream`; one launch; allocates nothing; num_post_pad is read
- * on the device.  Returns MRS_OK or a negative MRS_ERR_* code before any launch.
+ * on the device.  Returns MRS_OK or a negative MRS_ERR_* code before any launch;
+ * MRS_ERR_OVERFLOW where the rows pass 32 bits, or the tiles of a launch 2^24
+ * (16 to 128 rows x 256 columns: 2^28 rows or more of blocks of 16, N <= 256).
  */
 int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                            const uint8_t* w_scales, const int32_t* sorted_ids, const int32_t* expert_of_block,
