@@ -580,18 +580,16 @@ def _foreign(stream, dev):
     return None if stream.cuda_stream == _handle(None, dev) else stream
 
 
-def _allocate(foreign, dev, make):
-    """make()'s tensors, which a call on the stream `foreign` writes: out of that
-    stream's memory (a block that the current stream's work still reads is not
+def _allocate(foreign, dev, make, *args):
+    """make(*args), the tensors that a call on the stream `foreign` writes: out of
+    that stream's memory (a block that the current stream's work still reads is not
     written), and not given back before the current stream, where they go, is
     through with them."""
     import torch
-    if foreign is None:
-        return make()
     with torch.cuda.stream(foreign):
-        made = make()
+        made = make(*args)
     current = torch.cuda.current_stream(dev)
-    for t in made:
+    for t in made if isinstance(made, tuple) else (made,):
         t.record_stream(current)
     return made
 
@@ -636,6 +634,11 @@ def _check_mxfp4(q, dev, dims: int, name: str) -> int:
     return Kp
 
 
+def _new_mxfp4(lead, Kp: int, dev) -> MXFP4:
+    import torch
+    return MXFP4(_empty((*lead, Kp // 2), torch.uint8, dev), _empty((*lead, Kp // 32), torch.uint8, dev))
+
+
 def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) -> MXFP4:
     """Rows of x to 4-bit rows (moe_mxfp4_quantize).
 
@@ -677,8 +680,8 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     Kp = (K + 127) // 128 * 128
     foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = _allocate(foreign, dev, lambda: MXFP4(_empty((*lead, Kp // 2), torch.uint8, dev),
-                                                    _empty((*lead, Kp // 32), torch.uint8, dev)))
+        out = (_new_mxfp4(lead, Kp, dev) if foreign is None else
+               _allocate(foreign, dev, _new_mxfp4, lead, Kp, dev))
     else:
         _check_mxfp4(out, dev, x.dim(), "out")
         if out.codes.shape != (*lead, Kp // 2):
@@ -727,7 +730,8 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
     _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
     foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out, = _allocate(foreign, dev, lambda: (_empty((max(rows, 1), N), out_dtype or torch.bfloat16, dev),))
+        new = (max(rows, 1), N), out_dtype or torch.bfloat16, dev
+        out = _empty(*new) if foreign is None else _allocate(foreign, dev, _empty, *new)
     elif not (isinstance(out, torch.Tensor) and out.device == dev and out.is_contiguous() and out.dim() == 2
               and out.shape[1] == N and out.shape[0] >= rows and (out_dtype is None or out.dtype == out_dtype)):
         raise ValueError("out must be a contiguous [max_rows, N] tensor of out_dtype on x's device")
@@ -792,6 +796,16 @@ def balance_workspace_bytes(M: int, E: int, k: int, B: int = 1) -> int:
     return v
 
 
+def _new_balance(B: int, E: int, dev) -> BalanceOutput:
+    import torch
+    return BalanceOutput(_empty((1,), torch.float32, dev), _empty((B, E), torch.int32, dev),
+                         _empty((B + 1,), torch.int32, dev), _empty((B, E), torch.float32, dev))
+
+
+def _clones(*tensors):
+    return tuple(t.clone() for t in tensors)
+
+
 def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None, out: Optional[BalanceOutput] = None,
                  workspace=None, stream=None) -> BalanceOutput:
     """Balance loss, per-expert counts and mean scores of a routing
@@ -801,16 +815,19 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
     them (ids outside [0, E) are dropped routes).  seq_offsets: int32 [B + 1],
     the loss is the mean over the sequences; mask: bool or uint8 [M], zero for
     padding tokens.  workspace: as for route_sort (balance_workspace_bytes);
-    stream: as for mxfp4_quantize."""
+    stream: as for mxfp4_quantize.
+
+    Where logits require a gradient (and grad mode is on) the returned loss carries
+    it (router_backward; counts and ids are constants).  With `out` the returned
+    loss is another tensor on out.loss's memory, and only the returned one does."""
     import torch
     dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
     dev = logits.device
     nbytes = balance_workspace_bytes(M, E, k, B)
     foreign = None if stream is None else _foreign(stream, dev)
-    if out is None:
-        out = _allocate(foreign, dev, lambda: BalanceOutput(
-            _empty((1,), torch.float32, dev), _empty((B, E), torch.int32, dev),
-            _empty((B + 1,), torch.int32, dev), _empty((B, E), torch.float32, dev)))
+    given = out is not None
+    if not given:
+        out = _new_balance(B, E, dev) if foreign is None else _allocate(foreign, dev, _new_balance, B, E, dev)
     else:
         for t, dtype, shape, name in ((out.loss, torch.float32, (1,), "out.loss"),
                                       (out.counts, torch.int32, (B, E), "out.counts"),
@@ -832,7 +849,38 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
         _hold(foreign, logits, ids, seq_offsets, mask, *out, workspace)
     if rc != MRS_OK:
         raise RouteSortError(rc)
+    if logits.requires_grad and torch.is_grad_enabled():
+        loss, counts, tokens, _ = out
+        if given:  # the caller may write its buffers again before the backward pass
+            loss = loss.detach()
+            counts, tokens = (_clones(counts, tokens) if foreign is None else
+                              _allocate(foreign, dev, _clones, counts, tokens))
+        out = out._replace(loss=_balance_function().apply(logits, (loss,), ids, counts, tokens, float(coef), seq_offsets,
+                                                          mask))
     return out
+
+
+@functools.lru_cache(maxsize=1)
+def _balance_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Balance(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, box, ids, counts, tokens, coef, seq_offsets, mask):
+            ctx.save_for_backward(logits, ids, counts, tokens, seq_offsets, mask)
+            ctx.coef = coef
+            return box[0]  # in a tuple: as an argument of its own torch would return a view of it
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad_loss):
+            logits, ids, counts, tokens, seq_offsets, mask = ctx.saved_tensors
+            return (router_backward(logits, ids, balance=BalanceOutput(None, counts, tokens, None), coef=ctx.coef,
+                                    grad_loss=grad_loss.float().contiguous(), seq_offsets=seq_offsets, mask=mask),
+                    ) + (None,) * 7
+
+    return Balance
 
 
 def router_backward(logits, ids, *, grad_weights=None, balance: Optional[BalanceOutput] = None, coef: float = 1.0,
@@ -858,7 +906,7 @@ def router_backward(logits, ids, *, grad_weights=None, balance: Optional[Balance
         _check_tensor(grad_loss, dev, torch.float32, 1, "grad_loss")
     foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out, = _allocate(foreign, dev, lambda: (torch.empty_like(logits),))
+        out = torch.empty_like(logits) if foreign is None else _allocate(foreign, dev, torch.empty_like, logits)
     else:
         _check_tensor(out, dev, logits.dtype, M * E, "out")
         if out.shape != logits.shape:
