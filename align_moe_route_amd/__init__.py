@@ -646,7 +646,10 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     last dimension is consecutive and the leading ones collapse to rows of one
     stride (a slice of a wider buffer's columns is fine).
     values: optional contiguous tensor of x's shape and type that takes the
-    values the 4-bit rows stand for (for training with rounded values).
+    values the 4-bit rows stand for, for training with rounded values.  It is a
+    plain buffer: rounding has no slope, and x whose gradient it would drop is
+    refused in grad mode.  The gradient that passes the rounding by is
+        amr.mxfp4_quantize(x.detach(), values=v);  y = x + (v - x.detach())
     out: optional MXFP4 to write into, codes [..., Kp / 2], scales [..., Kp / 32].
     stream: the stream to run on, by default the current one; on another the
     caller orders it after what made the inputs and before what reads the results."""
@@ -690,6 +693,8 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
         _check_tensor(values, dev, x.dtype, x.numel(), "values")
         if values.shape != x.shape:
             raise ValueError("values must have x's shape")
+        if (x.requires_grad or values.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("values carries no gradient: quantise x.detach(), and use x + (values - x.detach())")
     handle = _handle(stream, dev)
     rc = int(lib().moe_mxfp4_quantize(x.data_ptr(), dts[x.dtype], rows, K, row_stride, out.codes.data_ptr(),
                                       out.scales.data_ptr(), values.data_ptr() if values is not None else None,
