@@ -34,6 +34,8 @@ MRS_X_SORTED = 1
 FLAG_FORCE_SINGLE_WG = 1
 FLAG_FORCE_MULTI_WG = 2
 FLAG_FORCE_EXACT = 4
+PRODUCT_BY_RULE, PRODUCT_ROWS_16, PRODUCT_ROWS_32 = 0, 1, 2
+PRODUCT_TILE_16, PRODUCT_TILE_32, PRODUCT_TILE_64, PRODUCT_TILE_128 = 3, 4, 5, 6
 
 EXPORTED = [
     "moe_route_sort",
@@ -54,6 +56,7 @@ EXPORTED = [
     "moe_gate_route_sort",
     "moe_mxfp4_quantize",
     "moe_grouped_gemm_mxfp4",
+    "moe_grouped_gemm_mxfp4_ex",
     "moe_balance_workspace_bytes",
     "moe_balance_loss",
     "moe_route_far_weights",
@@ -116,6 +119,8 @@ def lib() -> ctypes.CDLL:
     L.moe_mxfp4_quantize.restype = i32
     L.moe_grouped_gemm_mxfp4.argtypes = [vp] * 7 + [i32] * 8 + [vp, vp]
     L.moe_grouped_gemm_mxfp4.restype = i32
+    L.moe_grouped_gemm_mxfp4_ex.argtypes = L.moe_grouped_gemm_mxfp4.argtypes + [i32]
+    L.moe_grouped_gemm_mxfp4_ex.restype = i32
     L.moe_balance_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.moe_balance_workspace_bytes.restype = sz
     L.moe_balance_loss.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]
@@ -707,7 +712,8 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
 
 
 def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post_pad, k: int, block: int, *,
-                       tokens: Optional[int] = None, out_dtype=None, out=None, stream=None):
+                       tokens: Optional[int] = None, out_dtype=None, out=None, stream=None,
+                       kernel: int = PRODUCT_BY_RULE):
     """Grouped product of 4-bit rows over the route-sort metadata
     (moe_grouped_gemm_mxfp4): y[r] = x[row(r)] . W[expert_of_block[r // block]]^T
     for sorted rows below num_post_pad, zeros for padding rows.
@@ -717,7 +723,8 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
     on the rows an earlier one wrote).  w: 4-bit rows [E, N].  block: a multiple
     of 16.  out_dtype: bfloat16 (default) or float32.  Returns y [max_rows, N];
     rows at or past num_post_pad are left as they were.  stream: as for
-    mxfp4_quantize."""
+    mxfp4_quantize.  kernel: a PRODUCT_* constant in place of the choice by sizes
+    (moe_grouped_gemm_mxfp4_ex; for tests and tuning)."""
     import torch
     if not (isinstance(x, MXFP4) and isinstance(x.codes, torch.Tensor) and x.codes.is_cuda):
         raise ValueError("x must be an MXFP4 of GPU tensors")
@@ -743,11 +750,11 @@ def grouped_gemm_mxfp4(x: MXFP4, w: MXFP4, sorted_ids, expert_of_block, num_post
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise NotImplementedError(f"y dtype {out.dtype} (bfloat16 or float32 only)")
     handle = _handle(stream, dev)
-    rc = int(lib().moe_grouped_gemm_mxfp4(
+    rc = int(lib().moe_grouped_gemm_mxfp4_ex(
         x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), sorted_ids.data_ptr(),
         expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, Kp, N, block,
         MRS_X_TOKENS if tokens is None else MRS_X_SORTED,
-        MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), handle))
+        MRS_DTYPE_BF16 if out.dtype == torch.bfloat16 else MRS_DTYPE_F32, out.data_ptr(), handle, kernel))
     if foreign is not None:
         _hold(foreign, *x, *w, sorted_ids, expert_of_block, num_post_pad, out)
     if rc != MRS_OK:

@@ -721,12 +721,23 @@ const void* product_kernel(int bm, int bn) {
 struct Shape {
   int bm, bn, run;
 };
-Shape shape_of(int64_t routes, int64_t used, int K, int N, int block) {
+// `kernel`: one that the caller names in place of the rule's (run by the rule).
+Shape shape_of(int64_t routes, int64_t used, int K, int N, int block, int kernel) {
   const int64_t cols = (N + kCols - 1) / kCols, strips = used * cols;
-  if (strips < 192 && strips * routes <= 768 * used && strips * (block / 16) <= 160 + K / 16)
-    return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32, 1};
-  int bm = block % 128 == 0 && routes > 48 * used ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
-  while (strips < 192 && bm > 32 && routes / bm * cols < 128) bm /= 2;
+  int bm;
+  switch (kernel) {
+    case MRS_PRODUCT_ROWS_16: return {16, 16, 1};
+    case MRS_PRODUCT_ROWS_32: return {16, 32, 1};
+    case MRS_PRODUCT_TILE_16: bm = 16; break;
+    case MRS_PRODUCT_TILE_32: bm = 32; break;
+    case MRS_PRODUCT_TILE_64: bm = 64; break;
+    case MRS_PRODUCT_TILE_128: bm = 128; break;
+    default:
+      if (strips < 192 && strips * routes <= 768 * used && strips * (block / 16) <= 160 + K / 16)
+        return {16, used * ((N + 31) / 32) < kRowsNarrow ? 16 : 32, 1};
+      bm = block % 128 == 0 && routes > 48 * used ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
+      while (strips < 192 && bm > 32 && routes / bm * cols < 128) bm /= 2;
+  }
   const int64_t tiles = routes / bm + used / 2;  // an expert's last tile is half full
   int run = 1;
   while (run < 16 && run * 128 <= tiles) run *= 2;
@@ -771,9 +782,19 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
                                       const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k,
                                       int E, int K, int N, int block, int x_rows, int y_dtype, void* y,
                                       void* stream) {
+  return moe_grouped_gemm_mxfp4_ex(x_codes, x_scales, w_codes, w_scales, sorted_ids, expert_of_block, num_post_pad, M,
+                                   k, E, K, N, block, x_rows, y_dtype, y, stream, MRS_PRODUCT_BY_RULE);
+}
+
+extern "C" int moe_grouped_gemm_mxfp4_ex(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                                         const uint8_t* w_scales, const int32_t* sorted_ids,
+                                         const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k,
+                                         int E, int K, int N, int block, int x_rows, int y_dtype, void* y,
+                                         void* stream, int kernel) {
   if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K <= 0 || K > (1 << 22) || K % 128 != 0 || N < 1 || block < 16 ||
       block % 16 != 0 || (x_rows != MRS_X_TOKENS && x_rows != MRS_X_SORTED) ||
-      (y_dtype != MRS_DTYPE_BF16 && y_dtype != MRS_DTYPE_F32))
+      (y_dtype != MRS_DTYPE_BF16 && y_dtype != MRS_DTYPE_F32) || kernel < MRS_PRODUCT_BY_RULE ||
+      kernel > MRS_PRODUCT_TILE_128 || (kernel >= MRS_PRODUCT_TILE_16 && block % (16 << (kernel - MRS_PRODUCT_TILE_16))))
     return MRS_ERR_INVALID_ARG;
   const int64_t max_rows = moe_route_sort_max_rows(M, E, k, block);
   if (max_rows < 0) return MRS_ERR_OVERFLOW;
@@ -785,7 +806,7 @@ extern "C" int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_s
       !aligned(sorted_ids, 4) || !aligned(expert_of_block, 4) || !aligned(num_post_pad, 4) || !aligned(y, 4))
     return MRS_ERR_MISALIGNED;
   const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E;
-  const Shape shape = shape_of(routes, used, K, N, block);
+  const Shape shape = shape_of(routes, used, K, N, block, kernel);
   const int bm = shape.bm, bn = shape.bn;
   const int64_t nrt = row_limit / bm, ntn = ((int64_t)N + bn - 1) / bn;
   int64_t grid;

@@ -89,6 +89,25 @@ int moe_grouped_gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
                            const int32_t* num_post_pad, int M, int k, int E, int K, int N, int block, int x_rows,
                            int y_dtype, void* y, void* stream);
 
+/* Kernels of the product, for tests and tuning; each computes the same rows of y
+ * (sums in another order). */
+enum {
+  MRS_PRODUCT_BY_RULE = 0, /* as moe_grouped_gemm_mxfp4 chooses by the sizes   */
+  MRS_PRODUCT_ROWS_16 = 1, /* tiles of 16 rows x 16 columns                    */
+  MRS_PRODUCT_ROWS_32 = 2, /* tiles of 16 rows x 32 columns                    */
+  MRS_PRODUCT_TILE_16 = 3, /* tiles of 16 rows x 256 columns, and so on; the   */
+  MRS_PRODUCT_TILE_32 = 4, /* rows have to divide block                        */
+  MRS_PRODUCT_TILE_64 = 5,
+  MRS_PRODUCT_TILE_128 = 6
+};
+
+/* moe_grouped_gemm_mxfp4 by a kernel that the caller names
+ * (MRS_ERR_INVALID_ARG where its rows do not divide block). */
+int moe_grouped_gemm_mxfp4_ex(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                              const uint8_t* w_scales, const int32_t* sorted_ids, const int32_t* expert_of_block,
+                              const int32_t* num_post_pad, int M, int k, int E, int K, int N, int block, int x_rows,
+                              int y_dtype, void* y, void* stream, int kernel);
+
 #ifdef __cplusplus
 }
 #endif
