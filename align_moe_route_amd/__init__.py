@@ -639,9 +639,8 @@ def _check_mxfp4(q, dev, dims: int, name: str) -> int:
     return Kp
 
 
-def _new_mxfp4(lead, Kp: int, dev) -> MXFP4:
-    import torch
-    return MXFP4(_empty((*lead, Kp // 2), torch.uint8, dev), _empty((*lead, Kp // 32), torch.uint8, dev))
+def _new_mxfp4(lead, Kp: int, u8, dev) -> MXFP4:
+    return MXFP4(_empty((*lead, Kp // 2), u8, dev), _empty((*lead, Kp // 32), u8, dev))
 
 
 def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) -> MXFP4:
@@ -688,8 +687,8 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     Kp = (K + 127) // 128 * 128
     foreign = None if stream is None else _foreign(stream, dev)
     if out is None:
-        out = (_new_mxfp4(lead, Kp, dev) if foreign is None else
-               _allocate(foreign, dev, _new_mxfp4, lead, Kp, dev))
+        out = (_new_mxfp4(lead, Kp, torch.uint8, dev) if foreign is None else
+               _allocate(foreign, dev, _new_mxfp4, lead, Kp, torch.uint8, dev))
     else:
         _check_mxfp4(out, dev, x.dim(), "out")
         if out.codes.shape != (*lead, Kp // 2):
@@ -808,10 +807,9 @@ def balance_workspace_bytes(M: int, E: int, k: int, B: int = 1) -> int:
     return v
 
 
-def _new_balance(B: int, E: int, dev) -> BalanceOutput:
-    import torch
-    return BalanceOutput(_empty((1,), torch.float32, dev), _empty((B, E), torch.int32, dev),
-                         _empty((B + 1,), torch.int32, dev), _empty((B, E), torch.float32, dev))
+def _new_balance(B: int, E: int, f32, i32, dev) -> BalanceOutput:
+    return BalanceOutput(_empty((1,), f32, dev), _empty((B, E), i32, dev), _empty((B + 1,), i32, dev),
+                         _empty((B, E), f32, dev))
 
 
 def _clones(*tensors):
@@ -831,7 +829,8 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
 
     Where logits require a gradient (and grad mode is on) the returned loss carries
     it (router_backward; counts and ids are constants).  With `out` the returned
-    loss is another tensor on out.loss's memory, and only the returned one does."""
+    loss is another tensor on out.loss's memory, and only the returned one does.
+    A captured training step calls router_backward itself (as for route_sort_train)."""
     import torch
     dt, M, E, k, B = _check_router(logits, ids, seq_offsets, mask)
     dev = logits.device
@@ -839,7 +838,8 @@ def balance_loss(logits, ids, coef: float = 1.0, *, seq_offsets=None, mask=None,
     foreign = None if stream is None else _foreign(stream, dev)
     given = out is not None
     if not given:
-        out = _new_balance(B, E, dev) if foreign is None else _allocate(foreign, dev, _new_balance, B, E, dev)
+        new = B, E, torch.float32, torch.int32, dev
+        out = _new_balance(*new) if foreign is None else _allocate(foreign, dev, _new_balance, *new)
     else:
         for t, dtype, shape, name in ((out.loss, torch.float32, (1,), "out.loss"),
                                       (out.counts, torch.int32, (B, E), "out.counts"),

@@ -12,12 +12,15 @@
 // from the same pass, and the picks' gradient joins in FP32 before the one
 // rounding.
 //
-// Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s):
+// Bound by the logits' bytes where there are many (a 2 GiB copy moves 4.9 TB/s).
+// With the same inputs call after call, which the 256 MB cache keeps in part:
 // forward 16384 x 4096 FP32, 37 sequences, in 60 us (276 MB, 4.6 TB/s; the pieces
 // add 37 MB and two small launches 11 us), 65536 x 512 FP32 in 30 us; backward 99
-// and 47 us (541 and 273 MB, 5.5 and 5.8 TB/s).  8192 x 896 BF16 takes 15.5 us
-// forward, 8 of them the second launch's chain of round trips, and 11.5 us backward
-// (30 MB; 6 us of arithmetic, the rest latency); 131072 x 128 BF16 20 and 24 us.
+// and 46 us (541 and 273 MB, 5.5 and 5.9 TB/s).  With other inputs each time the
+// first of them takes 68 us forward and 112 backward (4.0 and 4.8 TB/s).
+// 8192 x 896 BF16 takes 15.5 us forward, 8 of them the second launch's chain of
+// round trips, and 11 us backward (30 MB; 6 us of arithmetic, the rest latency);
+// 131072 x 128 BF16 20 and 22 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -130,9 +133,9 @@ struct Row<MRS_DTYPE_BF16> {
   static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
 
-// A workgroup has 256 threads, of which G share a row; a thread has NI times four
-// columns, at (i G + its place in the group) * 4.
-constexpr int kThreads = 256;
+// G threads of a workgroup share a row; a thread has NI times four columns, at
+// (i G + its place in the group) * 4.
+constexpr int kThreads = 256;  // of a workgroup, but for the forward pass (part_threads)
 
 // Four columns from c of a row of E, as stored; columns past E read as -infinity,
 // whose score is zero.  Rows need no more alignment than their elements.
@@ -289,13 +292,13 @@ __host__ __device__ constexpr int part_threads(int G) { return G < 256 ? 512 : 2
 template <int DT, int G, int NI, bool SINGLE>
 __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
   typedef typename Row<DT>::T T;
-  constexpr int kThreads = part_threads(G), kGroups = kThreads / G, R = kPartRows;
+  constexpr int kWork = part_threads(G), kGroups = kWork / G, R = kPartRows;
   constexpr int kSeg = G < 64 ? G : 64;
   extern __shared__ int32_t hist[];                     // [E]
   float* share = reinterpret_cast<float*>(hist + a.E);  // [kGroups][E]
   __shared__ float box[2][G > 64 ? G / 64 * R : 1], far_box[4];
   __shared__ int live_tokens;
-  __shared__ double loss_part[kThreads / 64];
+  __shared__ double loss_part[kWork / 64];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = G == 64 ? wv : tid / G, c0 = tid % G * 4;
   const int c = blockIdx.x;
@@ -319,10 +322,10 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
                                   i < NI - 1);
     };
     if (t1 > t0) fetch(t0 + grp * R);  // on their way while the ids are counted
-    for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
+    for (int e = tid; e < a.E; e += kWork) hist[e] = 0;
     if (tid == 0) live_tokens = 0;
     __syncthreads();
-    for (int i = tid; i < (t1 - t0) * a.k; i += kThreads) {
+    for (int i = tid; i < (t1 - t0) * a.k; i += kWork) {
       const int id = a.ids[(size_t)t0 * a.k + i], mask = a.mask ? a.mask[t0 + i / a.k] : 1;
       if (id >= 0 && id < a.E && mask) atomicAdd(&hist[id], 1);
     }
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
       return v;
     };
     if constexpr (SINGLE) {
-      for (int e = tid; e < a.E; e += kThreads) {
+      for (int e = tid; e < a.E; e += kWork) {
         const double mean = n > 0 ? (double)sum(e) / n : 0.0;
         a.counts[(size_t)b * a.E + e] = hist[e];
         a.shares[(size_t)b * a.E + e] = (float)mean;
@@ -400,7 +403,7 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
       if (tid == 0) a.tokens[b] = n;
     } else {
       const size_t piece = (size_t)(c + b) * a.E;
-      for (int e = tid; e < a.E; e += kThreads) {
+      for (int e = tid; e < a.E; e += kWork) {
         a.ws_share[piece + e] = sum(e);
         a.ws_count[piece + e] = hist[e];
       }
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(part_threads(G)) void k_balance_part(BArgs a) {
     __syncthreads();
     if (tid == 0) {
       loss = loss_part[0];
-      for (int w = 1; w < kThreads / 64; ++w) loss += loss_part[w];
+      for (int w = 1; w < kWork / 64; ++w) loss += loss_part[w];
       a.loss[0] = loss_of(a, loss, filled);
       a.tokens[a.B] = filled;
     }

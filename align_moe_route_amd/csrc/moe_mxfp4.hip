@@ -707,7 +707,11 @@ const void* product_kernel(int bm, int bn) {
 // 117 / 165 / 220), but none of 128 for fewer than 48 rows, of which most of the steps'
 // loads would be padding's (16 rows 97 / 87 / 91; blocks of 256 107 / 100 / 98), and
 // smaller ones where 128 workgroups would not come together (8 experts, 512 tokens:
-// tiles of 32 8.2 us, 64 10.2, 128 14.1).
+// tiles of 32 8.2 us, 64 10.2, 128 14.1).  With 128 to 255 workgroups of the chosen tile the
+// next smaller one is still 1 to 42 % faster, from 256 on they are level (us, tiles of 32
+// / 64 / 128; 2 experts, K = 3584, N = 2048: 512 rows each 18.1 / 21.5 / 29.6, 1024 rows 24.4 /
+// 22.1 / 30.8, 2048 rows 43.8 / 31.5 / 32.4; 24 experts, K = 1024, N = 396, 341 rows each 16.2 /
+// 13.4 / 15.2; 64 experts, K = 3584, N = 396, 256 rows each 56.1 / 49.5 / 44.1).
 //
 // Runs of row tiles: eight or more for each XCD, so that none has much more than
 // another (us with runs of 8 / with this rule: 2048 tokens, 64 experts, top-8 45.5 /

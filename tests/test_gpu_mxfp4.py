@@ -127,7 +127,7 @@ def run_product(rng, M, E, k, K, N, block, dtype, in_order, drop=0.0, skew=0.0, 
     return got[:npp], ref, ab
 
 
-SHAPES = [  # M, E, k, K, N, block, drop, skew
+SHAPES = [  # M, E, k, K, N, block, drop, skew; the kernel is chosen by the sizes
     (1, 8, 2, 128, 16, 16, 0, 0),
     (1, 32, 16, 3584, 768, 32, 0, 0),
     (3, 8, 8, 256, 17, 16, 0, 0),
@@ -142,19 +142,19 @@ SHAPES = [  # M, E, k, K, N, block, drop, skew
     (400, 5, 3, 33, 31, 96, 0, 0),
     (90, 6, 2, 2000, 70, 32, 1.0, 0),   # every route dropped
     (611, 1, 1, 256, 48, 128, 0, 0),
-    (400, 3, 1, 2200, 72, 128, 0, 0),   # more than eight steps of 256: scales staged again
+    (400, 3, 1, 2200, 72, 128, 0, 0),   # long rows, to the few-rows kernel as well
     (150, 3, 1, 4500, 40, 64, 0, 0),
     (70, 2, 1, 6200, 264, 32, 0, 0.5),
     (9, 3, 1, 9000, 33, 48, 0, 0),
-    # many experts with few rows: whole strips of weights, tiles of 16 to 128 rows
+    # many experts with few rows: whole strips of weights, tiles of 16 and 64 rows
     # most of which are padding
     (70, 200, 2, 256, 40, 16, 0.1, 0),
     (70, 200, 2, 384, 264, 48, 0, 0),
     (90, 220, 3, 128, 24, 64, 0.5, 0),
     (60, 250, 4, 300, 270, 128, 0.2, 0.5),
     (100, 130, 2, 640, 300, 256, 0, 0),
-    (2, 60, 20, 700, 80, 16, 0, 0),     # 32-column tiles of the few-rows kernel
-    (2, 90, 40, 520, 200, 32, 0, 0),
+    (2, 60, 20, 700, 80, 16, 0, 0),
+    (2, 90, 40, 520, 200, 32, 0, 0),    # 32-column tiles of the few-rows kernel
 ]
 
 
@@ -263,7 +263,7 @@ def test_offsets_past_32_bits():
     ws = torch.randint(124, 131, (E, N, K // 32), dtype=torch.uint8, device="cuda", generator=g)
     rng = np.random.default_rng(2)
     xc, xs = random_rows(rng, (M,), K)
-    for block in (16, 64):  # the few-rows and the tile kernel
+    for block in (16, 64):  # both by the few-rows kernel
         ids = np.stack([np.sort(rng.choice(np.arange(E - (20 if block == 16 else 4), E), k, replace=False))
                         for _ in range(M)]).astype(np.int32)
         out = amr.sort_from_ids(torch.from_numpy(ids).cuda(), E, block)
