@@ -31,6 +31,9 @@ MRS_DTYPE_BF16 = 1
 MRS_DTYPE_F16 = 2
 MRS_X_TOKENS = 0
 MRS_X_SORTED = 1
+MRS_INT4_PLAIN = 0
+MRS_INT4_GATED = 1
+MRS_INT4_SUM = 2
 FLAG_FORCE_SINGLE_WG = 1
 FLAG_FORCE_MULTI_WG = 2
 FLAG_FORCE_EXACT = 4
@@ -61,6 +64,16 @@ EXPORTED = [
     "moe_balance_loss",
     "moe_route_far_weights",
     "moe_router_backward",
+    "moe_grouped_gemm",
+    "moe_grouped_gemm_dx",
+    "moe_grouped_gemm_dw",
+    "moe_swiglu",
+    "moe_swiglu_backward",
+    "moe_slot_rows",
+    "moe_combine",
+    "moe_combine_backward",
+    "moe_int4_quantize",
+    "moe_int4_matvec",
 ]
 
 _lib = None
@@ -129,6 +142,26 @@ def lib() -> ctypes.CDLL:
     L.moe_route_far_weights.restype = i32
     L.moe_router_backward.argtypes = [vp, i32] + [vp] * 7 + [i32] * 4 + [f32, vp, vp]
     L.moe_router_backward.restype = i32
+    L.moe_grouped_gemm.argtypes = [vp, vp, i32, vp, vp, vp] + [i32] * 8 + [vp, vp]
+    L.moe_grouped_gemm.restype = i32
+    L.moe_grouped_gemm_dx.argtypes = [vp, vp, i32, vp, vp, vp] + [i32] * 7 + [vp, vp]
+    L.moe_grouped_gemm_dx.restype = i32
+    L.moe_grouped_gemm_dw.argtypes = L.moe_grouped_gemm.argtypes
+    L.moe_grouped_gemm_dw.restype = i32
+    L.moe_swiglu.argtypes = [vp, i32, vp, i64, i32, vp, vp]
+    L.moe_swiglu.restype = i32
+    L.moe_swiglu_backward.argtypes = [vp, vp, i32, vp, i64, i32, vp, vp]
+    L.moe_swiglu_backward.restype = i32
+    L.moe_slot_rows.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+    L.moe_slot_rows.restype = i32
+    L.moe_combine.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, i32, vp, vp]
+    L.moe_combine.restype = i32
+    L.moe_combine_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp]
+    L.moe_combine_backward.restype = i32
+    L.moe_int4_quantize.argtypes = [vp, i32, i64, i32, i64, i32, i32, vp, vp, vp]
+    L.moe_int4_quantize.restype = i32
+    L.moe_int4_matvec.argtypes = [vp, i32, vp, vp, vp, vp] + [i32] * 8 + [vp, vp]
+    L.moe_int4_matvec.restype = i32
     _lib = L
     return L
 
@@ -643,6 +676,28 @@ def _new_mxfp4(lead, Kp: int, u8, dev) -> MXFP4:
     return MXFP4(_empty((*lead, Kp // 2), u8, dev), _empty((*lead, Kp // 32), u8, dev))
 
 
+def _row_stride(x, K: int) -> int:
+    """The stride of x's rows of K consecutive values, leading dimensions collapsed."""
+    if x.numel() == 0 or x.is_contiguous():
+        return K
+    if K > 1 and x.stride(-1) != 1:
+        raise ValueError("x's last dimension must be consecutive")
+    step = None  # stride of the rows, from the innermost leading dimension outwards
+    span = 1
+    for n, st in zip(x.shape[-2::-1], x.stride()[-2::-1]):
+        if n == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != step * span:
+            raise ValueError("x's leading dimensions must collapse to rows of one stride")
+        span *= n
+    row_stride = K if step is None else step
+    if row_stride < K:
+        raise ValueError("x's rows must not overlap")
+    return row_stride
+
+
 def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) -> MXFP4:
     """Rows of x to 4-bit rows (moe_mxfp4_quantize).
 
@@ -666,23 +721,7 @@ def mxfp4_quantize(x, *, values=None, out: Optional[MXFP4] = None, stream=None) 
     *lead, K = x.shape
     if not 1 <= K <= 262144:
         raise ValueError("the last dimension must hold 1 to 262144 values")
-    rows, row_stride = x.numel() // K, K
-    if rows and not x.is_contiguous():
-        if K > 1 and x.stride(-1) != 1:
-            raise ValueError("x's last dimension must be consecutive")
-        step = None  # stride of the rows, from the innermost leading dimension outwards
-        span = 1
-        for n, st in zip(lead[::-1], x.stride()[-2::-1]):
-            if n == 1:
-                continue
-            if step is None:
-                step = st
-            elif st != step * span:
-                raise ValueError("x's leading dimensions must collapse to rows of one stride")
-            span *= n
-        row_stride = K if step is None else step
-        if row_stride < K:
-            raise ValueError("x's rows must not overlap")
+    rows, row_stride = x.numel() // K, _row_stride(x, K)
     dev = x.device
     Kp = (K + 127) // 128 * 128
     foreign = None if stream is None else _foreign(stream, dev)
@@ -991,3 +1030,7 @@ def route_sort_train(logits, bias, k: int, n_group: int, topk_group: int, block:
     w, loss, ids, sid, eob, npp, counts, tokens, shares = _route_train_function().apply(
         logits, bias, (k, n_group, topk_group, block), float(balance_coef), seq_offsets, mask)
     return RouteSortOutput(ids, w, sid, eob, npp), BalanceOutput(loss, counts, tokens, shares)
+
+
+from .experts import (Int4, combine, combine_backward, experts_train, grouped_gemm, grouped_gemm_dw,  # noqa: E402,F401
+                      grouped_gemm_dx, int4_matvec, int4_quantize, slot_rows, swiglu, swiglu_backward)

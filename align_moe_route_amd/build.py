@@ -7,7 +7,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route_sort.hip", "moe_gemm1.hip", "moe_gate.hip",
-                                                  "moe_mxfp4.hip", "moe_balance.hip")]
+                                                  "moe_mxfp4.hip", "moe_balance.hip", "moe_experts.hip",
+                                                  "moe_mix.hip", "moe_int4.hip")]
 OUT = os.path.join(HERE, "libmoe_route_sort.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

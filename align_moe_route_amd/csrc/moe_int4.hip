@@ -1,0 +1,324 @@
+// 4-bit weights with group scales and the matrix-vector products of routed tokens,
+// MI355X (gfx950, CDNA4, wave64).  Definitions: include/moe_int4.h.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "half.h"
+#include "moe_int4.h"
+#include "moe_route_sort.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------ quantisation
+//
+// A thread takes eight consecutive columns, so 4, 8 or 16 neighbouring lanes hold
+// a group; its largest magnitude is the integer maximum of the bit patterns (which
+// orders infinities and NaN above every number) over those lanes.
+
+struct QArgs {
+  const void* w;
+  uint8_t* codes;
+  uint16_t* scales;
+  int64_t rows, stride;
+  int K, gpr;          // gpr: eights of columns a row, Kp / 8
+  uint32_t gpr_mul;    // ceil(2^32 / gpr): exact below 2^16, gpr <= 2^15
+  uint64_t gpr_mul64;  // floor(2^64 / gpr) + 1: exact below 2^49
+};
+
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v, uint32_t o) { return max(v, o); }
+
+// Largest value of 4, 8 or 16 neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = dpp_max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));  // quad_perm [1,0,3,2]
+  v = dpp_max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // quad_perm [2,3,0,1]
+  if (LANES >= 8) v = dpp_max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));  // half mirror
+  if (LANES >= 16) v = dpp_max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ float value(const void* p, int64_t i) {
+  if constexpr (DT == MRS_DTYPE_F32) return static_cast<const float*>(p)[i];
+  else if constexpr (DT == MRS_DTYPE_BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  else return (float)static_cast<const _Float16*>(p)[i];
+}
+
+template <int DT, typename S, int GROUP>
+__global__ __launch_bounds__(kThreads) void k_quantize(QArgs a) {
+  const int64_t g0 = (int64_t)blockIdx.x * kThreads;
+  const int64_t row0 = (int64_t)__umul64hi((uint64_t)g0, a.gpr_mul64);  // g0 / gpr
+  const uint32_t in = (uint32_t)(g0 - row0 * a.gpr) + threadIdx.x;
+  const uint32_t dr = __umulhi(in, a.gpr_mul);  // in / gpr
+  const int64_t row = row0 + dr;
+  const int g = (int)(in - dr * (uint32_t)a.gpr), c0 = g * 8;
+  const bool live = row < a.rows;  // the same for the lanes of a group: gpr is a multiple of 16
+  float v[8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = live && c0 + i < a.K ? value<DT>(a.w, row * a.stride + c0 + i) : 0.0f;
+    top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  }
+  top = lanes_max<GROUP / 8>(top);
+  const uint32_t packed = S::pack(__uint_as_float(top) / 7.0f, 0.0f);  // the scale, in the low half
+  const float scale = S::lo(packed);
+  const bool bad = !(scale < __uint_as_float(0x7F800000u));  // an infinity or a NaN
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = bad || scale == 0.0f ? 0.0f : fminf(fmaxf(rintf(v[i] / scale), -7.0f), 7.0f);
+    code |= (uint32_t)((int)q + 8) << (4 * i);
+  }
+  if (!live) return;
+  reinterpret_cast<uint32_t*>(a.codes)[row * a.gpr + g] = code;
+  if (g % (GROUP / 8) == 0)
+    a.scales[(row * a.gpr + g) / (GROUP / 8)] =
+        bad ? (uint16_t)S::pack(__uint_as_float(0x7FC00000u), 0.0f) : (uint16_t)packed;
+}
+
+template <int DT, typename S>
+const void* quant_kernel(int group) {
+  return group == 32   ? reinterpret_cast<const void*>(k_quantize<DT, S, 32>)
+         : group == 64 ? reinterpret_cast<const void*>(k_quantize<DT, S, 64>)
+                       : reinterpret_cast<const void*>(k_quantize<DT, S, 128>);
+}
+
+template <typename S>
+const void* quant_kernel(int dtype, int group) {
+  return dtype == MRS_DTYPE_F32    ? quant_kernel<MRS_DTYPE_F32, S>(group)
+         : dtype == MRS_DTYPE_BF16 ? quant_kernel<MRS_DTYPE_BF16, S>(group)
+                                   : quant_kernel<MRS_DTYPE_F16, S>(group);
+}
+
+// A launch has to have fewer than 2^32 threads, and each takes one group of eight.
+constexpr int64_t kQLaunch = int64_t(1) << 31;
+
+// ---------------------------------------------------------- matrix-vector
+//
+// A lane takes chunks of 32 columns (16 bytes of codes): chunk q of the unit's
+// contraction, the columns of one slot or (sum) those of a token's picks one after
+// another.  L lanes share a row, so a wave works on 64 / L rows at once and R of
+// such sets; it keeps its x values in registers and loads R sets of codes at a
+// time.  A code c is made a 16-bit float by putting it into the top of the
+// mantissa of 16.0: the value 16 + c costs one shift and one and-or for two codes,
+// v_dot2 multiplies pairs into FP32, and 24 times the sum of x is taken off per
+// chunk: sum x (16 + c) - 24 sum x = sum x (c - 8).  Scale and pick weight enter
+// once a chunk.  The low and high half of a dword's pair hold codes i and i + 4, so
+// x is paired alike.
+
+struct MArgs {
+  const uint16_t* x;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const int32_t* ids;
+  const float* v;
+  uint16_t* y;
+  int M, k, E, K, N, per_slot;
+  int chunks;   // of a row: Kp / 32
+  int out;      // outputs of a slot: N, or N / 2 for gated results
+  int tiles;    // workgroups of a slot (of a token for sums)
+  uint32_t chunks_mul;  // ceil(2^32 / chunks)
+};
+
+template <typename H>
+struct Magic;
+template <>
+struct Magic<BF16> {  // 7 bits of mantissa: 16 + c = 0x4180 | c << 3
+  static constexpr uint32_t base = 0x41804180u, mask = 0x00780078u;
+  static constexpr int at = 3;
+  static constexpr uint32_t ones = 0x3F803F80u;
+};
+template <>
+struct Magic<FP16> {  // 10 bits: 16 + c = 0x4C00 | c << 6
+  static constexpr uint32_t base = 0x4C004C00u, mask = 0x03C003C0u;
+  static constexpr int at = 6;
+  static constexpr uint32_t ones = 0x3C003C00u;
+};
+
+// codes i and i + 4 of a dword as 16 + c
+template <typename H>
+__device__ __forceinline__ uint32_t pair_of(uint32_t q, int i) {
+  typedef Magic<H> G;
+  const int up = G::at - 4 * i;
+  return ((up >= 0 ? q << up : q >> -up) & G::mask) | G::base;
+}
+
+template <typename H, int MODE, int GROUP, int L, int R>
+__global__ __launch_bounds__(kThreads) void k_matvec(MArgs a) {
+  constexpr int kSets = 64 / L;  // rows a wave works on at once
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+  const int q0 = lane % L, sub = lane / L;
+  // gated: half of a wave's row sets are gates, the other half the columns they gate
+  constexpr int kOut = MODE == MRS_INT4_GATED ? R / 2 : R;  // outputs of a lane's row sets
+  const int n0 = (tile * (kThreads / 64) + wv) * kOut * kSets;
+  if (n0 >= a.out) return;
+  const int total = MODE == MRS_INT4_SUM ? a.k * a.chunks : a.chunks;
+  int e = 0;
+  if constexpr (MODE != MRS_INT4_SUM) {
+    e = a.ids[unit];
+    if (e < 0 || e >= a.E) {
+      for (int o = lane; o < kOut * kSets; o += 64)
+        if (n0 + o < a.out) a.y[(int64_t)unit * a.out + n0 + o] = 0;
+      return;
+    }
+  }
+  int row[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int n = n0 + (r % kOut) * kSets + sub;
+    row[r] = min(n, a.out - 1) + (r >= kOut ? a.out : 0);
+  }
+  float acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+  for (int q = q0; q < total; q += L) {
+    int64_t slot = unit;
+    int c = q;
+    float v = 1.0f;
+    bool ok = true;
+    if constexpr (MODE == MRS_INT4_SUM) {
+      const int j = (int)__umulhi((uint32_t)q, a.chunks_mul);  // q / chunks
+      c = q - j * a.chunks;
+      slot = (int64_t)unit * a.k + j;
+      e = a.ids[slot];
+      v = a.v[slot];
+      ok = e >= 0 && e < a.E;
+      e = ok ? e : 0;
+    }
+    const int64_t xr = MODE == MRS_INT4_SUM ? (a.per_slot ? slot : unit) : (a.per_slot ? slot : slot / a.k);
+    u32x4 w[R];
+    float sc[R];
+    const int64_t at = (int64_t)e * a.N;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.codes) + (at + row[r]) * a.chunks + c);
+      sc[r] = H::lo(a.scales[((at + row[r]) * a.chunks + c) / (GROUP / 32)]);
+    }
+    const uint16_t* x = a.x + xr * a.K + c * 32;
+    uint32_t xs[16];
+    float total_x = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const u32x4 p = load8(x + d * 8, a.K - c * 32 - d * 8);
+      // pairs (i, i + 4) of eight values: halves of dwords i / 2 and i / 2 + 2
+      xs[4 * d] = __builtin_amdgcn_perm(p[2], p[0], 0x05040100u);
+      xs[4 * d + 1] = __builtin_amdgcn_perm(p[2], p[0], 0x07060302u);
+      xs[4 * d + 2] = __builtin_amdgcn_perm(p[3], p[1], 0x05040100u);
+      xs[4 * d + 3] = __builtin_amdgcn_perm(p[3], p[1], 0x07060302u);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) total_x = H::dot2(xs[i], Magic<H>::ones, total_x);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float dot = -24.0f * total_x;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot = H::dot2(pair_of<H>(w[r][d], i), xs[4 * d + i], dot);
+      if constexpr (MODE == MRS_INT4_SUM) acc[r] += ok ? v * (sc[r] * dot) : 0.0f;
+      else acc[r] += sc[r] * dot;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) acc[r] += __shfl_xor(acc[r], d);
+#pragma unroll
+  for (int r = 0; r < kOut; ++r) {
+    const int n = n0 + r * kSets + sub;
+    float o = acc[r];
+    if constexpr (MODE == MRS_INT4_GATED) o = o / (1.0f + __expf(-o)) * acc[r + kOut];
+    if (q0 == 0 && n < a.out) a.y[(int64_t)unit * a.out + n] = (uint16_t)H::pack(o, 0.0f);
+  }
+}
+
+template <typename H, int MODE, int GROUP>
+const void* matvec_kernel(int lanes) {
+  switch (lanes) {
+    case 8: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 8, 4>);
+    case 16: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 16, 4>);
+    case 32: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 32, 4>);
+    default: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 64, 4>);
+  }
+}
+
+template <typename H, int MODE>
+const void* matvec_kernel(int group, int lanes) {
+  return group == 32 ? matvec_kernel<H, MODE, 32>(lanes)
+         : group == 64 ? matvec_kernel<H, MODE, 64>(lanes)
+                       : matvec_kernel<H, MODE, 128>(lanes);
+}
+
+template <typename H>
+const void* matvec_kernel(int mode, int group, int lanes) {
+  return mode == MRS_INT4_PLAIN   ? matvec_kernel<H, MRS_INT4_PLAIN>(group, lanes)
+         : mode == MRS_INT4_GATED ? matvec_kernel<H, MRS_INT4_GATED>(group, lanes)
+                                  : matvec_kernel<H, MRS_INT4_SUM>(group, lanes);
+}
+
+bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+}  // namespace
+
+extern "C" int moe_int4_quantize(const void* w, int dtype, int64_t rows, int K, int64_t row_stride, int group,
+                                 int scale_dtype, uint8_t* codes, void* scales, void* stream) {
+  if (rows < 0 || K < 1 || K > 262144 || row_stride < K || !group_ok(group) ||
+      (dtype != MRS_DTYPE_F32 && dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) ||
+      (scale_dtype != MRS_DTYPE_BF16 && scale_dtype != MRS_DTYPE_F16))
+    return MRS_ERR_INVALID_ARG;
+  if (rows == 0) return MRS_OK;
+  if (!w || !codes || !scales) return MRS_ERR_NULL_POINTER;
+  const int size = dtype == MRS_DTYPE_F32 ? 4 : 2;
+  if (!aligned_to(w, size) || !aligned_to(codes, 4) || !aligned_to(scales, 2)) return MRS_ERR_MISALIGNED;
+  const int gpr = (K + 127) / 128 * 16;
+  if (rows > (int64_t(1) << 38) / gpr) return MRS_ERR_OVERFLOW;
+  const void* fn = scale_dtype == MRS_DTYPE_BF16 ? quant_kernel<BF16>(dtype, group) : quant_kernel<FP16>(dtype, group);
+  const int64_t most = kQLaunch / gpr;
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = rows - r < most ? rows - r : most;
+    QArgs a{static_cast<const char*>(w) + r * row_stride * size, codes + r * gpr * 4,
+            static_cast<uint16_t*>(scales) + r * gpr * 8 / group, n, row_stride, K, gpr,
+            (uint32_t)(((uint64_t(1) << 32) + gpr - 1) / gpr), ~uint64_t(0) / gpr + 1};
+    void* params[] = {&a};
+    if (hipLaunchKernel(fn, dim3((unsigned)((n * gpr + kThreads - 1) / kThreads)), dim3(kThreads), params, 0,
+                        reinterpret_cast<hipStream_t>(stream)) != hipSuccess)
+      return MRS_ERR_LAUNCH;
+  }
+  return MRS_OK;
+}
+
+extern "C" int moe_int4_matvec(const void* x, int dtype, const uint8_t* codes, const void* scales, const int32_t* ids,
+                               const float* weights, int M, int k, int E, int K, int N, int group, int per_slot,
+                               int mode, void* y, void* stream) {
+  if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K < 1 || K > 262144 || N < 1 || N > 1 << 20 || !group_ok(group) ||
+      (dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) || mode < MRS_INT4_PLAIN || mode > MRS_INT4_SUM ||
+      (mode == MRS_INT4_GATED && N % 2 != 0) || (weights != nullptr) != (mode == MRS_INT4_SUM))
+    return MRS_ERR_INVALID_ARG;
+  if (M == 0) return MRS_OK;
+  if (!x || !codes || !scales || !ids || !y) return MRS_ERR_NULL_POINTER;
+  if (!aligned_to(x, 2) || !aligned_to(codes, 16) || !aligned_to(scales, 2) || !aligned_to(ids, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(y, 2))
+    return MRS_ERR_MISALIGNED;
+  MArgs a{static_cast<const uint16_t*>(x), codes, static_cast<const uint16_t*>(scales), ids, weights,
+          static_cast<uint16_t*>(y), M, k, E, K, N, per_slot != 0, (K + 127) / 128 * 4,
+          mode == MRS_INT4_GATED ? N / 2 : N, 0, 0};
+  a.chunks_mul = (uint32_t)(((uint64_t(1) << 32) + a.chunks - 1) / a.chunks);
+  const int total = mode == MRS_INT4_SUM ? k * a.chunks : a.chunks;
+  const int lanes = total >= 64 ? 64 : total >= 32 ? 32 : total >= 16 ? 16 : 8;
+  const int outs = (mode == MRS_INT4_GATED ? 2 : 4) * (64 / lanes) * (kThreads / 64);  // of a workgroup
+  a.tiles = (a.out + outs - 1) / outs;
+  const int64_t units = mode == MRS_INT4_SUM ? M : (int64_t)M * k;
+  const int64_t grid = units * a.tiles;
+  if (grid * kThreads > UINT32_MAX) return MRS_ERR_OVERFLOW;
+  const void* fn = dtype == MRS_DTYPE_BF16 ? matvec_kernel<BF16>(mode, group, lanes) : matvec_kernel<FP16>(mode, group, lanes);
+  void* params[] = {&a};
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kThreads), params, 0, reinterpret_cast<hipStream_t>(stream)) ==
+                 hipSuccess
+             ? MRS_OK
+             : MRS_ERR_LAUNCH;
+}

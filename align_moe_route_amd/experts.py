@@ -1,0 +1,477 @@
+"""Python binding of the experts' operators: 16-bit products grouped by expert with
+their gradients, the gated activation, the mix of the outputs (include/moe_experts.h)
+and matrix-vector products with 4-bit weights (include/moe_int4.h).
+
+Checks of arguments, allocation and streams as in the package's other calls: every
+call runs on the current stream, or on `stream`, which the caller then orders after
+what made the inputs and before what reads the results.  The calls that have an
+explicit backward entry point take no part in autograd and refuse, in grad mode,
+inputs whose gradient they would drop; experts_train joins them under autograd.
+"""
+from __future__ import annotations
+
+import functools
+from typing import NamedTuple, Optional
+
+from . import (MRS_DTYPE_BF16, MRS_DTYPE_F16, MRS_DTYPE_F32, MRS_INT4_GATED, MRS_INT4_PLAIN, MRS_INT4_SUM, MRS_OK,
+               MRS_X_SORTED, MRS_X_TOKENS, RouteSortError, _allocate, _capacity, _check_metadata, _check_tensor, _empty,
+               _foreign, _handle, _hold, _ptr, _row_stride, lib)
+
+
+def _code(dtype, name: str, f32: bool = False) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return MRS_DTYPE_BF16
+    if dtype == torch.float16:
+        return MRS_DTYPE_F16
+    if f32 and dtype == torch.float32:
+        return MRS_DTYPE_F32
+    raise NotImplementedError(f"{name} dtype {dtype} (bfloat16{', float16 or float32' if f32 else ' or float16'} only)")
+
+
+def _matrix(t, dims: int, name: str, dev=None, dtype=None):
+    """t is a contiguous GPU tensor of `dims` dimensions (on dev, of dtype)."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims and t.is_contiguous()
+            and (dev is None or t.device == dev) and (dtype is None or t.dtype == dtype)):
+        what = f"a contiguous {'' if dtype is None else f'{dtype} '}tensor of {dims} dimensions"
+        raise ValueError(f"{name} must be {what} on {'the GPU' if dev is None else dev}")
+
+
+def _no_grad(what: str, *tensors):
+    import torch
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what} takes no part in autograd: call it under no_grad with its backward entry point, "
+                         "or use experts_train")
+
+
+def _output(out, shape, dtype, dev, foreign, rows: Optional[int] = None):
+    """`out` checked (its first dimension may be larger than `rows`), or a new tensor."""
+    import torch
+    if out is None:
+        return _empty(shape, dtype, dev) if foreign is None else _allocate(foreign, dev, _empty, shape, dtype, dev)
+    if not (isinstance(out, torch.Tensor) and out.device == dev and out.dtype == dtype and out.is_contiguous()
+            and out.dim() == len(shape) and out.shape[1:] == tuple(shape[1:])
+            and (out.shape[0] == shape[0] if rows is None else out.shape[0] >= rows)):
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return out
+
+
+def _raise(rc: int):
+    if rc != MRS_OK:
+        raise RouteSortError(rc)
+
+
+def _sizes(M: int, E: int, k: int, block: int):
+    rows, blocks = _capacity(M, E, k, block)
+    if rows < 0:
+        raise ValueError("invalid sizes or row capacity overflow")
+    return rows, blocks
+
+
+def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block: int, *, tokens: Optional[int] = None,
+                 out_dtype=None, out=None, stream=None):
+    """16-bit product grouped by expert over the route-sort metadata
+    (moe_grouped_gemm): y[r] = x[row(r)] . w[expert_of_block[r // block]]^T for sorted
+    rows below num_post_pad, zeros for padding rows.
+
+    x: [M, K] bfloat16 or float16, row(r) = sorted_ids[r] // k; with `tokens` = M given
+    x holds max_rows rows in sorted order and row(r) = r.  w: [E, N, K] of x's type.
+    Any K and N; block: a multiple of 16.  out_dtype: x's type (default) or float32.
+    Returns y [max_rows, N]; rows at or past num_post_pad are left as they were."""
+    _matrix(x, 2, "x")
+    dt, dev = _code(x.dtype, "x"), x.device
+    _matrix(w, 3, "w", dev, x.dtype)
+    E, N, K = w.shape
+    if x.shape[1] != K:
+        raise ValueError("x and w disagree on K")
+    _no_grad("grouped_gemm", x, w)
+    M = x.shape[0] if tokens is None else int(tokens)
+    rows, blocks = _sizes(M, E, k, block)
+    if tokens is not None and x.shape[0] < rows:
+        raise ValueError(f"x must hold at least {rows} rows in sorted order")
+    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out_dtype = out_dtype or (x.dtype if out is None else out.dtype)
+    odt = dt if out_dtype == x.dtype else _code(out_dtype, "out", True)
+    out = _output(out, (max(rows, 1), N), out_dtype, dev, foreign, rows)
+    rc = int(lib().moe_grouped_gemm(x.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(), expert_of_block.data_ptr(),
+                                    num_post_pad.data_ptr(), M, k, E, K, N, block,
+                                    MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
+                                    _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, x, w, sorted_ids, expert_of_block, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: int, k: int, block: int, *,
+                    out_dtype=None, out=None, stream=None):
+    """Gradient of grouped_gemm's x in sorted rows (moe_grouped_gemm_dx): dx[r] = dy[r] .
+    w[expert_of_block[r // block]], zeros for padding rows.
+
+    dy: [max_rows, N], w: [E, N, K] of dy's type (bfloat16 or float16), tokens: M.
+    Returns dx [max_rows, K] of dy's type (default) or float32; rows at or past
+    num_post_pad are left as they were.  Of an x that holds the tokens' rows the
+    gradient is combine(dx, slot_rows(...))."""
+    _matrix(dy, 2, "dy")
+    dt, dev = _code(dy.dtype, "dy"), dy.device
+    _matrix(w, 3, "w", dev, dy.dtype)
+    E, N, K = w.shape
+    if dy.shape[1] != N:
+        raise ValueError("dy and w disagree on N")
+    _no_grad("grouped_gemm_dx", dy, w)
+    M = int(tokens)
+    rows, blocks = _sizes(M, E, k, block)
+    if dy.shape[0] < rows:
+        raise ValueError(f"dy must hold at least {rows} rows in sorted order")
+    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
+    odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
+    out = _output(out, (max(rows, 1), K), out_dtype, dev, foreign, rows)
+    rc = int(lib().moe_grouped_gemm_dx(dy.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
+                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block, odt,
+                                       out.data_ptr(), _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, dy, w, sorted_ids, expert_of_block, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def grouped_gemm_dw(dy, x, E: int, sorted_ids, expert_of_block, num_post_pad, k: int, block: int, *,
+                    tokens: Optional[int] = None, out_dtype=None, out=None, stream=None):
+    """Gradient of grouped_gemm's w (moe_grouped_gemm_dw): dw[e] = dy[rows of e]^T .
+    x[row(r)], zeros for an expert without a route.
+
+    dy: [max_rows, N]; x and `tokens` as for grouped_gemm; E: the experts.  Returns dw
+    [E, N, K] of dy's type (default) or float32; equal inputs give equal bits."""
+    _matrix(dy, 2, "dy")
+    dt, dev = _code(dy.dtype, "dy"), dy.device
+    _matrix(x, 2, "x", dev, dy.dtype)
+    N, K, E = dy.shape[1], x.shape[1], int(E)
+    _no_grad("grouped_gemm_dw", dy, x)
+    M = x.shape[0] if tokens is None else int(tokens)
+    rows, blocks = _sizes(M, E, k, block)
+    if dy.shape[0] < rows or (tokens is not None and x.shape[0] < rows):
+        raise ValueError(f"rows in sorted order must be at least {rows}")
+    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
+    odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
+    out = _output(out, (E, N, K), out_dtype, dev, foreign)
+    rc = int(lib().moe_grouped_gemm_dw(dy.data_ptr(), x.data_ptr(), dt, sorted_ids.data_ptr(),
+                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
+                                       MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
+                                       _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, dy, x, sorted_ids, expert_of_block, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def _check_count(num_post_pad, dev):
+    import torch
+    if num_post_pad is not None:
+        _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+
+
+def swiglu(a, num_post_pad=None, *, out=None, stream=None):
+    """Gated activation (moe_swiglu): h[r, i] = silu(a[r, i]) * a[r, I + i].
+
+    a: [rows, 2 I] bfloat16 or float16.  num_post_pad: int32 [1] on the device, the
+    rows to take (the others of h are left as they were); by default all."""
+    _matrix(a, 2, "a")
+    dt, dev = _code(a.dtype, "a"), a.device
+    rows, I2 = a.shape
+    if I2 % 2 or I2 == 0:
+        raise ValueError("a must have an even number of columns")
+    _no_grad("swiglu", a)
+    _check_count(num_post_pad, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out = _output(out, (rows, I2 // 2), a.dtype, dev, foreign)
+    rc = int(lib().moe_swiglu(a.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2, out.data_ptr(), _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, a, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def swiglu_backward(a, dh, num_post_pad=None, *, out=None, stream=None):
+    """Gradient of swiglu's a (moe_swiglu_backward) from dh [rows, I]; `out` may be a."""
+    _matrix(a, 2, "a")
+    dt, dev = _code(a.dtype, "a"), a.device
+    rows, I2 = a.shape
+    if I2 % 2 or I2 == 0:
+        raise ValueError("a must have an even number of columns")
+    _matrix(dh, 2, "dh", dev, a.dtype)
+    if dh.shape != (rows, I2 // 2):
+        raise ValueError(f"dh must have shape {(rows, I2 // 2)}")
+    _no_grad("swiglu_backward", a, dh)
+    _check_count(num_post_pad, dev)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out = _output(out, (rows, I2), a.dtype, dev, foreign)
+    rc = int(lib().moe_swiglu_backward(a.data_ptr(), dh.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2,
+                                       out.data_ptr(), _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, a, dh, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def slot_rows(sorted_ids, num_post_pad, tokens: int, k: int, *, out=None, stream=None):
+    """Sorted row of every slot (moe_slot_rows): int32 [M, k], -1 for a dropped route."""
+    import torch
+    if not isinstance(sorted_ids, torch.Tensor) or not sorted_ids.is_cuda:
+        raise ValueError("sorted_ids must be a GPU tensor")
+    dev, M = sorted_ids.device, int(tokens)
+    _check_tensor(sorted_ids, dev, torch.int32, 0, "sorted_ids")
+    _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+    if M < 0 or k < 1:
+        raise ValueError("tokens must not be negative and k at least 1")
+    foreign = None if stream is None else _foreign(stream, dev)
+    out = _output(out, (M, k), torch.int32, dev, foreign)
+    rc = int(lib().moe_slot_rows(sorted_ids.data_ptr(), num_post_pad.data_ptr(), sorted_ids.numel(), M, k,
+                                 out.data_ptr(), _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, sorted_ids, num_post_pad, out)
+    _raise(rc)
+    return out
+
+
+def _check_weights(weights, M: int, k: int, dev):
+    import torch
+    if weights is not None:
+        _check_tensor(weights, dev, torch.float32, M * k, "weights")
+        if tuple(weights.shape) != (M, k):
+            raise ValueError(f"weights must have shape ({M}, {k})")
+
+
+def combine(y, rows, weights=None, *, out_dtype=None, out=None, stream=None):
+    """Mix of the picks' rows (moe_combine): out[t] = sum_j weights[t, j] * y[rows[t, j]].
+
+    y: [R, N] bfloat16 or float16.  rows: int32 [M, k] (slot_rows; a row outside [0, R)
+    adds nothing), or an integer k for y in slot order.  weights: float32 [M, k], by
+    default ones.  Returns [M, N] of y's type (default) or float32."""
+    import torch
+    _matrix(y, 2, "y")
+    dt, dev = _code(y.dtype, "y"), y.device
+    R, N = y.shape
+    if isinstance(rows, int):
+        k, rows = rows, None
+        if k < 1 or R % k:
+            raise ValueError("y must hold k rows for every token")
+        M = R // k
+    else:
+        _matrix(rows, 2, "rows", dev, torch.int32)
+        M, k = rows.shape
+    _check_weights(weights, M, k, dev)
+    _no_grad("combine", y, weights)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out_dtype = out_dtype or (y.dtype if out is None else out.dtype)
+    odt = dt if out_dtype == y.dtype else _code(out_dtype, "out", True)
+    out = _output(out, (M, N), out_dtype, dev, foreign)
+    rc = int(lib().moe_combine(y.data_ptr(), dt, _ptr(rows), _ptr(weights), R, M, k, N, odt, out.data_ptr(),
+                               _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, y, rows, weights, out)
+    _raise(rc)
+    return out
+
+
+def combine_backward(dout, rows, sorted_ids, num_post_pad, *, weights=None, y=None, out=None, stream=None):
+    """Gradients of combine (moe_combine_backward): dy[r] = weights[s] * dout[s // k] of
+    the slot s = sorted_ids[r], zeros in padding rows, and, when y (what combine was
+    given) is, the weights' gradient [M, k] float32.
+
+    dout: [M, N] bfloat16 or float16; rows: slot_rows of this metadata.  Returns dy
+    [rows of y, or of sorted_ids; N], or (dy, dweights); rows of dy at or past
+    num_post_pad are left as they were."""
+    import torch
+    _matrix(dout, 2, "dout")
+    dt, dev = _code(dout.dtype, "dout"), dout.device
+    M, N = dout.shape
+    _matrix(rows, 2, "rows", dev, torch.int32)
+    if rows.shape[0] != M:
+        raise ValueError(f"rows must have shape ({M}, k)")
+    k = rows.shape[1]
+    _check_weights(weights, M, k, dev)
+    R = sorted_ids.numel() if y is None else y.shape[0]
+    if y is not None:
+        _matrix(y, 2, "y", dev, dout.dtype)
+        if y.shape[1] != N:
+            raise ValueError("y and dout disagree on N")
+    _check_tensor(sorted_ids, dev, torch.int32, R, "sorted_ids")
+    _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+    _no_grad("combine_backward", dout, weights, y)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out = _output(out, (R, N), dout.dtype, dev, foreign)
+    dv = None if y is None else _output(None, (M, k), torch.float32, dev, foreign)
+    rc = int(lib().moe_combine_backward(dout.data_ptr(), _ptr(y), dt, rows.data_ptr(), sorted_ids.data_ptr(),
+                                        num_post_pad.data_ptr(), _ptr(weights), R, M, k, N, out.data_ptr(), _ptr(dv),
+                                        _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, dout, y, rows, sorted_ids, num_post_pad, weights, out, dv)
+    _raise(rc)
+    return out if dv is None else (out, dv)
+
+
+@functools.lru_cache(maxsize=1)
+def _experts_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Experts(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w_up, w_down, weights, sorted_ids, expert_of_block, num_post_pad, block):
+            meta = (sorted_ids, expert_of_block, num_post_pad)
+            M, k = weights.shape
+            a = grouped_gemm(x, w_up, *meta, k, block)
+            h = swiglu(a, num_post_pad)
+            y = grouped_gemm(h, w_down, *meta, k, block, tokens=M)
+            rows = slot_rows(sorted_ids, num_post_pad, M, k)
+            ctx.save_for_backward(x, w_up, w_down, weights, a, h, y, rows, *meta)
+            ctx.block = block
+            return combine(y, rows, weights)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dout):
+            x, w_up, w_down, weights, a, h, y, rows, *meta = ctx.saved_tensors
+            sorted_ids, _, num_post_pad = meta
+            (M, k), block, E = weights.shape, ctx.block, w_up.shape[0]
+            need_x, need_up, need_down, need_v = ctx.needs_input_grad[:4]
+            dy = combine_backward(dout.contiguous(), rows, sorted_ids, num_post_pad, weights=weights,
+                                  y=y if need_v else None)
+            dy, dv = dy if need_v else (dy, None)
+            dx = d_up = d_down = None
+            if need_down:
+                d_down = grouped_gemm_dw(dy, h, E, *meta, k, block, tokens=M)
+            if need_x or need_up:
+                da = swiglu_backward(a, grouped_gemm_dx(dy, w_down, *meta, M, k, block), num_post_pad)
+                if need_up:
+                    d_up = grouped_gemm_dw(da, x, E, *meta, k, block)
+                if need_x:
+                    dx = combine(grouped_gemm_dx(da, w_up, *meta, M, k, block), rows)
+            return dx, d_up, d_down, dv, None, None, None, None
+
+    return Experts
+
+
+def experts_train(x, w_up, w_down, route, block: int):
+    """The experts of a routed layer under autograd: out[t] = sum over t's picks of
+    weight * w_down[e] . (silu(gate) * up) with (gate, up) = w_up[e] . x[t].
+
+    x: [M, H] bfloat16 or float16; w_up: [E, 2 I, H] (the gates' rows first) and w_down:
+    [E, H, I] of x's type; route: what route_sort, or route_sort_train (whose weights
+    pass the gradient on to the logits), returned for `block`.  Returns [M, H] with
+    gradients to x, both weights and route.weights.  To capture a training step in a
+    graph call the entry points themselves, as for route_sort_train."""
+    _matrix(x, 2, "x")
+    dev = x.device
+    _matrix(w_up, 3, "w_up", dev, x.dtype)
+    _matrix(w_down, 3, "w_down", dev, x.dtype)
+    _matrix(route.weights, 2, "route.weights", dev)
+    E, two, H = w_up.shape
+    if x.shape[1] != H or two % 2 or tuple(w_down.shape) != (E, H, two // 2) or route.weights.shape[0] != x.shape[0]:
+        raise ValueError("w_up must be [E, 2 I, H], w_down [E, H, I] and route.weights [M, k] for x [M, H]")
+    return _experts_function().apply(x, w_up, w_down, route.weights, route.sorted_ids, route.expert_of_block,
+                                     route.num_post_pad, block)
+
+
+class Int4(NamedTuple):
+    """int4 rows (include/moe_int4.h): K columns padded with zeros to Kp, a multiple of
+    128, in groups that share a scale; weight = scale * (code - 8)."""
+    codes: "torch.Tensor"   # uint8 [..., Kp / 2], two codes a byte, the even column in the low half
+    scales: "torch.Tensor"  # bfloat16 or float16 [..., Kp / group]
+
+
+def _group_of(q, dev, dims: int, name: str) -> int:
+    """q holds contiguous int4 rows with `dims` dimensions on dev; returns the group."""
+    import torch
+    if not isinstance(q, Int4):
+        raise ValueError(f"{name} must be an Int4")
+    _matrix(q.codes, dims, f"{name}.codes", dev, torch.uint8)
+    _matrix(q.scales, dims, f"{name}.scales", dev)
+    Kp, n = q.codes.shape[-1] * 2, q.scales.shape[-1]
+    if Kp == 0 or Kp % 128 or q.codes.shape[:-1] != q.scales.shape[:-1] or n == 0 or Kp % n or Kp // n not in (32, 64, 128):
+        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows, Kp a multiple of "
+                         "128, group 32, 64 or 128")
+    return Kp // n
+
+
+def _new_int4(lead, Kp: int, group: int, u8, dtype, dev) -> Int4:
+    return Int4(_empty((*lead, Kp // 2), u8, dev), _empty((*lead, Kp // group), dtype, dev))
+
+
+def int4_quantize(w, group: int = 128, *, scale_dtype=None, out: Optional[Int4] = None, stream=None) -> Int4:
+    """Rows of w to int4 rows (moe_int4_quantize).
+
+    w: float32, bfloat16 or float16 GPU tensor [..., K], 1 <= K <= 262144, rows of one
+    stride as for mxfp4_quantize.  group: 32, 64 or 128 columns to a scale.  scale_dtype:
+    bfloat16 or float16, the type of the x that the weights will meet (default: w's, or
+    bfloat16 for float32 weights)."""
+    import torch
+    if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dim() >= 1):
+        raise ValueError("w must be a GPU tensor of at least one dimension")
+    dt, dev = _code(w.dtype, "w", True), w.device
+    *lead, K = w.shape
+    if not 1 <= K <= 262144:
+        raise ValueError("the last dimension must hold 1 to 262144 values")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    rows, row_stride = w.numel() // K, _row_stride(w, K)
+    if scale_dtype is None:
+        scale_dtype = (torch.bfloat16 if w.dtype == torch.float32 else w.dtype) if out is None else out.scales.dtype
+    sdt = _code(scale_dtype, "scale")
+    Kp = (K + 127) // 128 * 128
+    foreign = None if stream is None else _foreign(stream, dev)
+    if out is None:
+        new = lead, Kp, group, torch.uint8, scale_dtype, dev
+        out = _new_int4(*new) if foreign is None else _allocate(foreign, dev, _new_int4, *new)
+    elif _group_of(out, dev, w.dim(), "out") != group or out.codes.shape != (*lead, Kp // 2) or \
+            out.scales.dtype != scale_dtype:
+        raise ValueError(f"out must hold codes {(*lead, Kp // 2)} and {scale_dtype} scales {(*lead, Kp // group)}")
+    rc = int(lib().moe_int4_quantize(w.data_ptr(), dt, rows, K, row_stride, group, sdt, out.codes.data_ptr(),
+                                     out.scales.data_ptr(), _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, w, *out)
+    _raise(rc)
+    return out
+
+
+def int4_matvec(x, w: Int4, ids, *, gated: bool = False, weights=None, out=None, stream=None):
+    """Matrix-vector products of routed tokens with 4-bit weights (moe_int4_matvec),
+    for few tokens: p[t, j] = w[ids[t, j]] . x[t] (or x[t, j]).
+
+    x: [M, K], or [M, k, K] with a row for every pick, bfloat16 or float16.  w: int4 rows
+    [E, N] of K columns, scales of x's type.  ids: int32 [M, k]; a pick outside [0, E)
+    gives zeros.  Returns p [M, k, N]; with `gated` [M, k, N / 2], silu(p[..., :N / 2]) *
+    p[..., N / 2:]; with weights (float32 [M, k]) their sum over the picks [M, N]."""
+    import torch
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (2, 3) and x.is_contiguous()):
+        raise ValueError("x must be a contiguous [M, K] or [M, k, K] GPU tensor")
+    dt, dev = _code(x.dtype, "x"), x.device
+    group = _group_of(w, dev, 3, "w")
+    if w.scales.dtype != x.dtype:
+        raise ValueError("w's scales must have x's type")
+    _matrix(ids, 2, "ids", dev, torch.int32)
+    M, k = ids.shape
+    E, N, half = w.codes.shape
+    K = x.shape[-1]
+    if tuple(x.shape[:-1]) != ((M,) if x.dim() == 2 else (M, k)) or (K + 127) // 128 * 128 != half * 2:
+        raise ValueError(f"x must have shape ({M}, K) or ({M}, {k}, K), K columns of w")
+    if gated and (weights is not None or N % 2):
+        raise ValueError("gated results need an even N and take no weights")
+    _check_weights(weights, M, k, dev)
+    _no_grad("int4_matvec", x, weights)
+    foreign = None if stream is None else _foreign(stream, dev)
+    out = _output(out, (M, k, N // 2 if gated else N) if weights is None else (M, N), x.dtype, dev, foreign)
+    mode = MRS_INT4_GATED if gated else MRS_INT4_PLAIN if weights is None else MRS_INT4_SUM
+    rc = int(lib().moe_int4_matvec(x.data_ptr(), dt, w.codes.data_ptr(), w.scales.data_ptr(), ids.data_ptr(),
+                                   _ptr(weights), M, k, E, K, N, group, int(x.dim() == 3), mode, out.data_ptr(),
+                                   _handle(stream, dev)))
+    if foreign is not None:
+        _hold(foreign, x, *w, ids, weights, out)
+    _raise(rc)
+    return out
