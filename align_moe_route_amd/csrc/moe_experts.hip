@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "half.h"
 #include "moe_experts.h"
 #include "moe_route_sort.h"
@@ -28,24 +30,22 @@ struct GArgs {
   int run;        // consecutive row tiles of an XCD
 };
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kStep = 32;  // of c
 
-// Operand tiles in LDS, in 16-byte chunks of eight values.
+// Operand tiles in LDS, in 16-byte chunks of eight values, a step of STEP values of c.
 //
-// Rows along c: 4 chunks a row, the chunk at slot p of row r is p ^ ((r ^ (r >> 2)) & 3),
-// so that the 32 rows of an operand read hit distinct banks.
+// Rows along c: the chunk at slot p of row r is p ^ ((r ^ (r >> 2)) & 3) (4 chunks a row)
+// or p ^ (r & 7) ^ (r >> 3 & 1) (8 chunks), so that the 32 rows of an operand read hit
+// distinct banks.
 //
 // Rows along the tile (one LDS row per c, W values wide): read by ds_read_b64_tr_b16,
 // in which 16 lanes together read four rows of 16 values and each lane receives one
 // column's four values.  Slot p of row c holds chunk p ^ (c & 3) << 2: the four rows
 // that 32 lanes read 64 bytes of lie on distinct banks.
-__device__ __forceinline__ int swz(int r, int p) { return p ^ ((r ^ (r >> 2)) & 3); }
-template <int W>
-__device__ __forceinline__ int swz_across(int c, int p) {
-  static_assert(W >= 128, "chunk moves within the row");
-  return p ^ ((c & 3) << 2);
+template <int STEP>
+__device__ __forceinline__ int swz(int r, int p) {
+  return STEP == 64 ? p ^ (r & 7) ^ ((r >> 3) & 1) : p ^ ((r ^ (r >> 2)) & 3);
 }
+__device__ __forceinline__ int swz_across(int c, int p) { return p ^ ((c & 3) << 2); }
 
 typedef __attribute__((address_space(3))) char* lds_t;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -57,16 +57,17 @@ __device__ __forceinline__ u32x2 read_turned(const char* p) {
 
 // Operand of v_mfma_*_32x32x16: lane l holds values 8 (l / 32) .. + 7 of c of row l mod
 // 32; rows m0 .., c from 16 kk.
-template <bool ACROSS, int W>
+template <bool ACROSS, int W, int STEP>
 __device__ __forceinline__ u32x4 operand(const u32x4* tile, int m0, int kk) {
   const int lane = threadIdx.x & 63;
   if constexpr (!ACROSS) {
     const int r = m0 + (lane & 31);
-    return tile[r * (kStep / 8) + swz(r, kk * 2 + (lane >> 5))];
+    return tile[r * (STEP / 8) + swz<STEP>(r, kk * 2 + (lane >> 5))];
   } else {
+    static_assert(W >= 128, "chunks move within a row");
     const int c = kk * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
     const int m = m0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-    const char* p = reinterpret_cast<const char*>(tile + c * (W / 8) + swz_across<W>(c, m / 8)) + (m & 4) * 2;
+    const char* p = reinterpret_cast<const char*>(tile + c * (W / 8) + swz_across(c, m / 8)) + (m & 4) * 2;
     const u32x2 lo = read_turned(p), hi = read_turned(p + 4 * (W / 8) * 16);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   }
@@ -123,47 +124,48 @@ __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& f
 }
 
 constexpr int kXcds = 8;
+constexpr int kRowsAhead = 4096;  // rows of an expert whose sources are kept in LDS at once (kWeights)
 
-template <int BM>
-constexpr int tile_rows() {
-  return BM < 32 ? 32 : BM;
-}
-template <int BM>
-constexpr int stages() {
-  return BM < 64 ? 4 : 3;
-}
-constexpr int kRowsAhead = 1024;  // rows of an expert whose sources are kept in LDS at once (kWeights)
+// A tile of BM x BN results by NW waves, in steps of STEP values of c, S stages of LDS.
+template <int BM_, int BN_, int NW_, int STEP_, int S_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, NW = NW_, STEP = STEP_, S = S_;
+  static constexpr int TR = BM < 32 ? 32 : BM;   // rows that are multiplied
+  static constexpr int WI = BM >= 256 ? 4 : BM >= 128 ? 2 : 1, WJ = NW / WI;  // waves along i and j
+  static constexpr int FM = TR / WI / 32, FN = BN / WJ / 32;  // operands of a wave
+  static constexpr int kThreads = NW * 64;
+};
 
-template <int DIR, int BM, int BN>
+template <int DIR, typename P>
 struct Ring {
-  static constexpr int kRows = tile_rows<BM>();
-  u32x4 a[stages<BM>()][kRows * kStep / 8], b[stages<BM>()][BN * kStep / 8];
-  int32_t row[DIR == kWeights ? kRowsAhead : kRows];
+  u32x4 a[P::S][P::TR * P::STEP / 8], b[P::S][P::BN * P::STEP / 8];
+  int32_t row[DIR == kWeights ? kRowsAhead + P::S * P::STEP : P::TR];
 };
 
 // DA, DB: the operand's rows and chunks are whole and 16-byte aligned, and go from
 // memory into LDS; otherwise through registers.
-template <typename H, int DIR, int BM, int BN, bool F32, bool DA, bool DB>
-__global__ __launch_bounds__(kThreads, 2) void k_product(GArgs g) {
+template <typename H, int DIR, typename P, bool F32, bool DA, bool DB>
+__global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
   constexpr bool kAcrossA = DIR == kWeights, kAcrossB = DIR != kForward;
-  constexpr int TR = tile_rows<BM>(), S = stages<BM>();
-  constexpr int WI = BM >= 128 ? 2 : 1, WJ = kWaves / WI;  // waves along i and j
-  constexpr int FM = TR / WI / 32, FN = BN / WJ / 32;
+  constexpr int BM = P::BM, BN = P::BN, TR = P::TR, S = P::S, kStep = P::STEP, kThreads = P::kThreads;
+  constexpr int WJ = P::WJ, FM = P::FM, FN = P::FN, kWaves = P::NW;
   constexpr int kChunks = kStep / 8;
   constexpr int AT = TR * kChunks;  // chunks of a stage of A
   constexpr int AP = (AT + kThreads - 1) / kThreads, BP = BN * kChunks / kThreads;  // of a thread
-  constexpr int L = AP + BP;  // loads into LDS of a wave and stage
-  __shared__ Ring<DIR, BM, BN> l;
+  constexpr int L = AP + BP;      // loads of a thread and stage
+  constexpr int KK = kStep / 16;  // matrix instructions' steps of a stage
+  __shared__ Ring<DIR, P> l;
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int npp = min(*g.npp, g.row_limit);
 
+  const int wi = wv / WJ * FM * 32, wj = wv % WJ * FN * 32;  // this wave's part of the tile
   int i0, j0, e, c_first = 0, c_end;  // the tile, its expert, the range of c
-  uint64_t has[2] = {~0ull, ~0ull};   // rows that hold a slot
+  uint64_t has = ~0ull;               // this wave's rows that hold a slot
   if constexpr (DIR == kWeights) {
-    const int h = blockIdx.x, x = h % kXcds, j = h / kXcds, each = g.nrt * g.nct;
-    e = j / each * kXcds + x;
+    const int h = blockIdx.x, x = h % kXcds, q = h / kXcds, u = q / g.nrt * kXcds + x;
+    e = u / g.nct;
     if (e >= g.E) return;
-    i0 = j % each / g.nct * BM, j0 = j % each % g.nct * BN;
+    i0 = q % g.nrt * BM, j0 = u % g.nct * BN;
     int first, last;
     segment(g.eob, max(npp, 0) / g.block, e, first, last);
     c_first = first * g.block, c_end = last * g.block;
@@ -182,17 +184,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(GArgs g) {
       l.row[tid] = !ok ? -1 : (DIR == kForward && !g.sorted) ? s / g.k : i0 + tid;
     }
     __syncthreads();
-    has[0] = __ballot(lane < TR && l.row[lane % TR] >= 0);
-    has[1] = TR > 64 ? __ballot(l.row[(64 + lane) % TR] >= 0) : 0;
+    has = __ballot(lane < FM * 32 && l.row[wi + lane % (FM * 32)] >= 0);
   }
   e = __builtin_amdgcn_readfirstlane(e);
 
   // Sources of this thread's chunks p: slot tid + p * kThreads of a stage.
   // Rows along c: row sr + p * 64, chunk sc.  Across: c = tid / W + p * S, chunk by swz_across.
   constexpr int kRowStep = kThreads / kChunks;
-  const int sr = tid / kChunks, sc = swz(sr, tid % kChunks) * 8;
+  const int sr = tid / kChunks, sc = swz<kStep>(sr, tid % kChunks) * 8;
   constexpr int WA = TR / 8, SA = kThreads / WA, WB = BN / 8, SB = kThreads / WB;
-  const int ia = i0 + swz_across<128>(tid / WA, tid % WA) * 8, jb = j0 + swz_across<BN>(tid / WB, tid % WB) * 8;
+  const int ia = i0 + swz_across(tid / WA, tid % WA) * 8, jb = j0 + swz_across(tid / WB, tid % WB) * 8;
   const uint16_t* const end_a = g.a_end;
   const uint16_t* const end_b = g.b_end;
   const uint16_t *pa[kAcrossA ? 1 : AP], *pb[DIR == kWeights ? 1 : BP];
@@ -218,45 +219,60 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(GArgs g) {
   const void* const zeros = &kZeros;
   u32x4 ra[AP], rb[BP];
 
-  // step t of c: into stage `buf` of LDS, or into registers
-  auto issue = [&](int t, int buf) {
-    const int c0 = t * kStep;  // kWeights: from the first of the rows in l.row
-    if constexpr (!kAcrossA) {
+  // kWeights: the sources of a step's rows, -1 for none; the same for both operands where
+  // their tiles are equally wide
+  constexpr bool kOneMap = WA == WB;
+  constexpr int RP = DIR != kWeights ? 1 : kOneMap ? AP : AP + BP;
+  int rows[RP];
+  auto find = [&](int (&to)[RP], int t) {
+    if constexpr (DIR == kWeights) {
 #pragma unroll
-      for (int p = 0; p < AP; ++p) {
+      for (int p = 0; p < AP; ++p) to[p] = l.row[t * kStep + tid / WA + p * SA];
+      if constexpr (!kOneMap) {
+#pragma unroll
+        for (int p = 0; p < BP; ++p) to[AP + p] = l.row[t * kStep + tid / WB + p * SB];
+      }
+    }
+  };
+  // A part of step t of c, a KK-th (all of it where kPart is KK): into stage `buf` of LDS, or
+  // into registers.
+  auto issue = [&](int t, int buf, auto part) {
+    constexpr int kPart = decltype(part)::value;
+    auto mine = [](int q) { return kPart == KK || q * KK / L == kPart; };
+    const int c0 = t * kStep;  // kWeights: from the first of the rows in l.row
+#pragma unroll
+    for (int p = 0; p < AP; ++p) {
+      if (!mine(p)) continue;
+      const uint32_t dst = lds_a + (buf * AT + p * kThreads) * 16;
+      if constexpr (!kAcrossA) {
         if (AT % kThreads == 0 || tid + p * kThreads < AT) {
           const uint16_t* src = pa[p] + c0;
-          if constexpr (DA)
-            load_lds(c0 + kStep <= c_end || c0 + sc < c_end ? src : zeros,
-                     lds_a + (buf * AT + p * kThreads) * 16);
-          else
-            ra[p] = load8_any(src, c_end - c0 - sc, end_a);
+          if constexpr (DA) load_lds(c0 + sc < c_end ? src : zeros, dst);
+          else ra[p] = load8_any(src, c_end - c0 - sc, end_a);
         }
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < AP; ++p) {
+      } else {
         const int c = c0 + tid / WA + p * SA;
-        const bool ok = l.row[c] >= 0;
+        const bool ok = rows[p] >= 0;
         const uint16_t* src = g.a + (int64_t)(c_first + c) * g.I + (DA ? min(ia, g.I - 8) : ia);
-        if constexpr (DA) load_lds(ok ? src : zeros, lds_a + (buf * AT + p * kThreads) * 16);
+        if constexpr (DA) load_lds(ok ? src : zeros, dst);
         else ra[p] = load8_any(src, ok ? g.I - ia : 0, end_a);
       }
     }
 #pragma unroll
     for (int p = 0; p < BP; ++p) {
+      if (!mine(AP + p)) continue;
       const uint32_t dst = lds_b + (buf * BN * kChunks + p * kThreads) * 16;
       if constexpr (DIR == kForward) {
         const uint16_t* src = pb[p] + c0;
-        if constexpr (DB) load_lds(c0 + kStep <= c_end || c0 + sc < c_end ? src : zeros, dst);
+        if constexpr (DB) load_lds(c0 + sc < c_end ? src : zeros, dst);
         else rb[p] = load8_any(src, c_end - c0 - sc, end_b);
       } else if constexpr (DIR == kRows) {
         const uint16_t* src = pb[p] + (int64_t)c0 * g.J;
         const bool ok = c0 + tid / WB + p * SB < c_end;
-        if constexpr (DB) load_lds(c0 + kStep <= c_end || ok ? src : zeros, dst);
+        if constexpr (DB) load_lds(ok ? src : zeros, dst);
         else rb[p] = load8_any(src, ok ? g.J - jb : 0, end_b);
       } else {
-        const int row = l.row[c0 + tid / WB + p * SB];
+        const int row = rows[kOneMap ? p : AP + p];
         const uint16_t* src = g.b + (int64_t)max(row, 0) * g.J + (DB ? min(jb, g.J - 8) : jb);
         if constexpr (DB) load_lds(row >= 0 ? src : zeros, dst);
         else rb[p] = load8_any(src, row >= 0 ? g.J - jb : 0, end_b);
@@ -280,52 +296,122 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(GArgs g) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-  const int wi = wv / WJ * FM * 32, wj = wv % WJ * FN * 32;
-  auto multiply = [&](int buf) {
+  struct Operands {
+    u32x4 a[FM], b[FN];
+  };
+  auto read_one = [&](Operands& f, int buf, int kk, int q) {
+    if (q < FM) f.a[q] = operand<kAcrossA, TR, kStep>(l.a[buf], wi + q * 32, kk);
+    else f.b[q - FM] = operand<kAcrossB, BN, kStep>(l.b[buf], wj + (q - FM) * 32, kk);
+  };
+  auto multiply_one = [&](const Operands& f, int q) { acc[q / FN][q % FN] = H::mfma32(f.b[q % FN], f.a[q / FN], acc[q / FN][q % FN]); };
+  auto next = [](int buf) { return buf + 1 == S ? 0 : buf + 1; };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  typedef std::integral_constant<int, KK> All;
+  // Steps 0 .. n - 1 of c, all operands straight into LDS.  S - 1 stages are in flight; a
+  // step past the last asks for zeros, so that every wait is for the same number.  The
+  // matrix instructions of a k-step are interleaved with the reads of the next one's
+  // operands and with a part of a stage's loads (left to itself the compiler reads the
+  // operands right before their use).  A step has one barrier: past it the next stage
+  // has arrived, and the stage read before is free.
+  auto run_direct = [&](int n, auto active) {
+    constexpr bool kActive = decltype(active)::value;  // a wave without rows only loads
+    constexpr int kReads = FM + FN, kMul = FM * FN;
+    Operands f[2];
+    // this wave's loads of S - 2 stages may be in flight
+    auto wait_stage = [&] {
+      if (AT < kThreads && wv >= AT / 64) wait_loads<(S - 2) * BP>();  // it loads no part of A
+      else wait_loads<(S - 2) * L>();
+    };
 #pragma unroll
-    for (int kk = 0; kk < kStep / 16; ++kk) {
-      u32x4 fa[FM], fb[FN];
+    for (int s = 0; s < S - 1; ++s) {
+      find(rows, s);
+      issue(s, s, All());
+    }
+    find(rows, S - 1);
+    wait_stage();
+    barrier();
+    int buf = 0, last = S - 1;  // the stages of step t and of step t + S - 1
+    issue(S - 1, last, std::integral_constant<int, 0>());
+    if constexpr (kActive) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = operand<kAcrossA, TR>(l.a[buf], wi + i * 32, kk);
+      for (int q = 0; q < kReads; ++q) read_one(f[0], 0, 0, q);
+    }
+    for (int t = 0; t < n; ++t) {
+      int ahead[RP];
+      auto go = [&](auto kc) {
+        constexpr int kk = decltype(kc)::value, kAt = kk == KK - 1 && kMul > 1 ? 1 : 0;  // instructions before the reads
+        fence();
 #pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = operand<kAcrossB, BN>(l.b[buf], wj + j * 32, kk);
+        for (int q = 0; q < kMul; ++q) {
+          if (kk == KK - 1 && q == kAt) {
+            wait_stage();
+            barrier();
+            last = buf, buf = next(buf);
+          }
+          if (q == kAt) {
+            if constexpr (kk == 0) find(ahead, t + S);
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+            for (int r = 0; r < (kReads + 1) / 2; ++r)
+              if constexpr (kActive) read_one(f[(kk + 1) & 1], buf, (kk + 1) % KK, r);
+          }
+          if (kActive && q == (kAt + 1 < kMul ? kAt + 1 : kAt)) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = H::mfma32(fb[j], fa[i], acc[i][j]);
+            for (int r = (kReads + 1) / 2; r < kReads; ++r) read_one(f[(kk + 1) & 1], buf, (kk + 1) % KK, r);
+          }
+          if constexpr (kActive) multiply_one(f[kk & 1], q);
+          fence();
+          if (q == (kMul > 2 ? 2 : kMul - 1)) {
+            if constexpr (kk == KK - 1) {
+#pragma unroll
+              for (int r = 0; r < RP; ++r) rows[r] = ahead[r];
+              issue(t + S, last, std::integral_constant<int, 0>());
+            } else {
+              issue(t + S - 1, last, std::integral_constant<int, kk + 1>());
+            }
+            fence();
+          }
+        }
+      };
+      go(std::integral_constant<int, 0>());
+      go(std::integral_constant<int, 1>());
+      if constexpr (KK == 4) {
+        go(std::integral_constant<int, 2>());
+        go(std::integral_constant<int, 3>());
+      }
+    }
+    wait_loads<0>();
+  };
+  // Through registers: a step's are stored when the next one's have been asked for.
+  auto run_staged = [&](int n, bool active) {
+    find(rows, 0);
+    issue(0, 0, All());
+    int buf = 0;
+    for (int t = 0; t < n; ++t) {
+      store(buf);
+      wait_loads<0>();
+      barrier();
+      if (t + 1 < n) {
+        find(rows, t + 1);
+        issue(t + 1, next(buf), All());
+      }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        if (!active) break;
+        Operands f;
+#pragma unroll
+        for (int q = 0; q < FM + FN; ++q) read_one(f, buf, kk, q);
+#pragma unroll
+        for (int q = 0; q < FM * FN; ++q) multiply_one(f, q);
+      }
+      buf = next(buf);
     }
   };
-  auto next = [](int buf) { return buf + 1 == S ? 0 : buf + 1; };
-  // Steps 0 .. n - 1 of c.  All operands straight into LDS: S - 1 stages in flight, one
-  // barrier a step, past which the stage multiplied before is free.  Through registers:
-  // a step's are stored when the next one's have been asked for.
-  auto run = [&](int n) {
+  auto run = [&](int n, bool active) {
     if constexpr (DA && DB) {
-#pragma unroll
-      for (int s = 0; s < S - 1; ++s)
-        if (s < n) issue(s, s);
-      int buf = 0, free = S - 1;
-      for (int t = 0; t < n; ++t) {
-        const int newer = min(S - 2, n - 1 - t);  // stages asked for after this one
-        if (newer == 0) wait_loads<0>();
-        else if (AT < kThreads && wv >= AT / 64) newer == 1 ? wait_loads<BP>() : wait_loads<2 * BP>();  // no part of A
-        else newer == 1 ? wait_loads<L>() : wait_loads<2 * L>();
-        barrier();
-        if (t + S - 1 < n) issue(t + S - 1, free);
-        multiply(buf);
-        buf = next(buf), free = next(free);
-      }
+      if (active) run_direct(n, std::true_type());
+      else run_direct(n, std::false_type());
     } else {
-      issue(0, 0);
-      int buf = 0;
-      for (int t = 0; t < n; ++t) {
-        store(buf);
-        wait_loads<0>();
-        barrier();
-        if (t + 1 < n) issue(t + 1, next(buf));
-        multiply(buf);
-        buf = next(buf);
-      }
+      run_staged(n, active);
     }
     barrier();  // the stages and rows are free
   };
@@ -333,85 +419,134 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(GArgs g) {
     const int end = c_end;
     for (int c = c_first; c < end; c += kRowsAhead) {
       const int n = min(end - c, kRowsAhead), whole = (n + kStep - 1) / kStep * kStep;
-      for (int r = tid; r < whole; r += kThreads) {
+      for (int r = tid; r < whole + S * kStep; r += kThreads) {
         const int s = r < n ? g.sid[c + r] : -1;
         const bool ok = s >= 0 && s < g.routes;
         l.row[r] = !ok ? -1 : g.sorted ? c + r : s / g.k;
       }
       __syncthreads();
       c_first = c;
-      run(whole / kStep);
+      run(whole / kStep, true);
     }
   } else {
-    run((c_end + kStep - 1) / kStep);
+    run((c_end + kStep - 1) / kStep, has != 0);
   }
 
   // Result register v of lane l: column (of j) 8 (v / 4) + 4 (l / 32) + v mod 4, row (of i)
-  // l mod 32.  A wave turns 32 rows at a time in its part of the LDS into whole chunks of
-  // 16 bytes of the output's rows.
-  constexpr int kSize = F32 ? 4 : 2, kRow = FN * 32 * kSize, kPad = kRow + 16;  // bytes of a row in LDS
+  // l mod 32.  A wave turns 32 rows at a time, and of FP32 half of its columns, in its part
+  // of the LDS into whole chunks of 16 bytes of the output's rows.
+  constexpr int JP = F32 && FN > 1 ? FN / 2 : FN;
+  constexpr int kSize = F32 ? 4 : 2, kRow = JP * 32 * kSize, kPad = kRow + 16;  // bytes of a row in LDS
   static_assert(kWaves * 32 * kPad <= (int)(sizeof(l.a) + sizeof(l.b)), "the results fit");
   char* stage = reinterpret_cast<char*>(&l) + wv * 32 * kPad;
   const int64_t base = DIR == kWeights ? (int64_t)e * g.I : 0;
-  const int rows = DIR == kWeights ? g.I - i0 : BM;
+  const int valid = DIR == kWeights ? g.I - i0 : BM;  // rows to write
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int m0 = wi + i * 32, m = m0 + (lane & 31);
-    const bool ok = m >= 64 ? has[1] >> (m - 64) & 1 : has[0] >> m & 1;
+    const int m0 = wi + i * 32;
+    const bool ok = has >> (i * 32 + (lane & 31)) & 1;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int j1 = 0; j1 < FN; j1 += JP) {
 #pragma unroll
-      for (int v = 0; v < 16; v += 4) {
-        char* at = stage + (lane & 31) * kPad + (j * 32 + 8 * (v / 4) + 4 * (lane >> 5)) * kSize;
-        f32x4 o = {acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]};
-        if (!ok) o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (F32) *reinterpret_cast<f32x4*>(at) = o;
-        else *reinterpret_cast<u32x2*>(at) = u32x2{H::pack(o[0], o[1]), H::pack(o[2], o[3])};
-      }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int j = 0; j < JP; ++j)
 #pragma unroll
-    for (int q = 0; q < 32 * kRow / 1024; ++q) {
-      const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
-      const int n = j0 + wj + c * (16 / kSize);
-      if (m0 + r < rows && n < g.J) {
-        const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
-        const int64_t at = (base + i0 + m0 + r) * g.J + n;
-        if constexpr (F32) {
-          float* out = static_cast<float*>(g.out) + at;
-          if (n + 4 <= g.J) {
-            __builtin_nontemporal_store(o, reinterpret_cast<u32x4_f32*>(out));
+        for (int v = 0; v < 16; v += 4) {
+          char* at = stage + (lane & 31) * kPad + (j * 32 + 8 * (v / 4) + 4 * (lane >> 5)) * kSize;
+          const f32x16& r = acc[i][j1 + j];
+          f32x4 o = {r[v], r[v + 1], r[v + 2], r[v + 3]};
+          if (!ok) o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (F32) *reinterpret_cast<f32x4*>(at) = o;
+          else *reinterpret_cast<u32x2*>(at) = u32x2{H::pack(o[0], o[1]), H::pack(o[2], o[3])};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int q = 0; q < 32 * kRow / 1024; ++q) {
+        const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
+        const int n = j0 + wj + j1 * 32 + c * (16 / kSize);
+        if (m0 + r < valid && n < g.J) {
+          const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
+          const int64_t at = (base + i0 + m0 + r) * g.J + n;
+          if constexpr (F32) {
+            float* out = static_cast<float*>(g.out) + at;
+            if (n + 4 <= g.J) {
+              __builtin_nontemporal_store(o, reinterpret_cast<u32x4_f32*>(out));
+            } else {
+#pragma unroll
+              for (int x = 0; x < 3; ++x)
+                if (n + x < g.J) out[x] = __uint_as_float(o[x]);
+            }
           } else {
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-              if (n + x < g.J) out[x] = __uint_as_float(o[x]);
+            store8(static_cast<uint16_t*>(g.out) + at, o, g.J - n);
           }
-        } else {
-          store8(static_cast<uint16_t*>(g.out) + at, o, g.J - n);
         }
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
 constexpr int kCols = 256;
 
+// Tiles of i for each direction and the number of rows in them.
+template <int DIR, int BM>
+struct ShapeOf;
+#ifndef SH_W
+#define SH_W 256, kCols, 8, 32, 3
+#define SH_F128 128, kCols, 8, 64, 3
+#define SH_F64 64, kCols, 4, 64, 3
+#define SH_F32 32, kCols, 4, 64, 3
+#define SH_F16 16, kCols, 4, 64, 3
+#define SH_R128 128, kCols, 4, 32, 3
+#define SH_R64 64, kCols, 4, 32, 3
+#define SH_R32 32, kCols, 4, 32, 4
+#define SH_R16 16, kCols, 4, 32, 4
+#endif
+template <>
+struct ShapeOf<kForward, 128> : Shape<SH_F128> {};
+template <>
+struct ShapeOf<kForward, 64> : Shape<SH_F64> {};
+template <>
+struct ShapeOf<kForward, 32> : Shape<SH_F32> {};
+template <>
+struct ShapeOf<kForward, 16> : Shape<SH_F16> {};
+template <>
+struct ShapeOf<kRows, 128> : Shape<SH_R128> {};
+template <>
+struct ShapeOf<kRows, 64> : Shape<SH_R64> {};
+template <>
+struct ShapeOf<kRows, 32> : Shape<SH_R32> {};
+template <>
+struct ShapeOf<kRows, 16> : Shape<SH_R16> {};
+template <>
+struct ShapeOf<kWeights, 256> : Shape<SH_W> {};
+
+struct Launch {
+  const void* kernel;
+  int threads;
+};
+
+template <typename H, int DIR, bool F32, bool DA, bool DB, int BM>
+Launch launch_of() {
+  typedef ShapeOf<DIR, BM> P;
+  return {reinterpret_cast<const void*>(k_product<H, DIR, P, F32, DA, DB>), P::kThreads};
+}
+
 template <typename H, int DIR, bool F32, bool DA, bool DB>
-const void* product_kernel(int bm) {
+Launch product_kernel(int bm) {
   if constexpr (DIR == kWeights) {
-    return reinterpret_cast<const void*>(k_product<H, DIR, 128, kCols, F32, DA, DB>);
+    return launch_of<H, DIR, F32, DA, DB, 256>();
   } else {
     switch (bm) {
-      case 128: return reinterpret_cast<const void*>(k_product<H, DIR, 128, kCols, F32, DA, DB>);
-      case 64: return reinterpret_cast<const void*>(k_product<H, DIR, 64, kCols, F32, DA, DB>);
-      case 32: return reinterpret_cast<const void*>(k_product<H, DIR, 32, kCols, F32, DA, DB>);
-      default: return reinterpret_cast<const void*>(k_product<H, DIR, 16, kCols, F32, DA, DB>);
+      case 128: return launch_of<H, DIR, F32, DA, DB, 128>();
+      case 64: return launch_of<H, DIR, F32, DA, DB, 64>();
+      case 32: return launch_of<H, DIR, F32, DA, DB, 32>();
+      default: return launch_of<H, DIR, F32, DA, DB, 16>();
     }
   }
 }
 
 template <typename H, int DIR, bool F32>
-const void* product_kernel(int bm, bool da, bool db) {
+Launch product_kernel(int bm, bool da, bool db) {
   if (da && db) return product_kernel<H, DIR, F32, true, true>(bm);
   // rows along c have one length in both operands
   if constexpr (DIR != kForward) {
@@ -422,7 +557,7 @@ const void* product_kernel(int bm, bool da, bool db) {
 }
 
 template <int DIR>
-const void* product_kernel(int dtype, bool f32, int bm, bool da, bool db) {
+Launch product_kernel(int dtype, bool f32, int bm, bool da, bool db) {
   if (dtype == MRS_DTYPE_BF16)
     return f32 ? product_kernel<BF16, DIR, true>(bm, da, db) : product_kernel<BF16, DIR, false>(bm, da, db);
   return f32 ? product_kernel<FP16, DIR, true>(bm, da, db) : product_kernel<FP16, DIR, false>(bm, da, db);
@@ -453,10 +588,10 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
   int bm;
   int64_t grid;
   if constexpr (DIR == kWeights) {
-    bm = 128;
+    bm = 256;
     g.I = N, g.J = K;
     g.nrt = (N + bm - 1) / bm, g.nct = (K + kCols - 1) / kCols;
-    grid = (int64_t)(E + kXcds - 1) / kXcds * kXcds * g.nrt * g.nct;
+    grid = ((int64_t)E * g.nct + kXcds - 1) / kXcds * kXcds * g.nrt;
   } else {
     bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
     g.C = DIR == kForward ? K : N, g.J = DIR == kForward ? N : K;
@@ -464,16 +599,17 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     g.run = 8;
     grid = ((int64_t)g.nrt + kXcds * g.run - 1) / (kXcds * g.run) * g.run * kXcds * g.nct;
   }
-  if (grid * kThreads > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   // lengths of the operands' rows and their numbers
   const int la = DIR == kForward ? K : N, lb = K;
   const int64_t na = DIR == kForward && !g.sorted ? M : max_rows;
   const int64_t nb = DIR != kWeights ? (int64_t)E * N : g.sorted ? max_rows : M;
   g.a_end = g.a + na * la, g.b_end = g.b + nb * lb;
   const bool da = la % 8 == 0 && aligned_to(a, 16), db = lb % 8 == 0 && aligned_to(b, 16);
+  const Launch p = product_kernel<DIR>(dtype, out_dtype == MRS_DTYPE_F32, bm, da, db);
+  if (grid * p.threads > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   void* params[] = {&g};
-  return hipLaunchKernel(product_kernel<DIR>(dtype, out_dtype == MRS_DTYPE_F32, bm, da, db), dim3((unsigned)grid), dim3(kThreads),
-                         params, 0, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+  return hipLaunchKernel(p.kernel, dim3((unsigned)grid), dim3(p.threads), params, 0,
+                         reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? MRS_OK
              : MRS_ERR_LAUNCH;
 }
