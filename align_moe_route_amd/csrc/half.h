@@ -58,14 +58,18 @@ struct FP16 {
   }
 };
 
-// Eight consecutive 16-bit values at any element's address, zeros past the first n.
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
-  if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+// The first n (up to seven) of eight 16-bit values, the others zero.
+__device__ __forceinline__ u32x4 load_few(const uint16_t* p, int n) {
   uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
     if (i < n) v[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
   return u32x4{v[0], v[1], v[2], v[3]};
+}
+
+// Eight consecutive 16-bit values at any element's address, zeros past the first n.
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
+  return n >= 8 ? *reinterpret_cast<const u32x4_any*>(p) : load_few(p, n);
 }
 
 // The first n of eight values, at any element's address.

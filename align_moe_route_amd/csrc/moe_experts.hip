@@ -20,7 +20,7 @@ namespace {
 enum Dir { kForward, kRows, kWeights };
 
 struct GArgs {
-  const uint16_t *a, *b, *a_end, *b_end;
+  const uint16_t *a, *b;
   const int32_t *sid, *eob, *npp;
   void* out;
   int routes, k, E, block, sorted;
@@ -28,6 +28,7 @@ struct GArgs {
   int row_limit;  // rows the metadata can hold: (max_rows / block) * block
   int nrt, nct;   // tiles of i (over all sorted rows, or of one expert), tiles of j
   int run;        // consecutive row tiles of an XCD
+  bool tiny;      // an operand's rows have fewer than eight values
 };
 
 
@@ -90,16 +91,12 @@ __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
-// Eight values at any element's address, zeros past the first n; `end` is the end of
-// the matrix: a load that stays below it is made whole and its tail cleared.
-__device__ __forceinline__ u32x4 load8_any(const uint16_t* p, int n, const uint16_t* end) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (n <= 0) return v;
-  if (p + 8 > end) return load8(p, n);
-  v = *reinterpret_cast<const u32x4_any*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = n >= 2 * i + 2 ? v[i] : n == 2 * i + 1 ? v[i] & 0xFFFFu : 0u;
-  return v;
+// The eight values without the first n (n >= 0), zeros behind them.
+__device__ __forceinline__ u32x4 drop(u32x4 v, int n) {
+  if (n & 4) v = u32x4{v[2], v[3], 0u, 0u};
+  if (n & 2) v = u32x4{v[1], v[2], v[3], 0u};
+  if (n & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return n < 8 ? v : u32x4{0u, 0u, 0u, 0u};
 }
 
 // First block of [0, n) whose expert is at least e (found for e and e + 1), by 64-ary
@@ -134,18 +131,20 @@ struct Shape {
   static constexpr int WI = BM >= 256 ? 4 : BM >= 128 ? 2 : 1, WJ = NW / WI;  // waves along i and j
   static constexpr int FM = TR / WI / 32, FN = BN / WJ / 32;  // operands of a wave
   static constexpr int kThreads = NW * 64;
+  // workgroups of a compute unit by their LDS (160 KB), and so waves of a SIMD
+  static constexpr int kPerSimd = (NW == 4 && (TR + BN) * STEP * 2 * S <= 76 << 10 ? 2 : 1) * NW / 4;
 };
 
 template <int DIR, typename P>
 struct Ring {
   u32x4 a[P::S][P::TR * P::STEP / 8], b[P::S][P::BN * P::STEP / 8];
-  int32_t row[DIR == kWeights ? kRowsAhead + P::S * P::STEP : P::TR];
+  int32_t row[DIR == kWeights ? kRowsAhead + 4 * P::STEP : P::TR];
 };
 
-// DA, DB: the operand's rows and chunks are whole and 16-byte aligned, and go from
-// memory into LDS; otherwise through registers.
-template <typename H, int DIR, typename P, bool F32, bool DA, bool DB>
-__global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
+// DIRECT: the operands' rows are whole 16-byte chunks at multiples of 16 bytes, and go
+// from memory into LDS; otherwise through registers.
+template <typename H, int DIR, typename P, bool F32, bool DIRECT>
+__global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   constexpr bool kAcrossA = DIR == kWeights, kAcrossB = DIR != kForward;
   constexpr int BM = P::BM, BN = P::BN, TR = P::TR, S = P::S, kStep = P::STEP, kThreads = P::kThreads;
   constexpr int WJ = P::WJ, FM = P::FM, FN = P::FN, kWaves = P::NW;
@@ -194,8 +193,6 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
   const int sr = tid / kChunks, sc = swz<kStep>(sr, tid % kChunks) * 8;
   constexpr int WA = TR / 8, SA = kThreads / WA, WB = BN / 8, SB = kThreads / WB;
   const int ia = i0 + swz_across(tid / WA, tid % WA) * 8, jb = j0 + swz_across(tid / WB, tid % WB) * 8;
-  const uint16_t* const end_a = g.a_end;
-  const uint16_t* const end_b = g.b_end;
   const uint16_t *pa[kAcrossA ? 1 : AP], *pb[DIR == kWeights ? 1 : BP];
   if constexpr (!kAcrossA) {
 #pragma unroll
@@ -210,20 +207,16 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
       pb[p] = g.b + ((int64_t)e * g.J + min(j0 + sr + p * kRowStep, g.J - 1)) * g.C + sc;
   } else if constexpr (DIR == kRows) {
 #pragma unroll
-    for (int p = 0; p < BP; ++p)
-      pb[p] = g.b + ((int64_t)e * g.C + tid / WB + p * SB) * g.J + (DB ? min(jb, g.J - 8) : jb);
+    for (int p = 0; p < BP; ++p) pb[p] = g.b + ((int64_t)e * g.C + tid / WB + p * SB) * g.J;
   }
 
   const uint32_t lds_a = (uint32_t)(uintptr_t)(lds_t)(char*)l.a + (uint32_t)wv * 1024;
   const uint32_t lds_b = (uint32_t)(uintptr_t)(lds_t)(char*)l.b + (uint32_t)wv * 1024;
   const void* const zeros = &kZeros;
-  u32x4 ra[AP], rb[BP];
-
   // kWeights: the sources of a step's rows, -1 for none; the same for both operands where
   // their tiles are equally wide
   constexpr bool kOneMap = WA == WB;
   constexpr int RP = DIR != kWeights ? 1 : kOneMap ? AP : AP + BP;
-  int rows[RP];
   auto find = [&](int (&to)[RP], int t) {
     if constexpr (DIR == kWeights) {
 #pragma unroll
@@ -234,61 +227,96 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
       }
     }
   };
-  // A part of step t of c, a KK-th (all of it where kPart is KK): into stage `buf` of LDS, or
-  // into registers.
-  auto issue = [&](int t, int buf, auto part) {
+  // Chunks whose rows run across the tile: the last chunk of a row ends with it, and so
+  // do the results that come of it (out_of below).
+  const int i_at = min(ia, g.I - 8), j_at = min(jb, g.J - 8);
+  // Chunks along c: where a row ends inside step t its last chunks are read as its last
+  // eight values, and moved down when they have arrived.
+  auto along = [&](int t) {
+    const int c0 = t * kStep;
+    return DIRECT || c0 + kStep <= c_end ? c0 : min(c0 + sc, c_end - 8) - sc;
+  };
+  auto past = [&](int t) { return t * kStep + kStep <= c_end ? 0 : max(t * kStep + sc + 8 - c_end, 0); };
+  auto chunk_a = [&](int t, int p, const int (&rows)[RP]) {
+    if constexpr (!kAcrossA) return pa[p] + along(t);
+    else return g.a + (int64_t)(c_first + t * kStep + tid / WA + p * SA) * g.I + i_at;
+  };
+  auto chunk_b = [&](int t, int p, const int (&rows)[RP]) {
+    if constexpr (DIR == kForward) return pb[p] + along(t);
+    else if constexpr (DIR == kRows) return pb[p] + (int64_t)t * kStep * g.J + j_at;
+    else return g.b + (int64_t)max(rows[kOneMap ? p : AP + p], 0) * g.J + j_at;
+  };
+  // Whether a chunk's row of c (or, along c and straight into LDS, the chunk) exists.
+  auto has_a = [&](int t, int p, const int (&rows)[RP]) {
+    return kAcrossA ? rows[kAcrossA ? p : 0] >= 0 : !DIRECT || t * kStep + sc < c_end;
+  };
+  auto has_b = [&](int t, int p, const int (&rows)[RP]) {
+    return DIR == kForward ? !DIRECT || t * kStep + sc < c_end
+           : DIR == kRows  ? t * kStep + tid / WB + p * SB < c_end
+                           : rows[DIR != kWeights ? 0 : kOneMap ? p : AP + p] >= 0;
+  };
+  // A part of step t of c, a KK-th (all of it where kPart is KK), into stage `buf` of LDS.
+  auto issue = [&](int t, int buf, const int (&rows)[RP], auto part) {
     constexpr int kPart = decltype(part)::value;
     auto mine = [](int q) { return kPart == KK || q * KK / L == kPart; };
-    const int c0 = t * kStep;  // kWeights: from the first of the rows in l.row
 #pragma unroll
     for (int p = 0; p < AP; ++p) {
-      if (!mine(p)) continue;
-      const uint32_t dst = lds_a + (buf * AT + p * kThreads) * 16;
-      if constexpr (!kAcrossA) {
-        if (AT % kThreads == 0 || tid + p * kThreads < AT) {
-          const uint16_t* src = pa[p] + c0;
-          if constexpr (DA) load_lds(c0 + sc < c_end ? src : zeros, dst);
-          else ra[p] = load8_any(src, c_end - c0 - sc, end_a);
-        }
-      } else {
-        const int c = c0 + tid / WA + p * SA;
-        const bool ok = rows[p] >= 0;
-        const uint16_t* src = g.a + (int64_t)(c_first + c) * g.I + (DA ? min(ia, g.I - 8) : ia);
-        if constexpr (DA) load_lds(ok ? src : zeros, dst);
-        else ra[p] = load8_any(src, ok ? g.I - ia : 0, end_a);
-      }
+      if (!mine(p) || (AT % kThreads != 0 && tid + p * kThreads >= AT)) continue;
+      const uint16_t* src = chunk_a(t, p, rows);
+      load_lds(has_a(t, p, rows) ? src : zeros, lds_a + (buf * AT + p * kThreads) * 16);
     }
 #pragma unroll
     for (int p = 0; p < BP; ++p) {
       if (!mine(AP + p)) continue;
-      const uint32_t dst = lds_b + (buf * BN * kChunks + p * kThreads) * 16;
-      if constexpr (DIR == kForward) {
-        const uint16_t* src = pb[p] + c0;
-        if constexpr (DB) load_lds(c0 + sc < c_end ? src : zeros, dst);
-        else rb[p] = load8_any(src, c_end - c0 - sc, end_b);
-      } else if constexpr (DIR == kRows) {
-        const uint16_t* src = pb[p] + (int64_t)c0 * g.J;
-        const bool ok = c0 + tid / WB + p * SB < c_end;
-        if constexpr (DB) load_lds(ok ? src : zeros, dst);
-        else rb[p] = load8_any(src, ok ? g.J - jb : 0, end_b);
+      const uint16_t* src = chunk_b(t, p, rows);
+      load_lds(has_b(t, p, rows) ? src : zeros, lds_b + (buf * BN * kChunks + p * kThreads) * 16);
+    }
+  };
+  // Step t of c asked for into registers, and from there into stage `buf`.  Rows of fewer
+  // than eight values (TINY) are loaded for themselves, one by one.
+  struct Staged {
+    u32x4 a[AP], b[BP];
+    int rows[RP];
+  };
+  typedef const __attribute__((address_space(1))) u32x4_any* any_t;  // a choice of pointers keeps the address space
+  auto fetch = [&](int t, Staged& r, auto tiny) {
+    constexpr bool kTiny = decltype(tiny)::value;
+#pragma unroll
+    for (int p = 0; p < AP; ++p) {
+      if (AT % kThreads != 0 && tid + p * kThreads >= AT) continue;
+      if constexpr (kTiny) {
+        const uint16_t* src = kAcrossA ? chunk_a(t, p, r.rows) - i_at + ia : pa[p] + t * kStep;
+        r.a[p] = load8(src, !has_a(t, p, r.rows) ? 0 : kAcrossA ? g.I - ia : c_end - t * kStep - sc);
       } else {
-        const int row = rows[kOneMap ? p : AP + p];
-        const uint16_t* src = g.b + (int64_t)max(row, 0) * g.J + (DB ? min(jb, g.J - 8) : jb);
-        if constexpr (DB) load_lds(row >= 0 ? src : zeros, dst);
-        else rb[p] = load8_any(src, row >= 0 ? g.J - jb : 0, end_b);
+        const any_t src = (any_t)(const u32x4_any*)chunk_a(t, p, r.rows);
+        r.a[p] = *(has_a(t, p, r.rows) ? src : (any_t)(const u32x4_any*)&kZeros);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < BP; ++p) {
+      if constexpr (kTiny) {
+        const uint16_t* src = kAcrossB ? chunk_b(t, p, r.rows) - j_at + jb : pb[p] + t * kStep;
+        r.b[p] = load8(src, !has_b(t, p, r.rows) ? 0 : kAcrossB ? g.J - jb : c_end - t * kStep - sc);
+      } else {
+        const any_t src = (any_t)(const u32x4_any*)chunk_b(t, p, r.rows);
+        r.b[p] = *(has_b(t, p, r.rows) ? src : (any_t)(const u32x4_any*)&kZeros);
       }
     }
   };
-  auto store = [&](int buf) {
-    if constexpr (!DA) {
+  auto store = [&](int t, int buf, Staged& r, auto tiny) {
+    if (!decltype(tiny)::value && DIR != kWeights && t * kStep + kStep > c_end) {
 #pragma unroll
-      for (int p = 0; p < AP; ++p)
-        if (AT % kThreads == 0 || tid + p * kThreads < AT) l.a[buf][tid + p * kThreads] = ra[p];
-    }
-    if constexpr (!DB) {
+      for (int p = 0; p < AP; ++p) r.a[p] = drop(r.a[p], past(t));
+      if constexpr (DIR == kForward) {
 #pragma unroll
-      for (int p = 0; p < BP; ++p) l.b[buf][tid + p * kThreads] = rb[p];
+        for (int p = 0; p < BP; ++p) r.b[p] = drop(r.b[p], past(t));
+      }
     }
+#pragma unroll
+    for (int p = 0; p < AP; ++p)
+      if (AT % kThreads == 0 || tid + p * kThreads < AT) l.a[buf][tid + p * kThreads] = r.a[p];
+#pragma unroll
+    for (int p = 0; p < BP; ++p) l.b[buf][tid + p * kThreads] = r.b[p];
   };
 
   f32x16 acc[FM][FN];
@@ -317,6 +345,7 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
     constexpr bool kActive = decltype(active)::value;  // a wave without rows only loads
     constexpr int kReads = FM + FN, kMul = FM * FN;
     Operands f[2];
+    int rows[RP];
     // this wave's loads of S - 2 stages may be in flight
     auto wait_stage = [&] {
       if (AT < kThreads && wv >= AT / 64) wait_loads<(S - 2) * BP>();  // it loads no part of A
@@ -325,13 +354,13 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) {
       find(rows, s);
-      issue(s, s, All());
+      issue(s, s, rows, All());
     }
     find(rows, S - 1);
     wait_stage();
     barrier();
     int buf = 0, last = S - 1;  // the stages of step t and of step t + S - 1
-    issue(S - 1, last, std::integral_constant<int, 0>());
+    issue(S - 1, last, rows, std::integral_constant<int, 0>());
     if constexpr (kActive) {
 #pragma unroll
       for (int q = 0; q < kReads; ++q) read_one(f[0], 0, 0, q);
@@ -364,9 +393,9 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
             if constexpr (kk == KK - 1) {
 #pragma unroll
               for (int r = 0; r < RP; ++r) rows[r] = ahead[r];
-              issue(t + S, last, std::integral_constant<int, 0>());
+              issue(t + S, last, rows, std::integral_constant<int, 0>());
             } else {
-              issue(t + S - 1, last, std::integral_constant<int, kk + 1>());
+              issue(t + S - 1, last, rows, std::integral_constant<int, kk + 1>());
             }
             fence();
           }
@@ -381,37 +410,45 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
     }
     wait_loads<0>();
   };
-  // Through registers: a step's are stored when the next one's have been asked for.
-  auto run_staged = [&](int n, bool active) {
-    find(rows, 0);
-    issue(0, 0, All());
+  // Through registers, two steps in flight: a step is stored into LDS when it is its turn,
+  // and the one after the next asked for.
+  auto run_staged = [&](int n, bool active, auto tiny) {
+    Staged r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      find(r[i].rows, i);
+      fetch(i, r[i], tiny);
+    }
     int buf = 0;
-    for (int t = 0; t < n; ++t) {
-      store(buf);
-      wait_loads<0>();
+    auto step = [&](int t, Staged& q) {
+      store(t, buf, q, tiny);
+      find(q.rows, t + 2);
       barrier();
-      if (t + 1 < n) {
-        find(rows, t + 1);
-        issue(t + 1, next(buf), All());
-      }
+      fetch(t + 2, q, tiny);
+      if (active) {
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        if (!active) break;
-        Operands f;
+        for (int kk = 0; kk < KK; ++kk) {
+          Operands f;
 #pragma unroll
-        for (int q = 0; q < FM + FN; ++q) read_one(f, buf, kk, q);
+          for (int x = 0; x < FM + FN; ++x) read_one(f, buf, kk, x);
 #pragma unroll
-        for (int q = 0; q < FM * FN; ++q) multiply_one(f, q);
+          for (int x = 0; x < FM * FN; ++x) multiply_one(f, x);
+        }
       }
       buf = next(buf);
+    };
+    for (int t = 0; t < n; t += 2) {  // a step past the last adds zeros
+      step(t, r[0]);
+      step(t + 1, r[1]);
     }
   };
   auto run = [&](int n, bool active) {
-    if constexpr (DA && DB) {
+    if constexpr (DIRECT) {
       if (active) run_direct(n, std::true_type());
       else run_direct(n, std::false_type());
     } else {
-      run_staged(n, active);
+      if (g.tiny) run_staged(n, active, std::true_type());  // rows of fewer than eight values
+      else run_staged(n, active, std::false_type());
     }
     barrier();  // the stages and rows are free
   };
@@ -419,7 +456,7 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
     const int end = c_end;
     for (int c = c_first; c < end; c += kRowsAhead) {
       const int n = min(end - c, kRowsAhead), whole = (n + kStep - 1) / kStep * kStep;
-      for (int r = tid; r < whole + S * kStep; r += kThreads) {
+      for (int r = tid; r < whole + 4 * kStep; r += kThreads) {
         const int s = r < n ? g.sid[c + r] : -1;
         const bool ok = s >= 0 && s < g.routes;
         l.row[r] = !ok ? -1 : g.sorted ? c + r : s / g.k;
@@ -440,7 +477,14 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
   static_assert(kWaves * 32 * kPad <= (int)(sizeof(l.a) + sizeof(l.b)), "the results fit");
   char* stage = reinterpret_cast<char*>(&l) + wv * 32 * kPad;
   const int64_t base = DIR == kWeights ? (int64_t)e * g.I : 0;
-  const int valid = DIR == kWeights ? g.I - i0 : BM;  // rows to write
+  // Where a row or column of the tile is stored, -1 for nowhere.  Of a chunk of eight that
+  // passes the edge and was read as the last eight, all eight are: those before its own
+  // place are stored twice, the same.
+  auto out_of = [&](int at, int size) {
+    const int first = at & ~7;
+    if (DIRECT || g.tiny) return at < size ? at : -1;
+    return first < size ? at - max(first + 8 - size, 0) : -1;
+  };
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m0 = wi + i * 32;
@@ -462,10 +506,13 @@ __global__ __launch_bounds__(P::kThreads, 2) void k_product(GArgs g) {
 #pragma unroll
       for (int q = 0; q < 32 * kRow / 1024; ++q) {
         const int r = (q * 64 + lane) / (kRow / 16), c = (q * 64 + lane) % (kRow / 16);
-        const int n = j0 + wj + j1 * 32 + c * (16 / kSize);
-        if (m0 + r < valid && n < g.J) {
+        const int m = DIR == kWeights ? out_of(i0 + m0 + r, g.I) : m0 + r < BM ? i0 + m0 + r : -1;
+        // rows of kForward and kRows are one of B's for each j, or one chunk for eight
+        const int j = j0 + wj + j1 * 32 + c * (16 / kSize);
+        const int n = DIR == kForward ? (j < g.J ? j : -1) : out_of(j, g.J);
+        if (m >= 0 && n >= 0) {
           const u32x4 o = *reinterpret_cast<const u32x4*>(stage + r * kPad + c * 16);
-          const int64_t at = (base + i0 + m0 + r) * g.J + n;
+          const int64_t at = (base + m) * g.J + n;
           if constexpr (F32) {
             float* out = static_cast<float*>(g.out) + at;
             if (n + 4 <= g.J) {
@@ -492,6 +539,7 @@ template <int DIR, int BM>
 struct ShapeOf;
 #ifndef SH_W
 #define SH_W 256, kCols, 8, 32, 3
+#define SH_WS 128, 128, 4, 32, 3
 #define SH_F128 128, kCols, 8, 64, 3
 #define SH_F64 64, kCols, 4, 64, 3
 #define SH_F32 32, kCols, 4, 64, 3
@@ -519,48 +567,38 @@ template <>
 struct ShapeOf<kRows, 16> : Shape<SH_R16> {};
 template <>
 struct ShapeOf<kWeights, 256> : Shape<SH_W> {};
+template <>
+struct ShapeOf<kWeights, 128> : Shape<SH_WS> {};
 
 struct Launch {
   const void* kernel;
   int threads;
 };
 
-template <typename H, int DIR, bool F32, bool DA, bool DB, int BM>
+template <typename H, int DIR, bool F32, bool DIRECT, int BM>
 Launch launch_of() {
   typedef ShapeOf<DIR, BM> P;
-  return {reinterpret_cast<const void*>(k_product<H, DIR, P, F32, DA, DB>), P::kThreads};
+  return {reinterpret_cast<const void*>(k_product<H, DIR, P, F32, DIRECT>), P::kThreads};
 }
 
-template <typename H, int DIR, bool F32, bool DA, bool DB>
+template <typename H, int DIR, bool F32, bool DIRECT>
 Launch product_kernel(int bm) {
   if constexpr (DIR == kWeights) {
-    return launch_of<H, DIR, F32, DA, DB, 256>();
+    return launch_of<H, DIR, F32, DIRECT, DIRECT ? 256 : 128>();
   } else {
     switch (bm) {
-      case 128: return launch_of<H, DIR, F32, DA, DB, 128>();
-      case 64: return launch_of<H, DIR, F32, DA, DB, 64>();
-      case 32: return launch_of<H, DIR, F32, DA, DB, 32>();
-      default: return launch_of<H, DIR, F32, DA, DB, 16>();
+      case 128: return launch_of<H, DIR, F32, DIRECT, 128>();
+      case 64: return launch_of<H, DIR, F32, DIRECT, 64>();
+      case 32: return launch_of<H, DIR, F32, DIRECT, 32>();
+      default: return launch_of<H, DIR, F32, DIRECT, 16>();
     }
   }
 }
 
-template <typename H, int DIR, bool F32>
-Launch product_kernel(int bm, bool da, bool db) {
-  if (da && db) return product_kernel<H, DIR, F32, true, true>(bm);
-  // rows along c have one length in both operands
-  if constexpr (DIR != kForward) {
-    if (da) return product_kernel<H, DIR, F32, true, false>(bm);
-    if (db) return product_kernel<H, DIR, F32, false, true>(bm);
-  }
-  return product_kernel<H, DIR, F32, false, false>(bm);
-}
-
-template <int DIR>
-Launch product_kernel(int dtype, bool f32, int bm, bool da, bool db) {
-  if (dtype == MRS_DTYPE_BF16)
-    return f32 ? product_kernel<BF16, DIR, true>(bm, da, db) : product_kernel<BF16, DIR, false>(bm, da, db);
-  return f32 ? product_kernel<FP16, DIR, true>(bm, da, db) : product_kernel<FP16, DIR, false>(bm, da, db);
+template <typename H, int DIR>
+Launch product_kernel(bool f32, int bm, bool direct) {
+  if (direct) return f32 ? product_kernel<H, DIR, true, true>(bm) : product_kernel<H, DIR, false, true>(bm);
+  return f32 ? product_kernel<H, DIR, true, false>(bm) : product_kernel<H, DIR, false, false>(bm);
 }
 
 constexpr int kMaxCols = 1 << 20;
@@ -585,27 +623,26 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
   g.sid = sid, g.eob = eob, g.npp = npp, g.out = out;
   g.routes = M * k, g.k = k, g.E = E, g.block = block, g.sorted = x_rows == MRS_X_SORTED;
   g.row_limit = (int)row_limit;
-  int bm;
+  // lengths of the operands' rows
+  const int la = DIR == kForward ? K : N, lb = K;
+  g.tiny = la < 8 || lb < 8;
+  const bool direct = la % 8 == 0 && aligned_to(a, 16) && lb % 8 == 0 && aligned_to(b, 16), f32 = out_dtype == MRS_DTYPE_F32;
+  int bm, bn = kCols;
   int64_t grid;
   if constexpr (DIR == kWeights) {
-    bm = 256;
+    bm = direct ? 256 : 128, bn = direct ? kCols : 128;
     g.I = N, g.J = K;
-    g.nrt = (N + bm - 1) / bm, g.nct = (K + kCols - 1) / kCols;
+    g.nrt = (N + bm - 1) / bm, g.nct = (K + bn - 1) / bn;
     grid = ((int64_t)E * g.nct + kXcds - 1) / kXcds * kXcds * g.nrt;
   } else {
     bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
     g.C = DIR == kForward ? K : N, g.J = DIR == kForward ? N : K;
-    g.nrt = (int)(row_limit / bm), g.nct = (g.J + kCols - 1) / kCols;
+    g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
     g.run = 8;
     grid = ((int64_t)g.nrt + kXcds * g.run - 1) / (kXcds * g.run) * g.run * kXcds * g.nct;
   }
-  // lengths of the operands' rows and their numbers
-  const int la = DIR == kForward ? K : N, lb = K;
-  const int64_t na = DIR == kForward && !g.sorted ? M : max_rows;
-  const int64_t nb = DIR != kWeights ? (int64_t)E * N : g.sorted ? max_rows : M;
-  g.a_end = g.a + na * la, g.b_end = g.b + nb * lb;
-  const bool da = la % 8 == 0 && aligned_to(a, 16), db = lb % 8 == 0 && aligned_to(b, 16);
-  const Launch p = product_kernel<DIR>(dtype, out_dtype == MRS_DTYPE_F32, bm, da, db);
+  const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, direct)
+                                           : product_kernel<FP16, DIR>(f32, bm, direct);
   if (grid * p.threads > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   void* params[] = {&g};
   return hipLaunchKernel(p.kernel, dim3((unsigned)grid), dim3(p.threads), params, 0,

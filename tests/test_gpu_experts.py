@@ -30,6 +30,9 @@ SHAPES = [
     (64, 12, 4, 1001, 395, 64, 0.1),
     (9, 4, 2, 8, 2048, 16, 0.0),
     (150, 1, 1, 640, 384, 128, 0.0),   # one expert
+    (40, 3, 2, 5, 300, 32, 0.1),       # rows of fewer than eight values on one side
+    (40, 3, 2, 300, 3, 64, 0.0),
+    (200, 2, 1, 9, 15, 128, 0.0),      # just above eight
 ]
 
 
