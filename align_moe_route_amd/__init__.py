@@ -65,7 +65,9 @@ EXPORTED = [
     "moe_route_far_weights",
     "moe_router_backward",
     "moe_grouped_gemm",
+    "moe_grouped_gemm_ex",
     "moe_grouped_gemm_dx",
+    "moe_grouped_gemm_dx_ex",
     "moe_grouped_gemm_dw",
     "moe_swiglu",
     "moe_swiglu_backward",
@@ -147,6 +149,10 @@ def lib() -> ctypes.CDLL:
     L.moe_grouped_gemm_dx.argtypes = [vp, vp, i32, vp, vp, vp] + [i32] * 7 + [vp, vp]
     L.moe_grouped_gemm_dx.restype = i32
     L.moe_grouped_gemm_dw.argtypes = L.moe_grouped_gemm.argtypes
+    L.moe_grouped_gemm_ex.argtypes = L.moe_grouped_gemm.argtypes + [i32]
+    L.moe_grouped_gemm_ex.restype = i32
+    L.moe_grouped_gemm_dx_ex.argtypes = L.moe_grouped_gemm_dx.argtypes + [i32]
+    L.moe_grouped_gemm_dx_ex.restype = i32
     L.moe_grouped_gemm_dw.restype = i32
     L.moe_swiglu.argtypes = [vp, i32, vp, i64, i32, vp, vp]
     L.moe_swiglu.restype = i32

@@ -121,6 +121,7 @@ __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& f
 }
 
 constexpr int kXcds = 8;
+constexpr int kRun = 4;  // consecutive row tiles of an XCD
 constexpr int kRowsAhead = 4096;  // rows of an expert whose sources are kept in LDS at once (kWeights)
 
 // A tile of BM x BN results by NW waves, in steps of STEP values of c, S stages of LDS.
@@ -539,7 +540,7 @@ template <int DIR, int BM>
 struct ShapeOf;
 #ifndef SH_W
 #define SH_W 256, kCols, 8, 32, 3
-#define SH_WS 128, 128, 4, 32, 3
+#define SH_WS 128, 128, 8, 32, 3
 #define SH_F128 128, kCols, 8, 64, 3
 #define SH_F64 64, kCols, 4, 64, 3
 #define SH_F32 32, kCols, 4, 64, 3
@@ -605,10 +606,11 @@ constexpr int kMaxCols = 1 << 20;
 
 template <int DIR>
 int product(const void* a, const void* b, int dtype, const int32_t* sid, const int32_t* eob, const int32_t* npp, int M,
-            int k, int E, int K, int N, int block, int x_rows, int out_dtype, void* out, void* stream) {
+            int k, int E, int K, int N, int block, int x_rows, int out_dtype, void* out, void* stream, int tile = 0) {
   if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K < 1 || K > kMaxCols || N < 1 || N > kMaxCols || block < 16 ||
       block % 16 != 0 || (dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) ||
-      (out_dtype != dtype && out_dtype != MRS_DTYPE_F32) || (x_rows != MRS_X_TOKENS && x_rows != MRS_X_SORTED))
+      (out_dtype != dtype && out_dtype != MRS_DTYPE_F32) || (x_rows != MRS_X_TOKENS && x_rows != MRS_X_SORTED) ||
+      (tile != 0 && ((tile != 16 && tile != 32 && tile != 64 && tile != 128) || block % tile != 0)))
     return MRS_ERR_INVALID_ARG;
   const int64_t max_rows = moe_route_sort_max_rows(M, E, k, block);
   if (max_rows < 0) return MRS_ERR_OVERFLOW;
@@ -630,15 +632,24 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
   int bm, bn = kCols;
   int64_t grid;
   if constexpr (DIR == kWeights) {
-    bm = direct ? 256 : 128, bn = direct ? kCols : 128;
+    typedef ShapeOf<kWeights, 256> Large;
+    typedef ShapeOf<kWeights, 128> Staged;
+    bm = direct ? Large::BM : Staged::BM, bn = direct ? Large::BN : Staged::BN;
     g.I = N, g.J = K;
     g.nrt = (N + bm - 1) / bm, g.nct = (K + bn - 1) / bn;
     grid = ((int64_t)E * g.nct + kXcds - 1) / kXcds * kXcds * g.nrt;
   } else {
-    bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
     g.C = DIR == kForward ? K : N, g.J = DIR == kForward ? N : K;
+    // The largest tile that divides the block, but a smaller one where fewer than 128
+    // workgroups would come of it (us; 300 tokens of 8 experts, top-2, K 2048, N 1024, blocks
+    // of 128: tiles of 128 26.8, 64 21.5, 32 17.3; 777 tokens of 24, top-6, K 1000, N 400: 19.1,
+    // 16.6, 26.7).
+    bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
+    const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E;
+    while (bm > 32 && used * ((routes / used + bm - 1) / bm) * ((g.J + bn - 1) / bn) < 128) bm /= 2;
+    if (tile != 0) bm = tile;
     g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
-    g.run = 8;
+    g.run = kRun;
     grid = ((int64_t)g.nrt + kXcds * g.run - 1) / (kXcds * g.run) * g.run * kXcds * g.nct;
   }
   const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, direct)
@@ -653,18 +664,32 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
 
 }  // namespace
 
+extern "C" int moe_grouped_gemm_ex(const void* x, const void* w, int dtype, const int32_t* sorted_ids,
+                                   const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E,
+                                   int K, int N, int block, int x_rows, int y_dtype, void* y, void* stream, int tile) {
+  return product<kForward>(x, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, x_rows, y_dtype,
+                           y, stream, tile);
+}
+
 extern "C" int moe_grouped_gemm(const void* x, const void* w, int dtype, const int32_t* sorted_ids,
                                 const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E, int K,
                                 int N, int block, int x_rows, int y_dtype, void* y, void* stream) {
-  return product<kForward>(x, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, x_rows, y_dtype,
-                           y, stream);
+  return moe_grouped_gemm_ex(x, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, x_rows,
+                             y_dtype, y, stream, 0);
+}
+
+extern "C" int moe_grouped_gemm_dx_ex(const void* dy, const void* w, int dtype, const int32_t* sorted_ids,
+                                      const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E,
+                                      int K, int N, int block, int dx_dtype, void* dx, void* stream, int tile) {
+  return product<kRows>(dy, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, MRS_X_SORTED,
+                        dx_dtype, dx, stream, tile);
 }
 
 extern "C" int moe_grouped_gemm_dx(const void* dy, const void* w, int dtype, const int32_t* sorted_ids,
                                    const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E,
                                    int K, int N, int block, int dx_dtype, void* dx, void* stream) {
-  return product<kRows>(dy, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, MRS_X_SORTED,
-                        dx_dtype, dx, stream);
+  return moe_grouped_gemm_dx_ex(dy, w, dtype, sorted_ids, expert_of_block, num_post_pad, M, k, E, K, N, block, dx_dtype,
+                                dx, stream, 0);
 }
 
 extern "C" int moe_grouped_gemm_dw(const void* dy, const void* x, int dtype, const int32_t* sorted_ids,

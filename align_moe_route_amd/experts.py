@@ -70,7 +70,7 @@ def _sizes(M: int, E: int, k: int, block: int):
 
 
 def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block: int, *, tokens: Optional[int] = None,
-                 out_dtype=None, out=None, stream=None):
+                 out_dtype=None, out=None, stream=None, tile: int = 0):
     """16-bit product grouped by expert over the route-sort metadata
     (moe_grouped_gemm): y[r] = x[row(r)] . w[expert_of_block[r // block]]^T for sorted
     rows below num_post_pad, zeros for padding rows.
@@ -78,7 +78,9 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     x: [M, K] bfloat16 or float16, row(r) = sorted_ids[r] // k; with `tokens` = M given
     x holds max_rows rows in sorted order and row(r) = r.  w: [E, N, K] of x's type.
     Any K and N; block: a multiple of 16.  out_dtype: x's type (default) or float32.
-    Returns y [max_rows, N]; rows at or past num_post_pad are left as they were."""
+    Returns y [max_rows, N]; rows at or past num_post_pad are left as they were.  tile:
+    rows of a tile (16, 32, 64 or 128, dividing block) in place of the choice by sizes,
+    for tests and tuning."""
     _matrix(x, 2, "x")
     dt, dev = _code(x.dtype, "x"), x.device
     _matrix(w, 3, "w", dev, x.dtype)
@@ -95,10 +97,10 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     out_dtype = out_dtype or (x.dtype if out is None else out.dtype)
     odt = dt if out_dtype == x.dtype else _code(out_dtype, "out", True)
     out = _output(out, (max(rows, 1), N), out_dtype, dev, foreign, rows)
-    rc = int(lib().moe_grouped_gemm(x.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(), expert_of_block.data_ptr(),
-                                    num_post_pad.data_ptr(), M, k, E, K, N, block,
-                                    MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
-                                    _handle(stream, dev)))
+    rc = int(lib().moe_grouped_gemm_ex(x.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
+                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
+                                       MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
+                                       _handle(stream, dev), tile))
     if foreign is not None:
         _hold(foreign, x, w, sorted_ids, expert_of_block, num_post_pad, out)
     _raise(rc)
@@ -106,14 +108,14 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
 
 
 def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: int, k: int, block: int, *,
-                    out_dtype=None, out=None, stream=None):
+                    out_dtype=None, out=None, stream=None, tile: int = 0):
     """Gradient of grouped_gemm's x in sorted rows (moe_grouped_gemm_dx): dx[r] = dy[r] .
     w[expert_of_block[r // block]], zeros for padding rows.
 
     dy: [max_rows, N], w: [E, N, K] of dy's type (bfloat16 or float16), tokens: M.
     Returns dx [max_rows, K] of dy's type (default) or float32; rows at or past
     num_post_pad are left as they were.  Of an x that holds the tokens' rows the
-    gradient is combine(dx, slot_rows(...))."""
+    gradient is combine(dx, slot_rows(...)).  tile: as for grouped_gemm."""
     _matrix(dy, 2, "dy")
     dt, dev = _code(dy.dtype, "dy"), dy.device
     _matrix(w, 3, "w", dev, dy.dtype)
@@ -130,9 +132,9 @@ def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: in
     out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
     odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
     out = _output(out, (max(rows, 1), K), out_dtype, dev, foreign, rows)
-    rc = int(lib().moe_grouped_gemm_dx(dy.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
-                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block, odt,
-                                       out.data_ptr(), _handle(stream, dev)))
+    rc = int(lib().moe_grouped_gemm_dx_ex(dy.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
+                                          expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block, odt,
+                                          out.data_ptr(), _handle(stream, dev), tile))
     if foreign is not None:
         _hold(foreign, dy, w, sorted_ids, expert_of_block, num_post_pad, out)
     _raise(rc)

@@ -59,6 +59,15 @@ int moe_grouped_gemm_dx(const void* dy, const void* w, int dtype, const int32_t*
                         const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E, int K, int N,
                         int block, int dx_dtype, void* dx, void* stream);
 
+/* The two products above by tiles of `tile` rows (16, 32, 64 or 128, dividing block; 0
+ * for the choice by sizes), for tests and tuning: the same results. */
+int moe_grouped_gemm_ex(const void* x, const void* w, int dtype, const int32_t* sorted_ids,
+                        const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E, int K, int N,
+                        int block, int x_rows, int y_dtype, void* y, void* stream, int tile);
+int moe_grouped_gemm_dx_ex(const void* dy, const void* w, int dtype, const int32_t* sorted_ids,
+                           const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E, int K,
+                           int N, int block, int dx_dtype, void* dx, void* stream, int tile);
+
 /*
  * moe_grouped_gemm_dw -- the gradient of moe_grouped_gemm's w:
  * dw[e, n, c] = sum of dy[r, n] * x[row(r), c] over e's rows that are no padding

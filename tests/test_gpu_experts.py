@@ -74,6 +74,41 @@ def test_products(shape, by_tokens, f32, dtype):
     assert torch.equal(dw, amr.grouped_gemm_dw(dy, x, E, *r.meta, k, block, tokens=tokens, out_dtype=odt))
 
 
+@pytest.mark.parametrize("K,N", [(200, 72), (1096, 520), (203, 77), (64, 1040), (771, 9)])
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
+def test_tiles(tile, K, N):
+    """Every tile size, with rows of whole chunks and of others, short and long sums, tiles
+    whose waves have no row with a slot, and both kinds of x rows."""
+    M, E, k, block = 330, 5, 2, 128
+    r = Routed(ids_of(M, E, k, 21, 0.1), E, block)
+    args = (r.sid, r.eob, r.npp, M, k, block)
+    for t, odt in ((torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32)):
+        x, w = normal((M, K), t, 22), normal((E, N, K), t, 23, K ** -0.5)
+        xr, dy = normal((r.cap, K), t, 24), normal((r.cap, N), t, 25)
+        y = amr.grouped_gemm(x, w, *r.meta, k, block, out_dtype=odt, tile=tile)
+        check(y[:r.npp], *orc.product(f64(x), f64(w), *args, True), steps(K), odt)
+        y = amr.grouped_gemm(xr, w, *r.meta, k, block, tokens=M, out_dtype=odt, tile=tile)
+        check(y[:r.npp], *orc.product(f64(xr), f64(w), *args, False), steps(K), odt)
+        dx = amr.grouped_gemm_dx(dy, w, *r.meta, M, k, block, out_dtype=odt, tile=tile)
+        check(dx[:r.npp], *orc.product_dx(f64(dy), f64(w), *args), steps(N), odt)
+
+
+@pytest.mark.parametrize("K,N,rows", [(520, 776, 5000), (203, 301, 4500)])
+def test_many_rows_of_an_expert(K, N, rows):
+    """Sums over more rows than are kept at a time, beside an expert of few."""
+    ids = np.zeros((rows, 1), dtype=np.int32)
+    ids[::600] = 1
+    r = Routed(ids, 2, 64)
+    x, dy = normal((rows, K), torch.bfloat16, 26), normal((r.cap, N), torch.bfloat16, 27)
+    s = r.sid[:r.npp]
+    xs, ds = f64(x), f64(dy)
+    for out in (torch.bfloat16, torch.float32):
+        dw = amr.grouped_gemm_dw(dy, x, 2, *r.meta, 1, 64, out_dtype=out)
+        for e in range(2):
+            at = np.flatnonzero(r.live & (r.eob[np.arange(r.npp) // 64] == e))
+            check(dw[e], ds[at].T @ xs[s[at]], np.abs(ds[at]).T @ np.abs(xs[s[at]]), steps(len(at)), out)
+
+
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
 @pytest.mark.parametrize("wide", [False, True])
 def test_padding_rows_hold_nothing(block, wide):

@@ -27,6 +27,14 @@ def test_product_codes(kw, code, which):
     assert product(which=which, **kw) == code
 
 
+@pytest.mark.parametrize("tile,code", [(8, -1), (48, -1), (256, -1), (128, -1), (-16, -1), (32, 0)])
+def test_tile_codes(tile, code):
+    """64 divides neither by 48 nor by 128; no token, so no launch."""
+    L = amr.lib()
+    assert L.moe_grouped_gemm_ex(P, P, 1, P, P, P, 0, 2, 8, 40, 24, 64, 0, 1, P, None, tile) == code
+    assert L.moe_grouped_gemm_dx_ex(P, P, 1, P, P, P, 0, 2, 8, 40, 24, 64, 1, P, None, tile) == code
+
+
 def test_no_tokens_need_no_launch():
     assert product(M=0) == 0 and product(M=0, which="_dx") == 0
     assert product(rows=2) == -1 and product(rows=2, which="_dw") == -1
