@@ -654,6 +654,8 @@ def _empty(shape, dtype, dev):
         return torch.empty_strided(shape, (1,), dtype=dtype, device=dev)
     if len(shape) == 2:
         return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=dev)
+    if len(shape) == 3:
+        return torch.empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype=dtype, device=dev)
     return torch.empty(shape, dtype=dtype, device=dev)
 
 

@@ -67,6 +67,14 @@ __device__ __forceinline__ u32x4 load_few(const uint16_t* p, int n) {
   return u32x4{v[0], v[1], v[2], v[3]};
 }
 
+// The eight values without the first n (n >= 0), zeros behind them.
+__device__ __forceinline__ u32x4 drop(u32x4 v, int n) {
+  if (n & 4) v = u32x4{v[2], v[3], 0u, 0u};
+  if (n & 2) v = u32x4{v[1], v[2], v[3], 0u};
+  if (n & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return n < 8 ? v : u32x4{0u, 0u, 0u, 0u};
+}
+
 // Eight consecutive 16-bit values at any element's address, zeros past the first n.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
   return n >= 8 ? *reinterpret_cast<const u32x4_any*>(p) : load_few(p, n);

@@ -91,14 +91,6 @@ __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
-// The eight values without the first n (n >= 0), zeros behind them.
-__device__ __forceinline__ u32x4 drop(u32x4 v, int n) {
-  if (n & 4) v = u32x4{v[2], v[3], 0u, 0u};
-  if (n & 2) v = u32x4{v[1], v[2], v[3], 0u};
-  if (n & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
-  return n < 8 ? v : u32x4{0u, 0u, 0u, 0u};
-}
-
 // First block of [0, n) whose expert is at least e (found for e and e + 1), by 64-ary
 // search: the experts of used blocks ascend.
 __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& first, int& last) {

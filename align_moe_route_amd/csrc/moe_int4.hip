@@ -139,15 +139,31 @@ struct Magic<FP16> {  // 10 bits: 16 + c = 0x4C00 | c << 6
   static constexpr uint32_t ones = 0x3C003C00u;
 };
 
-// codes i and i + 4 of a dword as 16 + c
+// Codes i and i + 4 of a dword as 16 + c.  The constants are in registers (`mask`, `base`):
+// as literals they would cost an instruction each.
 template <typename H>
-__device__ __forceinline__ uint32_t pair_of(uint32_t q, int i) {
-  typedef Magic<H> G;
-  const int up = G::at - 4 * i;
-  return ((up >= 0 ? q << up : q >> -up) & G::mask) | G::base;
+__device__ __forceinline__ uint32_t pair_of(uint32_t q, int i, uint32_t mask, uint32_t base) {
+  const int up = Magic<H>::at - 4 * i;
+  return ((up >= 0 ? q << up : q >> -up) & mask) | base;
 }
 
-template <typename H, int MODE, int GROUP, int L, int R>
+// Sum over L neighbouring lanes, in the last of them.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v = add_dpp<0x111>(v);  // row_shr:1, 2, 4, 8
+  v = add_dpp<0x112>(v);
+  v = add_dpp<0x114>(v);
+  if (L >= 16) v = add_dpp<0x118>(v);
+  if (L >= 32) v = add_dpp<0x142>(v);  // the last lane of the row before
+  if (L >= 64) v = add_dpp<0x143>(v);  // lane 31
+  return v;
+}
+
+template <typename H, int MODE, int GROUP, int L, int R, int U>
 __global__ __launch_bounds__(kThreads) void k_matvec(MArgs a) {
   constexpr int kSets = 64 / L;  // rows a wave works on at once
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -160,105 +176,140 @@ __global__ __launch_bounds__(kThreads) void k_matvec(MArgs a) {
   const int total = MODE == MRS_INT4_SUM ? a.k * a.chunks : a.chunks;
   int e = 0;
   if constexpr (MODE != MRS_INT4_SUM) {
-    e = a.ids[unit];
+    e = __builtin_amdgcn_readfirstlane(a.ids[unit]);
     if (e < 0 || e >= a.E) {
       for (int o = lane; o < kOut * kSets; o += 64)
         if (n0 + o < a.out) a.y[(int64_t)unit * a.out + n0 + o] = 0;
       return;
     }
   }
-  int row[R];
+  uint32_t row[R];  // first chunk of a lane's rows, counted from the expert's
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int n = n0 + (r % kOut) * kSets + sub;
-    row[r] = min(n, a.out - 1) + (r >= kOut ? a.out : 0);
+    row[r] = (uint32_t)(min(n, a.out - 1) + (r >= kOut ? a.out : 0)) * (uint32_t)a.chunks;
   }
+  uint32_t mask = Magic<H>::mask, base = Magic<H>::base;
+  asm volatile("" : "+v"(mask), "+v"(base));
+  const int64_t matrix = (int64_t)a.N * a.chunks;  // chunks of an expert
   float acc[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) acc[r] = 0.0f;
-  for (int q = q0; q < total; q += L) {
-    int64_t slot = unit;
-    int c = q;
-    float v = 1.0f;
-    bool ok = true;
-    if constexpr (MODE == MRS_INT4_SUM) {
-      const int j = (int)__umulhi((uint32_t)q, a.chunks_mul);  // q / chunks
-      c = q - j * a.chunks;
-      slot = (int64_t)unit * a.k + j;
-      e = a.ids[slot];
-      v = a.v[slot];
-      ok = e >= 0 && e < a.E;
-      e = ok ? e : 0;
+  for (int b = 0; b < total; b += L * U) {
+    u32x4 w[U][R], x[U][4];
+    float sc[U][R], v[U];
+    int left[U];  // values of x from a lane's chunk on, at most those of its row
+    // everything that U chunks need is asked for before the first is used
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u * L >= total) continue;
+      const int q = min(b + u * L + q0, total - 1);  // lanes past the last chunk repeat it and add nothing
+      bool ok = b + u * L + q0 < total;
+      int64_t slot = unit;
+      int c = q, eu = e;
+      v[u] = 1.0f;
+      if constexpr (MODE == MRS_INT4_SUM) {
+        const int j = (int)__umulhi((uint32_t)q, a.chunks_mul);  // q / chunks
+        c = q - j * a.chunks;
+        slot = (int64_t)unit * a.k + j;
+        eu = a.ids[slot];
+        v[u] = a.v[slot];
+        ok = ok && eu >= 0 && eu < a.E;
+        eu = eu >= 0 && eu < a.E ? eu : 0;
+      }
+      left[u] = ok ? a.K - c * 32 : 0;
+      const int64_t xr = MODE == MRS_INT4_SUM ? (a.per_slot ? slot : unit) : (a.per_slot ? slot : slot / a.k);
+      const uint16_t* xp = a.x + xr * a.K;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        if (a.K >= 8) x[u][d] = *reinterpret_cast<const u32x4_any*>(xp + min(c * 32 + d * 8, a.K - 8));
+        else x[u][d] = load_few(xp, d == 0 && c == 0 ? a.K : 0);
+      }
+      const u32x4* codes = reinterpret_cast<const u32x4*>(a.codes) + eu * matrix;
+      const uint16_t* scales = a.scales + eu * matrix / (GROUP / 32);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t at = row[r] + (uint32_t)c;
+        w[u][r] = codes[at];
+        sc[u][r] = H::lo(scales[at / (GROUP / 32)]);
+        if (!ok) sc[u][r] = 0.0f;  // neither a scale's NaN nor a weight's
+      }
+      if (!ok) v[u] = 0.0f;
     }
-    const int64_t xr = MODE == MRS_INT4_SUM ? (a.per_slot ? slot : unit) : (a.per_slot ? slot : slot / a.k);
-    u32x4 w[R];
-    float sc[R];
-    const int64_t at = (int64_t)e * a.N;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.codes) + (at + row[r]) * a.chunks + c);
-      sc[r] = H::lo(a.scales[((at + row[r]) * a.chunks + c) / (GROUP / 32)]);
-    }
-    const uint16_t* x = a.x + xr * a.K + c * 32;
-    uint32_t xs[16];
-    float total_x = 0.0f;
+    for (int u = 0; u < U; ++u) {
+      if (b + u * L >= total) continue;
+      if (a.K >= 8 && __ballot(left[u] < 32)) {  // the row ends in some lane's chunk: its last eight values, moved down
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const u32x4 p = load8(x + d * 8, a.K - c * 32 - d * 8);
-      // pairs (i, i + 4) of eight values: halves of dwords i / 2 and i / 2 + 2
-      xs[4 * d] = __builtin_amdgcn_perm(p[2], p[0], 0x05040100u);
-      xs[4 * d + 1] = __builtin_amdgcn_perm(p[2], p[0], 0x07060302u);
-      xs[4 * d + 2] = __builtin_amdgcn_perm(p[3], p[1], 0x05040100u);
-      xs[4 * d + 3] = __builtin_amdgcn_perm(p[3], p[1], 0x07060302u);
-    }
+        for (int d = 0; d < 4; ++d) x[u][d] = drop(x[u][d], min(max(d * 8 + 8 - left[u], 0), 8));
+      }
+      uint32_t xs[16];
+      float total_x = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) total_x = H::dot2(xs[i], Magic<H>::ones, total_x);
+      for (int d = 0; d < 4; ++d) {
+        const u32x4 p = x[u][d];
+        // pairs (i, i + 4) of eight values: halves of dwords i / 2 and i / 2 + 2
+        xs[4 * d] = __builtin_amdgcn_perm(p[2], p[0], 0x05040100u);
+        xs[4 * d + 1] = __builtin_amdgcn_perm(p[2], p[0], 0x07060302u);
+        xs[4 * d + 2] = __builtin_amdgcn_perm(p[3], p[1], 0x05040100u);
+        xs[4 * d + 3] = __builtin_amdgcn_perm(p[3], p[1], 0x07060302u);
+      }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float dot = -24.0f * total_x;
+      for (int i = 0; i < 16; ++i) total_x = H::dot2(xs[i], Magic<H>::ones, total_x);
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
+      for (int r = 0; r < R; ++r) {
+        float dot = -24.0f * total_x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dot = H::dot2(pair_of<H>(w[r][d], i), xs[4 * d + i], dot);
-      if constexpr (MODE == MRS_INT4_SUM) acc[r] += ok ? v * (sc[r] * dot) : 0.0f;
-      else acc[r] += sc[r] * dot;
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot = H::dot2(pair_of<H>(w[u][r][d], i, mask, base), xs[4 * d + i], dot);
+        acc[r] += MODE == MRS_INT4_SUM ? v[u] * (sc[u][r] * dot) : sc[u][r] * dot;
+      }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int d = 1; d < L; d *= 2) acc[r] += __shfl_xor(acc[r], d);
+  for (int r = 0; r < R; ++r) acc[r] = lanes_sum<L>(acc[r]);
 #pragma unroll
   for (int r = 0; r < kOut; ++r) {
     const int n = n0 + r * kSets + sub;
     float o = acc[r];
     if constexpr (MODE == MRS_INT4_GATED) o = o / (1.0f + __expf(-o)) * acc[r + kOut];
-    if (q0 == 0 && n < a.out) a.y[(int64_t)unit * a.out + n] = (uint16_t)H::pack(o, 0.0f);
+    if (q0 == L - 1 && n < a.out) a.y[(int64_t)unit * a.out + n] = (uint16_t)H::pack(o, 0.0f);
+  }
+}
+
+struct MShape {
+  int lanes, rows;  // lanes that share a row, row sets of a wave
+};
+
+template <typename H, int MODE, int GROUP, int R>
+const void* matvec_kernel(int lanes) {
+  constexpr int U = R == 4 ? 2 : 1;
+  switch (lanes) {
+    case 8: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 8, R, U>);
+    case 16: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 16, R, U>);
+    case 32: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 32, R, U>);
+    default: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 64, R, U>);
   }
 }
 
 template <typename H, int MODE, int GROUP>
-const void* matvec_kernel(int lanes) {
-  switch (lanes) {
-    case 8: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 8, 4>);
-    case 16: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 16, 4>);
-    case 32: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 32, 4>);
-    default: return reinterpret_cast<const void*>(k_matvec<H, MODE, GROUP, 64, 4>);
-  }
+const void* matvec_kernel(MShape s) {
+  return s.rows == 4 ? matvec_kernel<H, MODE, GROUP, 4>(s.lanes) : matvec_kernel<H, MODE, GROUP, 8>(s.lanes);
 }
 
 template <typename H, int MODE>
-const void* matvec_kernel(int group, int lanes) {
-  return group == 32 ? matvec_kernel<H, MODE, 32>(lanes)
-         : group == 64 ? matvec_kernel<H, MODE, 64>(lanes)
-                       : matvec_kernel<H, MODE, 128>(lanes);
+const void* matvec_kernel(int group, MShape s) {
+  return group == 32 ? matvec_kernel<H, MODE, 32>(s)
+         : group == 64 ? matvec_kernel<H, MODE, 64>(s)
+                       : matvec_kernel<H, MODE, 128>(s);
 }
 
 template <typename H>
-const void* matvec_kernel(int mode, int group, int lanes) {
-  return mode == MRS_INT4_PLAIN   ? matvec_kernel<H, MRS_INT4_PLAIN>(group, lanes)
-         : mode == MRS_INT4_GATED ? matvec_kernel<H, MRS_INT4_GATED>(group, lanes)
-                                  : matvec_kernel<H, MRS_INT4_SUM>(group, lanes);
+const void* matvec_kernel(int mode, int group, MShape s) {
+  return mode == MRS_INT4_PLAIN   ? matvec_kernel<H, MRS_INT4_PLAIN>(group, s)
+         : mode == MRS_INT4_GATED ? matvec_kernel<H, MRS_INT4_GATED>(group, s)
+                                  : matvec_kernel<H, MRS_INT4_SUM>(group, s);
 }
 
 bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
@@ -299,6 +350,7 @@ extern "C" int moe_int4_matvec(const void* x, int dtype, const uint8_t* codes, c
       (dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) || mode < MRS_INT4_PLAIN || mode > MRS_INT4_SUM ||
       (mode == MRS_INT4_GATED && N % 2 != 0) || (weights != nullptr) != (mode == MRS_INT4_SUM))
     return MRS_ERR_INVALID_ARG;
+  if ((int64_t)N * ((K + 127) / 128 * 4) > INT32_MAX / 16) return MRS_ERR_OVERFLOW;  // 32-bit offsets in a matrix
   if (M == 0) return MRS_OK;
   if (!x || !codes || !scales || !ids || !y) return MRS_ERR_NULL_POINTER;
   if (!aligned_to(x, 2) || !aligned_to(codes, 16) || !aligned_to(scales, 2) || !aligned_to(ids, 4) ||
@@ -309,13 +361,23 @@ extern "C" int moe_int4_matvec(const void* x, int dtype, const uint8_t* codes, c
           mode == MRS_INT4_GATED ? N / 2 : N, 0, 0};
   a.chunks_mul = (uint32_t)(((uint64_t(1) << 32) + a.chunks - 1) / a.chunks);
   const int total = mode == MRS_INT4_SUM ? k * a.chunks : a.chunks;
-  const int lanes = total >= 64 ? 64 : total >= 32 ? 32 : total >= 16 ? 16 : 8;
-  const int outs = (mode == MRS_INT4_GATED ? 2 : 4) * (64 / lanes) * (kThreads / 64);  // of a workgroup
-  a.tiles = (a.out + outs - 1) / outs;
   const int64_t units = mode == MRS_INT4_SUM ? M : (int64_t)M * k;
+  // Eight row sets share the work on x, four with two chunks at once come to more waves
+  // with more in flight: the rule's border is where the times cross (us, 8 / 4; workgroups
+  // of 8: one token of 896 experts, top-16, K 3584, N 768 gated, 384: 9.8 / 8.3; 4 tokens,
+  // 1536: 19.0 / 20.7; 64 tokens, 24576: 248 / 278; the sum of K 384, N 3584, 112: 7.9 / 6.2;
+  // 33 tokens, top-4 of 64, K 1001, N 515, 1188: 11.0 / 11.6; 40 tokens, top-4 of 16, K 500,
+  // N 600, 800: 8.2 / 7.5).
+  MShape shape{total >= 64 ? 64 : total >= 32 ? 32 : total >= 16 ? 16 : 8, 8};
+  auto tiles = [&] {
+    const int outs = (mode == MRS_INT4_GATED ? shape.rows / 2 : shape.rows) * (64 / shape.lanes) * (kThreads / 64);
+    return (a.out + outs - 1) / outs;
+  };
+  if (units * tiles() < 1024) shape.rows = 4;
+  a.tiles = tiles();
   const int64_t grid = units * a.tiles;
   if (grid * kThreads > UINT32_MAX) return MRS_ERR_OVERFLOW;
-  const void* fn = dtype == MRS_DTYPE_BF16 ? matvec_kernel<BF16>(mode, group, lanes) : matvec_kernel<FP16>(mode, group, lanes);
+  const void* fn = dtype == MRS_DTYPE_BF16 ? matvec_kernel<BF16>(mode, group, shape) : matvec_kernel<FP16>(mode, group, shape);
   void* params[] = {&a};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kThreads), params, 0, reinterpret_cast<hipStream_t>(stream)) ==
                  hipSuccess

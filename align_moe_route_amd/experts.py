@@ -40,7 +40,9 @@ def _matrix(t, dims: int, name: str, dev=None, dtype=None):
 
 def _no_grad(what: str, *tensors):
     import torch
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    for t in tensors:
+        if t is None or not t.requires_grad or not torch.is_grad_enabled():
+            continue
         raise ValueError(f"{what} takes no part in autograd: call it under no_grad with its backward entry point, "
                          "or use experts_train")
 
@@ -391,15 +393,16 @@ class Int4(NamedTuple):
 def _group_of(q, dev, dims: int, name: str) -> int:
     """q holds contiguous int4 rows with `dims` dimensions on dev; returns the group."""
     import torch
-    if not isinstance(q, Int4):
-        raise ValueError(f"{name} must be an Int4")
-    _matrix(q.codes, dims, f"{name}.codes", dev, torch.uint8)
-    _matrix(q.scales, dims, f"{name}.scales", dev)
-    Kp, n = q.codes.shape[-1] * 2, q.scales.shape[-1]
-    if Kp == 0 or Kp % 128 or q.codes.shape[:-1] != q.scales.shape[:-1] or n == 0 or Kp % n or Kp // n not in (32, 64, 128):
-        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows, Kp a multiple of "
-                         "128, group 32, 64 or 128")
-    return Kp // n
+    codes, scales = q if isinstance(q, Int4) else (None, None)
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.device == dev
+            and scales.device == dev and codes.dtype == torch.uint8 and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name} must be an Int4 of contiguous tensors, uint8 codes and scales, on {dev}")
+    *lead, Kb = codes.shape
+    *same, n = scales.shape
+    if len(lead) != dims - 1 or lead != same or Kb == 0 or Kb % 64 or n == 0 or 2 * Kb % n or 2 * Kb // n not in (32, 64, 128):
+        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows with {dims} dimensions, "
+                         "Kp a multiple of 128, group 32, 64 or 128")
+    return 2 * Kb // n
 
 
 def _new_int4(lead, Kp: int, group: int, u8, dtype, dev) -> Int4:
@@ -451,27 +454,31 @@ def int4_matvec(x, w: Int4, ids, *, gated: bool = False, weights=None, out=None,
     gives zeros.  Returns p [M, k, N]; with `gated` [M, k, N / 2], silu(p[..., :N / 2]) *
     p[..., N / 2:]; with weights (float32 [M, k]) their sum over the picks [M, N]."""
     import torch
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (2, 3) and x.is_contiguous()):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.is_contiguous()):
         raise ValueError("x must be a contiguous [M, K] or [M, k, K] GPU tensor")
-    dt, dev = _code(x.dtype, "x"), x.device
-    group = _group_of(w, dev, 3, "w")
-    if w.scales.dtype != x.dtype:
-        raise ValueError("w's scales must have x's type")
-    _matrix(ids, 2, "ids", dev, torch.int32)
+    xdt, dev, xshape = x.dtype, x.device, x.shape
+    dt = _code(xdt, "x")
+    if not (isinstance(ids, torch.Tensor) and ids.dtype == torch.int32 and ids.device == dev and ids.is_contiguous()
+            and ids.dim() == 2):
+        raise ValueError(f"ids must be a contiguous int32 [M, k] tensor on {dev}")
     M, k = ids.shape
+    group = _group_of(w, dev, 3, "w")
+    if w.scales.dtype != xdt:
+        raise ValueError("w's scales must have x's type")
     E, N, half = w.codes.shape
-    K = x.shape[-1]
-    if tuple(x.shape[:-1]) != ((M,) if x.dim() == 2 else (M, k)) or (K + 127) // 128 * 128 != half * 2:
+    K, slots = xshape[-1], len(xshape) == 3
+    if xshape[:-1] != ((M, k) if slots else (M,)) or (K + 127) // 128 * 64 != half:
         raise ValueError(f"x must have shape ({M}, K) or ({M}, {k}, K), K columns of w")
     if gated and (weights is not None or N % 2):
         raise ValueError("gated results need an even N and take no weights")
-    _check_weights(weights, M, k, dev)
+    if weights is not None:
+        _check_weights(weights, M, k, dev)
     _no_grad("int4_matvec", x, weights)
     foreign = None if stream is None else _foreign(stream, dev)
-    out = _output(out, (M, k, N // 2 if gated else N) if weights is None else (M, N), x.dtype, dev, foreign)
+    out = _output(out, (M, N) if weights is not None else (M, k, N // 2 if gated else N), xdt, dev, foreign)
     mode = MRS_INT4_GATED if gated else MRS_INT4_PLAIN if weights is None else MRS_INT4_SUM
     rc = int(lib().moe_int4_matvec(x.data_ptr(), dt, w.codes.data_ptr(), w.scales.data_ptr(), ids.data_ptr(),
-                                   _ptr(weights), M, k, E, K, N, group, int(x.dim() == 3), mode, out.data_ptr(),
+                                   _ptr(weights), M, k, E, K, N, group, int(slots), mode, out.data_ptr(),
                                    _handle(stream, dev)))
     if foreign is not None:
         _hold(foreign, x, *w, ids, weights, out)
