@@ -59,6 +59,18 @@ def _output(out, shape, dtype, dev, foreign, rows: Optional[int] = None):
     return out
 
 
+def _call(dev, entry, *args):
+    """An entry point of the library with dev as the current device, whichever that is:
+    the default stream's handle does not name its device."""
+    import torch
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = entry(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = entry(*args)
+    return int(rc)
+
+
 def _raise(rc: int):
     if rc != MRS_OK:
         raise RouteSortError(rc)
@@ -99,10 +111,10 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     out_dtype = out_dtype or (x.dtype if out is None else out.dtype)
     odt = dt if out_dtype == x.dtype else _code(out_dtype, "out", True)
     out = _output(out, (max(rows, 1), N), out_dtype, dev, foreign, rows)
-    rc = int(lib().moe_grouped_gemm_ex(x.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
-                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
-                                       MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
-                                       _handle(stream, dev), tile))
+    rc = _call(dev, lib().moe_grouped_gemm_ex, x.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
+               expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
+               MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
+               _handle(stream, dev), tile)
     if foreign is not None:
         _hold(foreign, x, w, sorted_ids, expert_of_block, num_post_pad, out)
     _raise(rc)
@@ -134,9 +146,9 @@ def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: in
     out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
     odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
     out = _output(out, (max(rows, 1), K), out_dtype, dev, foreign, rows)
-    rc = int(lib().moe_grouped_gemm_dx_ex(dy.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
-                                          expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block, odt,
-                                          out.data_ptr(), _handle(stream, dev), tile))
+    rc = _call(dev, lib().moe_grouped_gemm_dx_ex, dy.data_ptr(), w.data_ptr(), dt, sorted_ids.data_ptr(),
+               expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block, odt,
+               out.data_ptr(), _handle(stream, dev), tile)
     if foreign is not None:
         _hold(foreign, dy, w, sorted_ids, expert_of_block, num_post_pad, out)
     _raise(rc)
@@ -164,10 +176,10 @@ def grouped_gemm_dw(dy, x, E: int, sorted_ids, expert_of_block, num_post_pad, k:
     out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
     odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
     out = _output(out, (E, N, K), out_dtype, dev, foreign)
-    rc = int(lib().moe_grouped_gemm_dw(dy.data_ptr(), x.data_ptr(), dt, sorted_ids.data_ptr(),
-                                       expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
-                                       MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
-                                       _handle(stream, dev)))
+    rc = _call(dev, lib().moe_grouped_gemm_dw, dy.data_ptr(), x.data_ptr(), dt, sorted_ids.data_ptr(),
+               expert_of_block.data_ptr(), num_post_pad.data_ptr(), M, k, E, K, N, block,
+               MRS_X_TOKENS if tokens is None else MRS_X_SORTED, odt, out.data_ptr(),
+               _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, dy, x, sorted_ids, expert_of_block, num_post_pad, out)
     _raise(rc)
@@ -194,7 +206,8 @@ def swiglu(a, num_post_pad=None, *, out=None, stream=None):
     _check_count(num_post_pad, dev)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (rows, I2 // 2), a.dtype, dev, foreign)
-    rc = int(lib().moe_swiglu(a.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2, out.data_ptr(), _handle(stream, dev)))
+    rc = _call(dev, lib().moe_swiglu, a.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2, out.data_ptr(),
+               _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, a, num_post_pad, out)
     _raise(rc)
@@ -215,8 +228,8 @@ def swiglu_backward(a, dh, num_post_pad=None, *, out=None, stream=None):
     _check_count(num_post_pad, dev)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (rows, I2), a.dtype, dev, foreign)
-    rc = int(lib().moe_swiglu_backward(a.data_ptr(), dh.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2,
-                                       out.data_ptr(), _handle(stream, dev)))
+    rc = _call(dev, lib().moe_swiglu_backward, a.data_ptr(), dh.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2,
+               out.data_ptr(), _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, a, dh, num_post_pad, out)
     _raise(rc)
@@ -235,8 +248,8 @@ def slot_rows(sorted_ids, num_post_pad, tokens: int, k: int, *, out=None, stream
         raise ValueError("tokens must not be negative and k at least 1")
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (M, k), torch.int32, dev, foreign)
-    rc = int(lib().moe_slot_rows(sorted_ids.data_ptr(), num_post_pad.data_ptr(), sorted_ids.numel(), M, k,
-                                 out.data_ptr(), _handle(stream, dev)))
+    rc = _call(dev, lib().moe_slot_rows, sorted_ids.data_ptr(), num_post_pad.data_ptr(), sorted_ids.numel(), M, k,
+               out.data_ptr(), _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, sorted_ids, num_post_pad, out)
     _raise(rc)
@@ -275,8 +288,8 @@ def combine(y, rows, weights=None, *, out_dtype=None, out=None, stream=None):
     out_dtype = out_dtype or (y.dtype if out is None else out.dtype)
     odt = dt if out_dtype == y.dtype else _code(out_dtype, "out", True)
     out = _output(out, (M, N), out_dtype, dev, foreign)
-    rc = int(lib().moe_combine(y.data_ptr(), dt, _ptr(rows), _ptr(weights), R, M, k, N, odt, out.data_ptr(),
-                               _handle(stream, dev)))
+    rc = _call(dev, lib().moe_combine, y.data_ptr(), dt, _ptr(rows), _ptr(weights), R, M, k, N, odt, out.data_ptr(),
+               _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, y, rows, weights, out)
     _raise(rc)
@@ -311,9 +324,9 @@ def combine_backward(dout, rows, sorted_ids, num_post_pad, *, weights=None, y=No
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (R, N), dout.dtype, dev, foreign)
     dv = None if y is None else _output(None, (M, k), torch.float32, dev, foreign)
-    rc = int(lib().moe_combine_backward(dout.data_ptr(), _ptr(y), dt, rows.data_ptr(), sorted_ids.data_ptr(),
-                                        num_post_pad.data_ptr(), _ptr(weights), R, M, k, N, out.data_ptr(), _ptr(dv),
-                                        _handle(stream, dev)))
+    rc = _call(dev, lib().moe_combine_backward, dout.data_ptr(), _ptr(y), dt, rows.data_ptr(), sorted_ids.data_ptr(),
+               num_post_pad.data_ptr(), _ptr(weights), R, M, k, N, out.data_ptr(), _ptr(dv),
+               _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, dout, y, rows, sorted_ids, num_post_pad, weights, out, dv)
     _raise(rc)
@@ -395,13 +408,15 @@ def _group_of(q, dev, dims: int, name: str) -> int:
     import torch
     codes, scales = q if isinstance(q, Int4) else (None, None)
     if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.device == dev
-            and scales.device == dev and codes.dtype == torch.uint8 and codes.is_contiguous() and scales.is_contiguous()):
+            and scales.device == dev and codes.dtype == torch.uint8 and codes.is_contiguous()
+            and scales.is_contiguous()):
         raise ValueError(f"{name} must be an Int4 of contiguous tensors, uint8 codes and scales, on {dev}")
     *lead, Kb = codes.shape
     *same, n = scales.shape
-    if len(lead) != dims - 1 or lead != same or Kb == 0 or Kb % 64 or n == 0 or 2 * Kb % n or 2 * Kb // n not in (32, 64, 128):
-        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows with {dims} dimensions, "
-                         "Kp a multiple of 128, group 32, 64 or 128")
+    if len(lead) != dims - 1 or lead != same or Kb == 0 or Kb % 64 or n == 0 or 2 * Kb % n or \
+            2 * Kb // n not in (32, 64, 128):
+        raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows with {dims} "
+                         "dimensions, Kp a multiple of 128, group 32, 64 or 128")
     return 2 * Kb // n
 
 
@@ -437,8 +452,8 @@ def int4_quantize(w, group: int = 128, *, scale_dtype=None, out: Optional[Int4] 
     elif _group_of(out, dev, w.dim(), "out") != group or out.codes.shape != (*lead, Kp // 2) or \
             out.scales.dtype != scale_dtype:
         raise ValueError(f"out must hold codes {(*lead, Kp // 2)} and {scale_dtype} scales {(*lead, Kp // group)}")
-    rc = int(lib().moe_int4_quantize(w.data_ptr(), dt, rows, K, row_stride, group, sdt, out.codes.data_ptr(),
-                                     out.scales.data_ptr(), _handle(stream, dev)))
+    rc = _call(dev, lib().moe_int4_quantize, w.data_ptr(), dt, rows, K, row_stride, group, sdt, out.codes.data_ptr(),
+               out.scales.data_ptr(), _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, w, *out)
     _raise(rc)
@@ -477,9 +492,9 @@ def int4_matvec(x, w: Int4, ids, *, gated: bool = False, weights=None, out=None,
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (M, N) if weights is not None else (M, k, N // 2 if gated else N), xdt, dev, foreign)
     mode = MRS_INT4_GATED if gated else MRS_INT4_PLAIN if weights is None else MRS_INT4_SUM
-    rc = int(lib().moe_int4_matvec(x.data_ptr(), dt, w.codes.data_ptr(), w.scales.data_ptr(), ids.data_ptr(),
-                                   _ptr(weights), M, k, E, K, N, group, int(slots), mode, out.data_ptr(),
-                                   _handle(stream, dev)))
+    rc = _call(dev, lib().moe_int4_matvec, x.data_ptr(), dt, w.codes.data_ptr(), w.scales.data_ptr(), ids.data_ptr(),
+               _ptr(weights), M, k, E, K, N, group, int(slots), mode, out.data_ptr(),
+               _handle(stream, dev))
     if foreign is not None:
         _hold(foreign, x, *w, ids, weights, out)
     _raise(rc)
