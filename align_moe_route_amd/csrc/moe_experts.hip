@@ -91,25 +91,30 @@ __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
-// First block of [0, n) whose expert is at least e (found for e and e + 1), by 64-ary
-// search: the experts of used blocks ascend.
+// The blocks [first, last) of [0, n) that are expert e's: the first ones whose expert is
+// at least e and at least e + 1, by two 64-ary searches side by side (the experts of used
+// blocks ascend).
 __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& first, int& last) {
   const int lane = threadIdx.x & 63;
-  auto lower = [&](int key) {
-    int lo = 0, len = n;  // the answer lies in [lo, lo + len]
-    while (len > 0) {
-      const int step = (len + 63) / 64, at = lo + lane * step;
-      const bool less = lane * step < len && eob[at] < key;
-      const int c = __builtin_popcountll(__ballot(less));  // probes 0 .. c - 1 are less
-      if (c == 0) return lo;
-      const int from = (c - 1) * step + 1;
-      lo += from;
-      len = min(step - 1, len - from);
+  int lo[2] = {0, 0}, len[2] = {n, n};  // the answers lie in [lo, lo + len]
+  while (len[0] > 0 || len[1] > 0) {
+    bool less[2];
+    int step[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      step[i] = (len[i] + 63) / 64;
+      less[i] = lane * step[i] < len[i] && eob[lo[i] + lane * step[i]] < e + i;
     }
-    return lo;
-  };
-  first = lower(e);
-  last = lower(e + 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = __builtin_popcountll(__ballot(less[i]));  // probes 0 .. c - 1 are less
+      const int from = c == 0 ? 0 : (c - 1) * step[i] + 1;
+      lo[i] += from;
+      len[i] = c == 0 ? 0 : min(step[i] - 1, len[i] - from);
+    }
+  }
+  first = lo[0];
+  last = lo[1];
 }
 
 constexpr int kXcds = 8;
@@ -132,6 +137,7 @@ template <int DIR, typename P>
 struct Ring {
   u32x4 a[P::S][P::TR * P::STEP / 8], b[P::S][P::BN * P::STEP / 8];
   int32_t row[DIR == kWeights ? kRowsAhead + 4 * P::STEP : P::TR];
+  int32_t steps[P::NW];
 };
 
 // DIRECT: the operands' rows are whole 16-byte chunks at multiples of 16 bytes, and go
@@ -166,12 +172,12 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     const int rt = (i / g.run * kXcds + x) * g.run + i % g.run;
     if (rt >= g.nrt) return;
     i0 = rt * BM, j0 = j % g.nct * BN;
-    if (i0 + BM > npp) return;  // npp is a multiple of block and BM divides block
+    // asked for together, before any is looked at
     e = g.eob[i0 / g.block];
-    if (e < 0 || e >= g.E) return;
+    const int s = tid < BM ? g.sid[i0 + tid] : -1;
+    if (i0 + BM > npp || e < 0 || e >= g.E) return;  // npp is a multiple of block and BM divides block
     c_end = g.C;
     if (tid < TR) {
-      const int s = tid < BM ? g.sid[i0 + tid] : -1;
       const bool ok = s >= 0 && s < g.routes;
       l.row[tid] = !ok ? -1 : (DIR == kForward && !g.sorted) ? s / g.k : i0 + tid;
     }
@@ -449,14 +455,22 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     const int end = c_end;
     for (int c = c_first; c < end; c += kRowsAhead) {
       const int n = min(end - c, kRowsAhead), whole = (n + kStep - 1) / kStep * kStep;
+      int used = 0;  // steps up to the last row with a slot: an expert's padding comes last
       for (int r = tid; r < whole + 4 * kStep; r += kThreads) {
         const int s = r < n ? g.sid[c + r] : -1;
         const bool ok = s >= 0 && s < g.routes;
         l.row[r] = !ok ? -1 : g.sorted ? c + r : s / g.k;
+        if (ok) used = r / kStep + 1;
       }
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) used = max(used, __shfl_xor(used, d));
+      if (lane == 0) l.steps[wv] = used;
       __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) used = max(used, l.steps[w]);
+      used = __builtin_amdgcn_readfirstlane(used);
       c_first = c;
-      run(whole / kStep, true);
+      run(used, true);
     }
   } else {
     run((c_end + kStep - 1) / kStep, has != 0);
