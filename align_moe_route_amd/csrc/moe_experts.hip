@@ -326,9 +326,9 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   struct Operands {
     u32x4 a[FM], b[FN];
   };
-  auto read_one = [&](Operands& f, int buf, int kk, int q) {
-    if (q < FM) f.a[q] = operand<kAcrossA, TR, kStep>(l.a[buf], wi + q * 32, kk);
-    else f.b[q - FM] = operand<kAcrossB, BN, kStep>(l.b[buf], wj + (q - FM) * 32, kk);
+  auto read_one = [&](Operands& f, int buf, int kk, int q) {  // those of B first
+    if (q < FN) f.b[q] = operand<kAcrossB, BN, kStep>(l.b[buf], wj + q * 32, kk);
+    else f.a[q - FN] = operand<kAcrossA, TR, kStep>(l.a[buf], wi + (q - FN) * 32, kk);
   };
   auto multiply_one = [&](const Operands& f, int q) { acc[q / FN][q % FN] = H::mfma32(f.b[q % FN], f.a[q / FN], acc[q / FN][q % FN]); };
   auto next = [](int buf) { return buf + 1 == S ? 0 : buf + 1; };
@@ -340,9 +340,12 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   // operands and with a part of a stage's loads (left to itself the compiler reads the
   // operands right before their use).  A step has one barrier: past it the next stage
   // has arrived, and the stage read before is free.
-  auto run_direct = [&](int n, auto active) {
-    constexpr bool kActive = decltype(active)::value;  // a wave without rows only loads
-    constexpr int kReads = FM + FN, kMul = FM * FN;
+  auto run_direct = [&](int n, auto parts) {
+    // the leading parts of 32 rows of this wave that are multiplied: one without a slot is
+    // not, and a wave without any only loads
+    constexpr int kParts = decltype(parts)::value;
+    constexpr bool kActive = kParts > 0;
+    constexpr int kReads = kParts + FN, kMul = kActive ? kParts * FN : FN;
     Operands f[2];
     int rows[RP];
     // this wave's loads of S - 2 stages may be in flight
@@ -443,8 +446,9 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   };
   auto run = [&](int n, bool active) {
     if constexpr (DIRECT) {
-      if (active) run_direct(n, std::true_type());
-      else run_direct(n, std::false_type());
+      if (!active) run_direct(n, std::integral_constant<int, 0>());
+      else if (FM == 2 && has >> 32 == 0) run_direct(n, std::integral_constant<int, 1>());
+      else run_direct(n, std::integral_constant<int, FM>());
     } else {
       if (g.tiny) run_staged(n, active, std::true_type());  // rows of fewer than eight values
       else run_staged(n, active, std::false_type());
