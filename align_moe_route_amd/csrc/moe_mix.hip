@@ -94,6 +94,24 @@ __global__ __launch_bounds__(kThreads) void k_slot_rows(const int32_t* sid, cons
   if (s >= 0 && s < n) rows[s] = r;
 }
 
+// Few slots: one workgroup and one launch, through LDS, up to where it takes as long as the
+// two (us, one launch / two; 4 slots 1.8 / 3.4, 1024 slots in 14464 rows 2.7 / 3.5, 8192 in
+// 12224 3.6 / 3.9, 16384 in 20416 5.5 / 3.9), which also cost the host another launch.
+constexpr int kSlotThreads = 1024, kFewSlots = 8192, kFewRows = 16384;
+__global__ __launch_bounds__(kSlotThreads) void k_slot_rows_few(const int32_t* sid, const int32_t* npp, int capacity,
+                                                                int32_t* rows, int n) {
+  __shared__ int32_t at[kFewSlots];
+  const int end = min(*npp, capacity);
+  for (int i = threadIdx.x; i < n; i += kSlotThreads) at[i] = -1;
+  __syncthreads();
+  for (int r = threadIdx.x; r < end; r += kSlotThreads) {
+    const int s = sid[r];
+    if (s >= 0 && s < n) at[s] = r;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kSlotThreads) rows[i] = at[i];
+}
+
 // -------------------------------------------------------------------- mix
 //
 // A wave takes 512 columns of a token, eight a lane, and its picks in turn, eight
@@ -219,8 +237,8 @@ bool half_dtype(int dtype) { return dtype == MRS_DTYPE_BF16 || dtype == MRS_DTYP
 
 constexpr int kMaxCols = 1 << 20;
 
-int launch(const void* fn, int64_t grid, void** params, void* stream) {
-  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kThreads), params, 0, reinterpret_cast<hipStream_t>(stream)) ==
+int launch(const void* fn, int64_t grid, void** params, void* stream, int threads = kThreads) {
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), params, 0, reinterpret_cast<hipStream_t>(stream)) ==
                  hipSuccess
              ? MRS_OK
              : MRS_ERR_LAUNCH;
@@ -264,6 +282,10 @@ extern "C" int moe_slot_rows(const int32_t* sorted_ids, const int32_t* num_post_
   if (!sorted_ids || !num_post_pad || !rows) return MRS_ERR_NULL_POINTER;
   if (!aligned_to(sorted_ids, 4) || !aligned_to(num_post_pad, 4) || !aligned_to(rows, 4)) return MRS_ERR_MISALIGNED;
   int n = M * k, cap = (int)capacity;
+  if (n <= kFewSlots && cap <= kFewRows) {
+    void* params[] = {&sorted_ids, &num_post_pad, &cap, &rows, &n};
+    return launch(reinterpret_cast<const void*>(k_slot_rows_few), 1, params, stream, kSlotThreads);
+  }
   void* fill[] = {&rows, &n};
   const int rc = launch(reinterpret_cast<const void*>(k_fill_rows), (n + kThreads - 1) / kThreads, fill, stream);
   if (rc != MRS_OK || cap == 0) return rc;

@@ -98,7 +98,7 @@ int moe_swiglu_backward(const void* a, const void* dh, int dtype, const int32_t*
 
 /*
  * moe_slot_rows -- rows[s] = the row r < *num_post_pad with sorted_ids[r] = s, -1
- * for a slot that has none (a dropped route).  Two launches.
+ * for a slot that has none (a dropped route).  One or two launches, by the sizes.
  *   sorted_ids  `capacity` entries;  rows  [M, k] int32 (written whole)
  */
 int moe_slot_rows(const int32_t* sorted_ids, const int32_t* num_post_pad, int64_t capacity, int M, int k,

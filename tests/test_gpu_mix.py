@@ -102,6 +102,16 @@ def test_combine(shape, weighted, dtype):
     assert torch.equal(only[:r.npp], dy[:r.npp])
 
 
+@pytest.mark.parametrize("M,E,k,block", [(1024, 16, 8, 16), (1025, 16, 8, 16), (2000, 40, 1, 400), (2000, 30, 1, 512)])
+def test_slot_rows_sizes(M, E, k, block):
+    """Both sides of the border between one launch and two, by slots and by rows."""
+    ids = ids_of(M, E, k, 9, 0.2)
+    r = Routed(ids, E, block)
+    out = torch.full((M, k), 5, dtype=torch.int32, device="cuda")
+    assert amr.slot_rows(r.meta[0], r.meta[2], M, k, out=out) is out
+    assert np.array_equal(out.cpu().numpy(), orc.slot_rows(r.sid, r.npp, M, k))
+
+
 def test_combine_in_slot_order():
     y = normal((15, 33), torch.bfloat16, 1)
     v = torch.rand(5, 3, device="cuda")
