@@ -1040,5 +1040,19 @@ def route_sort_train(logits, bias, k: int, n_group: int, topk_group: int, block:
     return RouteSortOutput(ids, w, sid, eob, npp), BalanceOutput(loss, counts, tokens, shares)
 
 
-from .experts import (Int4, combine, combine_backward, experts_train, grouped_gemm, grouped_gemm_dw,  # noqa: E402,F401
-                      grouped_gemm_dx, int4_matvec, int4_quantize, slot_rows, swiglu, swiglu_backward)
+_EXPERTS = ("Int4", "combine", "combine_backward", "experts_train", "grouped_gemm", "grouped_gemm_dw", "grouped_gemm_dx",
+            "int4_matvec", "int4_quantize", "slot_rows", "swiglu", "swiglu_backward")
+
+
+def __getattr__(name):
+    """The experts' operators (experts.py), which import torch with their module: loaded
+    when the first is asked for."""
+    if name not in _EXPERTS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import experts
+    globals().update({n: getattr(experts, n) for n in _EXPERTS})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_EXPERTS})

@@ -17,6 +17,18 @@ namespace {
 //   kRows     i sorted rows, j = k, c = n: A = dy (rows along c), B = w (rows along j)
 //   kWeights  i = n, j = k, c sorted rows of one expert: A = dy (rows along i), B = x
 //             (rows along j)
+// on v_mfma_f32_32x32x16, which sums 16 products in FP32.
+//
+// What bounds them is how fast a compute unit takes operands out of its L2 (measured:
+// 120 GB/s in whole 128-byte lines, 62 in halves of lines, 37 at odd addresses; LDS reads
+// are 350 to 450), beside the matrix units at the clock that the power leaves. So: tiles as large as the
+// registers hold, operands straight into LDS in whole lines where rows are whole chunks
+// (steps of 64 along c), loads, LDS reads and matrix instructions of a wave interleaved,
+// and what an expert's tiles share read from one L2 at about the same time.
+//   8192 tokens, 896 experts, top-16, K 3584, N 768, blocks of 128: y in 1250 us; the bytes
+//   that must move take 1075 at a copy's 4.9 TB/s (weights 4.9 GB); 577 TFLOP/s of routes
+//   8192 tokens, 64 experts, top-8, the same K and N: dx in 480 us, dw in 400 (750 and 900
+//   TFLOP/s; an 8192^3 library product 1395; even experts of 2048 rows: 840 and 1030)
 enum Dir { kForward, kRows, kWeights };
 
 struct GArgs {
@@ -27,7 +39,6 @@ struct GArgs {
   int I, J, C;    // sizes of i, j, c (I: kWeights only; C: the others only)
   int row_limit;  // rows the metadata can hold: (max_rows / block) * block
   int nrt, nct;   // tiles of i (over all sorted rows, or of one expert), tiles of j
-  int run;        // consecutive row tiles of an XCD
   bool tiny;      // an operand's rows have fewer than eight values
 };
 
@@ -118,7 +129,13 @@ __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& f
 }
 
 constexpr int kXcds = 8;
-constexpr int kRun = 4;  // consecutive row tiles of an XCD
+// Workgroup h goes to XCD h mod 8.  Runs of kRun consecutive row tiles go to the XCDs in turn,
+// the column tiles of a row tile one after another (runs of 1, 2, 4, 8, 16, 32: the case above
+// 1333, 1285, 1261, 1272, 1285, 1258 us; 8192 tokens of 64 experts, top-4 251, 226, 221, 220, 256,
+// 298; 16 tokens of 64 experts 10.7, 10.7, 11.1, 13.2, 17.3, 32).  kWeights: an expert's column
+// tiles go to the XCDs in turn with all their row tiles, so that large experts are everyone's
+// (whole experts in turn 541 us, so 435).
+constexpr int kRun = 4;
 constexpr int kRowsAhead = 4096;  // rows of an expert whose sources are kept in LDS at once (kWeights)
 
 // A tile of BM x BN results by NW waves, in steps of STEP values of c, S stages of LDS.
@@ -169,7 +186,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     c_first = first * g.block, c_end = last * g.block;
   } else {
     const int h = blockIdx.x, x = h % kXcds, j = h / kXcds, i = j / g.nct;
-    const int rt = (i / g.run * kXcds + x) * g.run + i % g.run;
+    const int rt = (i / kRun * kXcds + x) * kRun + i % kRun;
     if (rt >= g.nrt) return;
     i0 = rt * BM, j0 = j % g.nct * BN;
     // asked for together, before any is looked at
@@ -330,7 +347,9 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     if (q < FN) f.b[q] = operand<kAcrossB, BN, kStep>(l.b[buf], wj + q * 32, kk);
     else f.a[q - FN] = operand<kAcrossA, TR, kStep>(l.a[buf], wi + (q - FN) * 32, kk);
   };
-  auto multiply_one = [&](const Operands& f, int q) { acc[q / FN][q % FN] = H::mfma32(f.b[q % FN], f.a[q / FN], acc[q / FN][q % FN]); };
+  auto multiply_one = [&](const Operands& f, int q) {
+    acc[q / FN][q % FN] = H::mfma32(f.b[q % FN], f.a[q / FN], acc[q / FN][q % FN]);
+  };
   auto next = [](int buf) { return buf + 1 == S ? 0 : buf + 1; };
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   typedef std::integral_constant<int, KK> All;
@@ -370,7 +389,8 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     for (int t = 0; t < n; ++t) {
       int ahead[RP];
       auto go = [&](auto kc) {
-        constexpr int kk = decltype(kc)::value, kAt = kk == KK - 1 && kMul > 1 ? 1 : 0;  // instructions before the reads
+        constexpr int kk = decltype(kc)::value;
+        constexpr int kAt = kk == KK - 1 && kMul > 1 ? 1 : 0;  // instructions before the reads
         fence();
 #pragma unroll
         for (int q = 0; q < kMul; ++q) {
@@ -545,41 +565,41 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
 
 constexpr int kCols = 256;
 
-// Tiles of i for each direction and the number of rows in them.
+// Tiles of each direction by their rows (us; kernels of 4 waves and up to 76 KB of LDS run
+// two to a compute unit).
+//   kForward, 128 rows: 8 waves, steps of 64 (whole lines) 1285 for the case above, 4 waves
+//     and steps of 32 1506; 384 columns 1391 to 1412; fewer rows: steps of 64 in place of 32
+//     445 for 486 (64 tokens of 896 experts, blocks of 16), 327 for 408 (2048 tokens of 256,
+//     top-8, blocks of 64); seven stages of steps of 32: 22.6 for 18.7 (777 tokens of 24)
+//   kRows: B runs across, in whole lines at any step: 128 rows by 4 waves and steps of 32
+//     485, by 8 waves and steps of 64 512, pairs of blocks as tiles of 256 x 256 506 (the
+//     case above; experts that share a pair take two passes)
+//   kWeights: 256 x 256 by 8 waves 440, 128 x 256 by 8 waves 480, 128 x 128 487 (the case
+//     above); 512 tokens of 896 experts 955, 1213, 1122
+//   kWeights through registers: 128 x 128 by 8 waves 21.3 (777 tokens of 24 experts, K 1000,
+//     N 397), by 4 waves 26.3, 128 x 256 24.0, 256 x 256 34 (it spills)
 template <int DIR, int BM>
 struct ShapeOf;
-#ifndef SH_W
-#define SH_W 256, kCols, 8, 32, 3
-#define SH_WS 128, 128, 8, 32, 3
-#define SH_F128 128, kCols, 8, 64, 3
-#define SH_F64 64, kCols, 4, 64, 3
-#define SH_F32 32, kCols, 4, 64, 3
-#define SH_F16 16, kCols, 4, 64, 3
-#define SH_R128 128, kCols, 4, 32, 3
-#define SH_R64 64, kCols, 4, 32, 3
-#define SH_R32 32, kCols, 4, 32, 4
-#define SH_R16 16, kCols, 4, 32, 4
-#endif
 template <>
-struct ShapeOf<kForward, 128> : Shape<SH_F128> {};
+struct ShapeOf<kForward, 128> : Shape<128, kCols, 8, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 64> : Shape<SH_F64> {};
+struct ShapeOf<kForward, 64> : Shape<64, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 32> : Shape<SH_F32> {};
+struct ShapeOf<kForward, 32> : Shape<32, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 16> : Shape<SH_F16> {};
+struct ShapeOf<kForward, 16> : Shape<16, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kRows, 128> : Shape<SH_R128> {};
+struct ShapeOf<kRows, 128> : Shape<128, kCols, 4, 32, 3> {};
 template <>
-struct ShapeOf<kRows, 64> : Shape<SH_R64> {};
+struct ShapeOf<kRows, 64> : Shape<64, kCols, 4, 32, 3> {};
 template <>
-struct ShapeOf<kRows, 32> : Shape<SH_R32> {};
+struct ShapeOf<kRows, 32> : Shape<32, kCols, 4, 32, 4> {};
 template <>
-struct ShapeOf<kRows, 16> : Shape<SH_R16> {};
+struct ShapeOf<kRows, 16> : Shape<16, kCols, 4, 32, 4> {};
 template <>
-struct ShapeOf<kWeights, 256> : Shape<SH_W> {};
+struct ShapeOf<kWeights, 256> : Shape<256, kCols, 8, 32, 3> {};  // straight into LDS
 template <>
-struct ShapeOf<kWeights, 128> : Shape<SH_WS> {};
+struct ShapeOf<kWeights, 128> : Shape<128, 128, 8, 32, 3> {};  // through registers
 
 struct Launch {
   const void* kernel;
@@ -638,7 +658,8 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
   // lengths of the operands' rows
   const int la = DIR == kForward ? K : N, lb = K;
   g.tiny = la < 8 || lb < 8;
-  const bool direct = la % 8 == 0 && aligned_to(a, 16) && lb % 8 == 0 && aligned_to(b, 16), f32 = out_dtype == MRS_DTYPE_F32;
+  const bool direct = la % 8 == 0 && aligned_to(a, 16) && lb % 8 == 0 && aligned_to(b, 16);
+  const bool f32 = out_dtype == MRS_DTYPE_F32;
   int bm, bn = kCols;
   int64_t grid;
   if constexpr (DIR == kWeights) {
@@ -659,8 +680,7 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     while (bm > 32 && used * ((routes / used + bm - 1) / bm) * ((g.J + bn - 1) / bn) < 128) bm /= 2;
     if (tile != 0) bm = tile;
     g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
-    g.run = kRun;
-    grid = ((int64_t)g.nrt + kXcds * g.run - 1) / (kXcds * g.run) * g.run * kXcds * g.nct;
+    grid = ((int64_t)g.nrt + kXcds * kRun - 1) / (kXcds * kRun) * kRun * kXcds * g.nct;
   }
   const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, direct)
                                            : product_kernel<FP16, DIR>(f32, bm, direct);

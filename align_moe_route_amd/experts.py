@@ -13,33 +13,52 @@ from __future__ import annotations
 import functools
 from typing import NamedTuple, Optional
 
+import torch
+from torch.autograd.function import once_differentiable
+
 from . import (MRS_DTYPE_BF16, MRS_DTYPE_F16, MRS_DTYPE_F32, MRS_INT4_GATED, MRS_INT4_PLAIN, MRS_INT4_SUM, MRS_OK,
                MRS_X_SORTED, MRS_X_TOKENS, RouteSortError, _allocate, _capacity, _check_metadata, _check_tensor, _empty,
                _foreign, _handle, _hold, _ptr, _row_stride, lib)
 
 
+_CODES = {torch.bfloat16: MRS_DTYPE_BF16, torch.float16: MRS_DTYPE_F16}
+_CODES_F32 = {**_CODES, torch.float32: MRS_DTYPE_F32}
+
+
 def _code(dtype, name: str, f32: bool = False) -> int:
-    import torch
-    if dtype == torch.bfloat16:
-        return MRS_DTYPE_BF16
-    if dtype == torch.float16:
-        return MRS_DTYPE_F16
-    if f32 and dtype == torch.float32:
-        return MRS_DTYPE_F32
-    raise NotImplementedError(f"{name} dtype {dtype} (bfloat16{', float16 or float32' if f32 else ' or float16'} only)")
+    code = (_CODES_F32 if f32 else _CODES).get(dtype)
+    if code is None:
+        raise NotImplementedError(f"{name} dtype {dtype} (bfloat16{', float16 or float32' if f32 else ' or float16'} only)")
+    return code
 
 
-def _matrix(t, dims: int, name: str, dev=None, dtype=None):
-    """t is a contiguous GPU tensor of `dims` dimensions (on dev, of dtype)."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims and t.is_contiguous()
-            and (dev is None or t.device == dev) and (dtype is None or t.dtype == dtype)):
-        what = f"a contiguous {'' if dtype is None else f'{dtype} '}tensor of {dims} dimensions"
-        raise ValueError(f"{name} must be {what} on {'the GPU' if dev is None else dev}")
+def _is(t, index: int, dtype) -> bool:
+    """t is a contiguous tensor of dtype on GPU `index` (short: a call of a token or two
+    takes as long as its checks)."""
+    return isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype == dtype and t.is_contiguous()
+
+
+def _first(t, dims: int, name: str):
+    """(type code, device, its index) of a call's first matrix."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous GPU tensor of {dims} dimensions")
+    return _code(t.dtype, name), t.device, t.get_device()
+
+
+def _matrix(t, dims: int, name: str, index: int, dtype):
+    """t is a contiguous tensor of `dims` dimensions and dtype on GPU `index`."""
+    if not (_is(t, index, dtype) and t.dim() == dims):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {dims} dimensions on GPU {index}")
+
+
+def _metadata(sorted_ids, expert_of_block, num_post_pad, rows: int, blocks: int, dev, index: int):
+    i32 = torch.int32
+    if not (_is(sorted_ids, index, i32) and sorted_ids.numel() >= rows and _is(expert_of_block, index, i32)
+            and expert_of_block.numel() >= blocks and _is(num_post_pad, index, i32) and num_post_pad.numel() >= 1):
+        _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
 
 
 def _no_grad(what: str, *tensors):
-    import torch
     for t in tensors:
         if t is None or not t.requires_grad or not torch.is_grad_enabled():
             continue
@@ -49,7 +68,6 @@ def _no_grad(what: str, *tensors):
 
 def _output(out, shape, dtype, dev, foreign, rows: Optional[int] = None):
     """`out` checked (its first dimension may be larger than `rows`), or a new tensor."""
-    import torch
     if out is None:
         return _empty(shape, dtype, dev) if foreign is None else _allocate(foreign, dev, _empty, shape, dtype, dev)
     if not (isinstance(out, torch.Tensor) and out.device == dev and out.dtype == dtype and out.is_contiguous()
@@ -62,7 +80,6 @@ def _output(out, shape, dtype, dev, foreign, rows: Optional[int] = None):
 def _call(dev, entry, *args):
     """An entry point of the library with dev as the current device, whichever that is:
     the default stream's handle does not name its device."""
-    import torch
     if torch._C._cuda_getDevice() == dev.index:
         rc = entry(*args)
     else:
@@ -95,18 +112,18 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     Returns y [max_rows, N]; rows at or past num_post_pad are left as they were.  tile:
     rows of a tile (16, 32, 64 or 128, dividing block) in place of the choice by sizes,
     for tests and tuning."""
-    _matrix(x, 2, "x")
-    dt, dev = _code(x.dtype, "x"), x.device
-    _matrix(w, 3, "w", dev, x.dtype)
+    dt, dev, index = _first(x, 2, "x")
+    _matrix(w, 3, "w", index, x.dtype)
     E, N, K = w.shape
-    if x.shape[1] != K:
+    given, width = x.shape
+    if width != K:
         raise ValueError("x and w disagree on K")
     _no_grad("grouped_gemm", x, w)
-    M = x.shape[0] if tokens is None else int(tokens)
+    M = given if tokens is None else int(tokens)
     rows, blocks = _sizes(M, E, k, block)
-    if tokens is not None and x.shape[0] < rows:
+    if tokens is not None and given < rows:
         raise ValueError(f"x must hold at least {rows} rows in sorted order")
-    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    _metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev, index)
     foreign = None if stream is None else _foreign(stream, dev)
     out_dtype = out_dtype or (x.dtype if out is None else out.dtype)
     odt = dt if out_dtype == x.dtype else _code(out_dtype, "out", True)
@@ -130,9 +147,8 @@ def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: in
     Returns dx [max_rows, K] of dy's type (default) or float32; rows at or past
     num_post_pad are left as they were.  Of an x that holds the tokens' rows the
     gradient is combine(dx, slot_rows(...)).  tile: as for grouped_gemm."""
-    _matrix(dy, 2, "dy")
-    dt, dev = _code(dy.dtype, "dy"), dy.device
-    _matrix(w, 3, "w", dev, dy.dtype)
+    dt, dev, index = _first(dy, 2, "dy")
+    _matrix(w, 3, "w", index, dy.dtype)
     E, N, K = w.shape
     if dy.shape[1] != N:
         raise ValueError("dy and w disagree on N")
@@ -141,7 +157,7 @@ def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: in
     rows, blocks = _sizes(M, E, k, block)
     if dy.shape[0] < rows:
         raise ValueError(f"dy must hold at least {rows} rows in sorted order")
-    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    _metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev, index)
     foreign = None if stream is None else _foreign(stream, dev)
     out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
     odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
@@ -162,16 +178,15 @@ def grouped_gemm_dw(dy, x, E: int, sorted_ids, expert_of_block, num_post_pad, k:
 
     dy: [max_rows, N]; x and `tokens` as for grouped_gemm; E: the experts.  Returns dw
     [E, N, K] of dy's type (default) or float32; equal inputs give equal bits."""
-    _matrix(dy, 2, "dy")
-    dt, dev = _code(dy.dtype, "dy"), dy.device
-    _matrix(x, 2, "x", dev, dy.dtype)
+    dt, dev, index = _first(dy, 2, "dy")
+    _matrix(x, 2, "x", index, dy.dtype)
     N, K, E = dy.shape[1], x.shape[1], int(E)
     _no_grad("grouped_gemm_dw", dy, x)
     M = x.shape[0] if tokens is None else int(tokens)
     rows, blocks = _sizes(M, E, k, block)
     if dy.shape[0] < rows or (tokens is not None and x.shape[0] < rows):
         raise ValueError(f"rows in sorted order must be at least {rows}")
-    _check_metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev)
+    _metadata(sorted_ids, expert_of_block, num_post_pad, rows, blocks, dev, index)
     foreign = None if stream is None else _foreign(stream, dev)
     out_dtype = out_dtype or (dy.dtype if out is None else out.dtype)
     odt = dt if out_dtype == dy.dtype else _code(out_dtype, "out", True)
@@ -186,10 +201,10 @@ def grouped_gemm_dw(dy, x, E: int, sorted_ids, expert_of_block, num_post_pad, k:
     return out
 
 
-def _check_count(num_post_pad, dev):
-    import torch
-    if num_post_pad is not None:
-        _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+def _vector(t, index: int, dtype, n: int, name: str, dev):
+    """t is a contiguous tensor of dtype with at least n values on GPU `index`."""
+    if not (_is(t, index, dtype) and t.numel() >= n):
+        _check_tensor(t, dev, dtype, n, name)
 
 
 def swiglu(a, num_post_pad=None, *, out=None, stream=None):
@@ -197,13 +212,13 @@ def swiglu(a, num_post_pad=None, *, out=None, stream=None):
 
     a: [rows, 2 I] bfloat16 or float16.  num_post_pad: int32 [1] on the device, the
     rows to take (the others of h are left as they were); by default all."""
-    _matrix(a, 2, "a")
-    dt, dev = _code(a.dtype, "a"), a.device
+    dt, dev, index = _first(a, 2, "a")
     rows, I2 = a.shape
     if I2 % 2 or I2 == 0:
         raise ValueError("a must have an even number of columns")
     _no_grad("swiglu", a)
-    _check_count(num_post_pad, dev)
+    if num_post_pad is not None:
+        _vector(num_post_pad, index, torch.int32, 1, "num_post_pad", dev)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (rows, I2 // 2), a.dtype, dev, foreign)
     rc = _call(dev, lib().moe_swiglu, a.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2, out.data_ptr(),
@@ -216,16 +231,16 @@ def swiglu(a, num_post_pad=None, *, out=None, stream=None):
 
 def swiglu_backward(a, dh, num_post_pad=None, *, out=None, stream=None):
     """Gradient of swiglu's a (moe_swiglu_backward) from dh [rows, I]; `out` may be a."""
-    _matrix(a, 2, "a")
-    dt, dev = _code(a.dtype, "a"), a.device
+    dt, dev, index = _first(a, 2, "a")
     rows, I2 = a.shape
     if I2 % 2 or I2 == 0:
         raise ValueError("a must have an even number of columns")
-    _matrix(dh, 2, "dh", dev, a.dtype)
+    _matrix(dh, 2, "dh", index, a.dtype)
     if dh.shape != (rows, I2 // 2):
         raise ValueError(f"dh must have shape {(rows, I2 // 2)}")
     _no_grad("swiglu_backward", a, dh)
-    _check_count(num_post_pad, dev)
+    if num_post_pad is not None:
+        _vector(num_post_pad, index, torch.int32, 1, "num_post_pad", dev)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (rows, I2), a.dtype, dev, foreign)
     rc = _call(dev, lib().moe_swiglu_backward, a.data_ptr(), dh.data_ptr(), dt, _ptr(num_post_pad), rows, I2 // 2,
@@ -238,12 +253,11 @@ def swiglu_backward(a, dh, num_post_pad=None, *, out=None, stream=None):
 
 def slot_rows(sorted_ids, num_post_pad, tokens: int, k: int, *, out=None, stream=None):
     """Sorted row of every slot (moe_slot_rows): int32 [M, k], -1 for a dropped route."""
-    import torch
     if not isinstance(sorted_ids, torch.Tensor) or not sorted_ids.is_cuda:
         raise ValueError("sorted_ids must be a GPU tensor")
-    dev, M = sorted_ids.device, int(tokens)
-    _check_tensor(sorted_ids, dev, torch.int32, 0, "sorted_ids")
-    _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+    dev, index, M = sorted_ids.device, sorted_ids.get_device(), int(tokens)
+    _vector(sorted_ids, index, torch.int32, 0, "sorted_ids", dev)
+    _vector(num_post_pad, index, torch.int32, 1, "num_post_pad", dev)
     if M < 0 or k < 1:
         raise ValueError("tokens must not be negative and k at least 1")
     foreign = None if stream is None else _foreign(stream, dev)
@@ -256,11 +270,10 @@ def slot_rows(sorted_ids, num_post_pad, tokens: int, k: int, *, out=None, stream
     return out
 
 
-def _check_weights(weights, M: int, k: int, dev):
-    import torch
+def _check_weights(weights, M: int, k: int, dev, index: int):
     if weights is not None:
-        _check_tensor(weights, dev, torch.float32, M * k, "weights")
-        if tuple(weights.shape) != (M, k):
+        _vector(weights, index, torch.float32, M * k, "weights", dev)
+        if weights.shape != (M, k):
             raise ValueError(f"weights must have shape ({M}, {k})")
 
 
@@ -270,9 +283,7 @@ def combine(y, rows, weights=None, *, out_dtype=None, out=None, stream=None):
     y: [R, N] bfloat16 or float16.  rows: int32 [M, k] (slot_rows; a row outside [0, R)
     adds nothing), or an integer k for y in slot order.  weights: float32 [M, k], by
     default ones.  Returns [M, N] of y's type (default) or float32."""
-    import torch
-    _matrix(y, 2, "y")
-    dt, dev = _code(y.dtype, "y"), y.device
+    dt, dev, index = _first(y, 2, "y")
     R, N = y.shape
     if isinstance(rows, int):
         k, rows = rows, None
@@ -280,9 +291,9 @@ def combine(y, rows, weights=None, *, out_dtype=None, out=None, stream=None):
             raise ValueError("y must hold k rows for every token")
         M = R // k
     else:
-        _matrix(rows, 2, "rows", dev, torch.int32)
+        _matrix(rows, 2, "rows", index, torch.int32)
         M, k = rows.shape
-    _check_weights(weights, M, k, dev)
+    _check_weights(weights, M, k, dev, index)
     _no_grad("combine", y, weights)
     foreign = None if stream is None else _foreign(stream, dev)
     out_dtype = out_dtype or (y.dtype if out is None else out.dtype)
@@ -304,22 +315,20 @@ def combine_backward(dout, rows, sorted_ids, num_post_pad, *, weights=None, y=No
     dout: [M, N] bfloat16 or float16; rows: slot_rows of this metadata.  Returns dy
     [rows of y, or of sorted_ids; N], or (dy, dweights); rows of dy at or past
     num_post_pad are left as they were."""
-    import torch
-    _matrix(dout, 2, "dout")
-    dt, dev = _code(dout.dtype, "dout"), dout.device
+    dt, dev, index = _first(dout, 2, "dout")
     M, N = dout.shape
-    _matrix(rows, 2, "rows", dev, torch.int32)
+    _matrix(rows, 2, "rows", index, torch.int32)
     if rows.shape[0] != M:
         raise ValueError(f"rows must have shape ({M}, k)")
     k = rows.shape[1]
-    _check_weights(weights, M, k, dev)
+    _check_weights(weights, M, k, dev, index)
     R = sorted_ids.numel() if y is None else y.shape[0]
     if y is not None:
-        _matrix(y, 2, "y", dev, dout.dtype)
+        _matrix(y, 2, "y", index, dout.dtype)
         if y.shape[1] != N:
             raise ValueError("y and dout disagree on N")
-    _check_tensor(sorted_ids, dev, torch.int32, R, "sorted_ids")
-    _check_tensor(num_post_pad, dev, torch.int32, 1, "num_post_pad")
+    _vector(sorted_ids, index, torch.int32, R, "sorted_ids", dev)
+    _vector(num_post_pad, index, torch.int32, 1, "num_post_pad", dev)
     _no_grad("combine_backward", dout, weights, y)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (R, N), dout.dtype, dev, foreign)
@@ -335,9 +344,6 @@ def combine_backward(dout, rows, sorted_ids, num_post_pad, *, weights=None, y=No
 
 @functools.lru_cache(maxsize=1)
 def _experts_function():
-    import torch
-    from torch.autograd.function import once_differentiable
-
     class Experts(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, w_up, w_down, weights, sorted_ids, expert_of_block, num_post_pad, block):
@@ -384,11 +390,10 @@ def experts_train(x, w_up, w_down, route, block: int):
     pass the gradient on to the logits), returned for `block`.  Returns [M, H] with
     gradients to x, both weights and route.weights.  To capture a training step in a
     graph call the entry points themselves, as for route_sort_train."""
-    _matrix(x, 2, "x")
-    dev = x.device
-    _matrix(w_up, 3, "w_up", dev, x.dtype)
-    _matrix(w_down, 3, "w_down", dev, x.dtype)
-    _matrix(route.weights, 2, "route.weights", dev)
+    _, _, index = _first(x, 2, "x")
+    _matrix(w_up, 3, "w_up", index, x.dtype)
+    _matrix(w_down, 3, "w_down", index, x.dtype)
+    _matrix(route.weights, 2, "route.weights", index, torch.float32)
     E, two, H = w_up.shape
     if x.shape[1] != H or two % 2 or tuple(w_down.shape) != (E, H, two // 2) or route.weights.shape[0] != x.shape[0]:
         raise ValueError("w_up must be [E, 2 I, H], w_down [E, H, I] and route.weights [M, k] for x [M, H]")
@@ -403,21 +408,20 @@ class Int4(NamedTuple):
     scales: "torch.Tensor"  # bfloat16 or float16 [..., Kp / group]
 
 
-def _group_of(q, dev, dims: int, name: str) -> int:
-    """q holds contiguous int4 rows with `dims` dimensions on dev; returns the group."""
-    import torch
+def _group_of(q, index: int, dims: int, name: str):
+    """q holds contiguous int4 rows with `dims` dimensions on GPU `index`; returns the group
+    and the codes' shape."""
     codes, scales = q if isinstance(q, Int4) else (None, None)
-    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.device == dev
-            and scales.device == dev and codes.dtype == torch.uint8 and codes.is_contiguous()
+    if not (_is(codes, index, torch.uint8) and isinstance(scales, torch.Tensor) and scales.get_device() == index
             and scales.is_contiguous()):
-        raise ValueError(f"{name} must be an Int4 of contiguous tensors, uint8 codes and scales, on {dev}")
-    *lead, Kb = codes.shape
-    *same, n = scales.shape
-    if len(lead) != dims - 1 or lead != same or Kb == 0 or Kb % 64 or n == 0 or 2 * Kb % n or \
-            2 * Kb // n not in (32, 64, 128):
+        raise ValueError(f"{name} must be an Int4 of contiguous tensors, uint8 codes and scales, on GPU {index}")
+    shape, (*same, n) = codes.shape, scales.shape
+    Kp = shape[-1] * 2
+    if len(shape) != dims or [*shape[:-1]] != same or Kp == 0 or Kp % 128 or n == 0 or Kp % n or \
+            Kp // n not in (32, 64, 128):
         raise ValueError(f"{name}: codes [..., Kp / 2] and scales [..., Kp / group] of the same rows with {dims} "
                          "dimensions, Kp a multiple of 128, group 32, 64 or 128")
-    return 2 * Kb // n
+    return Kp // n, shape
 
 
 def _new_int4(lead, Kp: int, group: int, u8, dtype, dev) -> Int4:
@@ -431,7 +435,6 @@ def int4_quantize(w, group: int = 128, *, scale_dtype=None, out: Optional[Int4] 
     stride as for mxfp4_quantize.  group: 32, 64 or 128 columns to a scale.  scale_dtype:
     bfloat16 or float16, the type of the x that the weights will meet (default: w's, or
     bfloat16 for float32 weights)."""
-    import torch
     if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dim() >= 1):
         raise ValueError("w must be a GPU tensor of at least one dimension")
     dt, dev = _code(w.dtype, "w", True), w.device
@@ -449,7 +452,7 @@ def int4_quantize(w, group: int = 128, *, scale_dtype=None, out: Optional[Int4] 
     if out is None:
         new = lead, Kp, group, torch.uint8, scale_dtype, dev
         out = _new_int4(*new) if foreign is None else _allocate(foreign, dev, _new_int4, *new)
-    elif _group_of(out, dev, w.dim(), "out") != group or out.codes.shape != (*lead, Kp // 2) or \
+    elif _group_of(out, w.get_device(), w.dim(), "out")[0] != group or out.codes.shape != (*lead, Kp // 2) or \
             out.scales.dtype != scale_dtype:
         raise ValueError(f"out must hold codes {(*lead, Kp // 2)} and {scale_dtype} scales {(*lead, Kp // group)}")
     rc = _call(dev, lib().moe_int4_quantize, w.data_ptr(), dt, rows, K, row_stride, group, sdt, out.codes.data_ptr(),
@@ -468,26 +471,22 @@ def int4_matvec(x, w: Int4, ids, *, gated: bool = False, weights=None, out=None,
     [E, N] of K columns, scales of x's type.  ids: int32 [M, k]; a pick outside [0, E)
     gives zeros.  Returns p [M, k, N]; with `gated` [M, k, N / 2], silu(p[..., :N / 2]) *
     p[..., N / 2:]; with weights (float32 [M, k]) their sum over the picks [M, N]."""
-    import torch
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.is_contiguous()):
         raise ValueError("x must be a contiguous [M, K] or [M, k, K] GPU tensor")
-    xdt, dev, xshape = x.dtype, x.device, x.shape
+    xdt, dev, index, xshape = x.dtype, x.device, x.get_device(), x.shape
     dt = _code(xdt, "x")
-    if not (isinstance(ids, torch.Tensor) and ids.dtype == torch.int32 and ids.device == dev and ids.is_contiguous()
-            and ids.dim() == 2):
-        raise ValueError(f"ids must be a contiguous int32 [M, k] tensor on {dev}")
+    _matrix(ids, 2, "ids", index, torch.int32)
     M, k = ids.shape
-    group = _group_of(w, dev, 3, "w")
+    group, (E, N, half) = _group_of(w, index, 3, "w")
     if w.scales.dtype != xdt:
         raise ValueError("w's scales must have x's type")
-    E, N, half = w.codes.shape
     K, slots = xshape[-1], len(xshape) == 3
     if xshape[:-1] != ((M, k) if slots else (M,)) or (K + 127) // 128 * 64 != half:
         raise ValueError(f"x must have shape ({M}, K) or ({M}, {k}, K), K columns of w")
     if gated and (weights is not None or N % 2):
         raise ValueError("gated results need an even N and take no weights")
     if weights is not None:
-        _check_weights(weights, M, k, dev)
+        _check_weights(weights, M, k, dev, index)
     _no_grad("int4_matvec", x, weights)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (M, N) if weights is not None else (M, k, N // 2 if gated else N), xdt, dev, foreign)
