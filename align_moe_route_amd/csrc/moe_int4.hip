@@ -355,7 +355,8 @@ extern "C" int moe_int4_matvec(const void* x, int dtype, const uint8_t* codes, c
                                int mode, void* y, void* stream) {
   if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K < 1 || K > 262144 || N < 1 || N > 1 << 20 || !group_ok(group) ||
       (dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) || mode < MRS_INT4_PLAIN || mode > MRS_INT4_SUM ||
-      (mode == MRS_INT4_GATED && N % 2 != 0) || (weights != nullptr) != (mode == MRS_INT4_SUM))
+      (mode == MRS_INT4_GATED && N % 2 != 0) ||
+      (M > 0 && (weights != nullptr) != (mode == MRS_INT4_SUM)))  // an empty one has no address
     return MRS_ERR_INVALID_ARG;
   if ((int64_t)N * ((K + 127) / 128 * 4) > INT32_MAX / 16) return MRS_ERR_OVERFLOW;  // 32-bit offsets in a matrix
   if (M == 0) return MRS_OK;

@@ -326,7 +326,8 @@ extern "C" int moe_combine(const void* y, int dtype, const int32_t* rows, const 
 extern "C" int moe_combine_backward(const void* dout, const void* y, int dtype, const int32_t* rows,
                                     const int32_t* sorted_ids, const int32_t* num_post_pad, const float* weights,
                                     int64_t capacity, int M, int k, int N, void* dy, float* dweights, void* stream) {
-  if (capacity < 0 || M < 0 || k < 1 || k > 64 || N < 1 || N > kMaxCols || !half_dtype(dtype) || !y != !dweights)
+  if (capacity < 0 || M < 0 || k < 1 || k > 64 || N < 1 || N > kMaxCols || !half_dtype(dtype) ||
+      (M > 0 && !y != !dweights))  // an empty dweights has no address
     return MRS_ERR_INVALID_ARG;
   if ((int64_t)M * k > INT32_MAX || capacity > INT32_MAX) return MRS_ERR_OVERFLOW;
   if (M == 0) return MRS_OK;

@@ -125,7 +125,8 @@ int moe_combine(const void* y, int dtype, const int32_t* rows, const float* weig
  *   rows      moe_slot_rows of this metadata; a row named twice is undefined
  *   sorted_ids, num_post_pad  the metadata, `capacity` rows
  *   weights   [M, k] FP32 or NULL for ones
- *   y, dweights  both given, or both NULL (no gradient of the weights is wanted)
+ *   y, dweights  both given, or both NULL (no gradient of the weights is wanted); not
+ *             looked at where M is 0
  *   dy        [capacity, N] (rows below *num_post_pad are written)
  */
 int moe_combine_backward(const void* dout, const void* y, int dtype, const int32_t* rows, const int32_t* sorted_ids,

@@ -66,10 +66,10 @@ enum {
  *             makes the results that it takes part in NaN)
  *   codes     int4 rows [E, N] of K columns, 16-byte aligned; scales of x's dtype
  *   ids       [M, k] int32
- *   weights   [M, k] FP32 (MRS_INT4_SUM only, else NULL)
- *   M         >= 0;  k  1 .. 64;  E  1 .. 4096;  K  1 .. 262144;  N  1 .. 2^20 with N * Kp / 2
- *             below 2^31 bytes (MRS_ERR_OVERFLOW), even
- *             for MRS_INT4_GATED
+ *   weights   [M, k] FP32 (MRS_INT4_SUM only, else NULL; not looked at where M is 0)
+ *   M         >= 0;  k  1 .. 64;  E  1 .. 4096;  K  1 .. 262144, any with the codes' Kp
+ *   N         1 .. 2^20, even for MRS_INT4_GATED; N * Kp / 2 below 2^31 bytes
+ *             (MRS_ERR_OVERFLOW)
  *   y         of x's dtype, 2-byte aligned
  * Asynchronous on `stream`; one launch; allocates nothing.  Returns MRS_OK or a
  * negative MRS_ERR_* code before any launch.

@@ -120,3 +120,10 @@ def test_int4_matvec_codes(kw, code):
     c.update(kw)
     assert amr.lib().moe_int4_matvec(c["x"], c["dt"], c["codes"], c["scales"], c["ids"], c["v"], c["M"], c["k"], c["E"],
                                      c["K"], c["N"], c["group"], c["slot"], c["mode"], c["y"], None) == code
+
+
+def test_empty_tensors_have_no_address():
+    """Without a token the weights of a sum, and their gradient, are empty."""
+    L = amr.lib()
+    assert L.moe_combine_backward(None, P, 1, None, P, P, None, 64, 0, 2, 8, P, None, None) == 0
+    assert L.moe_int4_matvec(None, 1, P, P, None, None, 0, 2, 8, 64, 16, 32, 0, 2, None, None) == 0
