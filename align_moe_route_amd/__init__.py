@@ -34,6 +34,7 @@ MRS_X_SORTED = 1
 MRS_INT4_PLAIN = 0
 MRS_INT4_GATED = 1
 MRS_INT4_SUM = 2
+MRS_TILE_NARROW = 1 << 16
 FLAG_FORCE_SINGLE_WG = 1
 FLAG_FORCE_MULTI_WG = 2
 FLAG_FORCE_EXACT = 4

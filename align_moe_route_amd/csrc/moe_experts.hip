@@ -21,10 +21,11 @@ namespace {
 //
 // What bounds them is how fast a compute unit takes operands out of its L2 (measured:
 // 120 GB/s in whole 128-byte lines, 62 in halves of lines, 37 at odd addresses; LDS reads
-// are 350 to 450), beside the matrix units at the clock that the power leaves. So: tiles as large as the
-// registers hold, operands straight into LDS in whole lines where rows are whole chunks
-// (steps of 64 along c), loads, LDS reads and matrix instructions of a wave interleaved,
-// and what an expert's tiles share read from one L2 at about the same time.
+// are 350 to 450), beside the matrix units at the clock that the power leaves. So: tiles as
+// large as the registers hold where there are enough of them for every compute unit, and
+// narrow ones where there are not; operands straight into LDS in whole lines where rows are
+// whole chunks (steps of 64 along c); loads, LDS reads and matrix instructions of a wave
+// interleaved; and what an expert's tiles share read from one L2 at about the same time.
 //   8192 tokens, 896 experts, top-16, K 3584, N 768, blocks of 128: y in 1250 us; the bytes
 //   that must move take 1075 at a copy's 4.9 TB/s (weights 4.9 GB); 577 TFLOP/s of routes
 //   8192 tokens, 64 experts, top-8, the same K and N: dx in 480 us, dw in 400 (750 and 900
@@ -39,9 +40,9 @@ struct GArgs {
   int I, J, C;    // sizes of i, j, c (I: kWeights only; C: the others only)
   int row_limit;  // rows the metadata can hold: (max_rows / block) * block
   int nrt, nct;   // tiles of i (over all sorted rows, or of one expert), tiles of j
+  int run;        // log2 of the row tiles of a run
   bool tiny;      // an operand's rows have fewer than eight values
 };
-
 
 // Operand tiles in LDS, in 16-byte chunks of eight values, a step of STEP values of c.
 //
@@ -129,13 +130,10 @@ __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& f
 }
 
 constexpr int kXcds = 8;
-// Workgroup h goes to XCD h mod 8.  Runs of kRun consecutive row tiles go to the XCDs in turn,
-// the column tiles of a row tile one after another (runs of 1, 2, 4, 8, 16, 32: the case above
-// 1333, 1285, 1261, 1272, 1285, 1258 us; 8192 tokens of 64 experts, top-4 251, 226, 221, 220, 256,
-// 298; 16 tokens of 64 experts 10.7, 10.7, 11.1, 13.2, 17.3, 32).  kWeights: an expert's column
-// tiles go to the XCDs in turn with all their row tiles, so that large experts are everyone's
-// (whole experts in turn 541 us, so 435).
-constexpr int kRun = 4;
+// Workgroup h goes to XCD h mod 8.  Runs of consecutive row tiles (run_of below) go to the XCDs
+// in turn, the column tiles of a row tile one after another.  kWeights: an expert's column tiles
+// go to the XCDs in turn with all their row tiles, so that large experts are everyone's (whole
+// experts in turn 541 us, so 435).
 constexpr int kRowsAhead = 4096;  // rows of an expert whose sources are kept in LDS at once (kWeights)
 
 // A tile of BM x BN results by NW waves, in steps of STEP values of c, S stages of LDS.
@@ -147,7 +145,7 @@ struct Shape {
   static constexpr int FM = TR / WI / 32, FN = BN / WJ / 32;  // operands of a wave
   static constexpr int kThreads = NW * 64;
   // workgroups of a compute unit by their LDS (160 KB), and so waves of a SIMD
-  static constexpr int kPerSimd = (NW == 4 && (TR + BN) * STEP * 2 * S <= 76 << 10 ? 2 : 1) * NW / 4;
+  static constexpr int kPerSimd = NW < 4 ? 1 : (NW == 4 && (TR + BN) * STEP * 2 * S <= 76 << 10 ? 2 : 1) * NW / 4;
 };
 
 template <int DIR, typename P>
@@ -186,7 +184,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     c_first = first * g.block, c_end = last * g.block;
   } else {
     const int h = blockIdx.x, x = h % kXcds, j = h / kXcds, i = j / g.nct;
-    const int rt = (i / kRun * kXcds + x) * kRun + i % kRun;
+    const int rt = (i >> g.run << 3 | x) << g.run | (i & ((1 << g.run) - 1));
     if (rt >= g.nrt) return;
     i0 = rt * BM, j0 = j % g.nct * BN;
     // asked for together, before any is looked at
@@ -578,58 +576,90 @@ constexpr int kCols = 256;
 //     above); 512 tokens of 896 experts 955, 1213, 1122
 //   kWeights through registers: 128 x 128 by 8 waves 21.3 (777 tokens of 24 experts, K 1000,
 //     N 397), by 4 waves 26.3, 128 x 256 24.0, 256 x 256 34 (it spills)
-template <int DIR, int BM>
+template <int DIR, int BM, int BN>
 struct ShapeOf;
 template <>
-struct ShapeOf<kForward, 128> : Shape<128, kCols, 8, 64, 3> {};
+struct ShapeOf<kForward, 128, kCols> : Shape<128, kCols, 8, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 64> : Shape<64, kCols, 4, 64, 3> {};
+struct ShapeOf<kForward, 64, kCols> : Shape<64, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 32> : Shape<32, kCols, 4, 64, 3> {};
+struct ShapeOf<kForward, 32, kCols> : Shape<32, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kForward, 16> : Shape<16, kCols, 4, 64, 3> {};
+struct ShapeOf<kForward, 16, kCols> : Shape<16, kCols, 4, 64, 3> {};
 template <>
-struct ShapeOf<kRows, 128> : Shape<128, kCols, 4, 32, 3> {};
+struct ShapeOf<kRows, 128, kCols> : Shape<128, kCols, 4, 32, 3> {};
 template <>
-struct ShapeOf<kRows, 64> : Shape<64, kCols, 4, 32, 3> {};
+struct ShapeOf<kRows, 64, kCols> : Shape<64, kCols, 4, 32, 3> {};
 template <>
-struct ShapeOf<kRows, 32> : Shape<32, kCols, 4, 32, 4> {};
+struct ShapeOf<kRows, 32, kCols> : Shape<32, kCols, 4, 32, 4> {};
 template <>
-struct ShapeOf<kRows, 16> : Shape<16, kCols, 4, 32, 4> {};
+struct ShapeOf<kRows, 16, kCols> : Shape<16, kCols, 4, 32, 4> {};
 template <>
-struct ShapeOf<kWeights, 256> : Shape<256, kCols, 8, 32, 3> {};  // straight into LDS
+struct ShapeOf<kWeights, 256, kCols> : Shape<256, kCols, 8, 32, 3> {};  // straight into LDS
 template <>
-struct ShapeOf<kWeights, 128> : Shape<128, 128, 8, 32, 3> {};  // through registers
+struct ShapeOf<kWeights, 128, 128> : Shape<128, 128, 8, 32, 3> {};  // through registers, or few of them
+// Narrow ones, for few workgroups
+constexpr int narrow(int dir) { return dir == kForward ? 64 : 128; }
+template <int BM>
+struct ShapeOf<kForward, BM, narrow(kForward)> : Shape<BM, narrow(kForward), 2, 64, 4> {};
+template <int BM>
+struct ShapeOf<kRows, BM, narrow(kRows)> : Shape<BM, narrow(kRows), 4, 32, 4> {};
 
 struct Launch {
   const void* kernel;
   int threads;
 };
 
-template <typename H, int DIR, bool F32, bool DIRECT, int BM>
+template <typename H, int DIR, bool F32, bool DIRECT, int BM, int BN>
 Launch launch_of() {
-  typedef ShapeOf<DIR, BM> P;
+  typedef ShapeOf<DIR, BM, BN> P;
   return {reinterpret_cast<const void*>(k_product<H, DIR, P, F32, DIRECT>), P::kThreads};
 }
 
-template <typename H, int DIR, bool F32, bool DIRECT>
+template <typename H, int DIR, bool F32, bool DIRECT, int BN>
 Launch product_kernel(int bm) {
+  switch (bm) {
+    case 64: return launch_of<H, DIR, F32, DIRECT, 64, BN>();
+    case 32: return launch_of<H, DIR, F32, DIRECT, 32, BN>();
+    default: return launch_of<H, DIR, F32, DIRECT, 16, BN>();
+  }
+}
+
+template <typename H, int DIR, bool F32, bool DIRECT>
+Launch product_kernel(int bm, int bn) {
   if constexpr (DIR == kWeights) {
-    return launch_of<H, DIR, F32, DIRECT, DIRECT ? 256 : 128>();
-  } else {
-    switch (bm) {
-      case 128: return launch_of<H, DIR, F32, DIRECT, 128>();
-      case 64: return launch_of<H, DIR, F32, DIRECT, 64>();
-      case 32: return launch_of<H, DIR, F32, DIRECT, 32>();
-      default: return launch_of<H, DIR, F32, DIRECT, 16>();
+    if constexpr (DIRECT) {
+      if (bm == 256) return launch_of<H, DIR, F32, DIRECT, 256, kCols>();
     }
+    return launch_of<H, DIR, F32, DIRECT, 128, 128>();
+  } else {
+    if (bn != kCols) return product_kernel<H, DIR, F32, DIRECT, narrow(DIR)>(bm);
+    if (bm == 128) return launch_of<H, DIR, F32, DIRECT, 128, kCols>();
+    return product_kernel<H, DIR, F32, DIRECT, kCols>(bm);
   }
 }
 
 template <typename H, int DIR>
-Launch product_kernel(bool f32, int bm, bool direct) {
-  if (direct) return f32 ? product_kernel<H, DIR, true, true>(bm) : product_kernel<H, DIR, false, true>(bm);
-  return f32 ? product_kernel<H, DIR, true, false>(bm) : product_kernel<H, DIR, false, false>(bm);
+Launch product_kernel(bool f32, int bm, int bn, bool direct) {
+  if (direct) return f32 ? product_kernel<H, DIR, true, true>(bm, bn) : product_kernel<H, DIR, false, true>(bm, bn);
+  return f32 ? product_kernel<H, DIR, true, false>(bm, bn) : product_kernel<H, DIR, false, false>(bm, bn);
+}
+
+// The row tiles of a run, as a power of two: those that share an expert's weights, up to four
+// (twice the average, for experts are uneven), and the tiles of a block, of which the first
+// ones hold the routes, as long as that leaves runs for every XCD.  Runs of 1, 2 and 4 (us):
+// 64 tokens of 896 experts, top-16, K 3584, N 768, blocks of 16 441, 441, 457; 512 tokens of
+// 64, top-8, blocks of 128 71, 71, 99; 2048 tokens of them, blocks of 64 227, 191, 180; 777
+// of 24, top-6, K 1000, N 397 18.7, 17.5, 17.1; runs of 1, 2, 4, 8, 16, 32: the case above 1333,
+// 1285, 1261, 1272, 1285, 1258.
+int run_of(int64_t average, int64_t row_tiles, int bm, int block) {
+  int64_t want = (2 * average + bm - 1) / bm;
+  want = want > 4 ? 4 : want;
+  const int64_t of_block = block / bm < row_tiles / 4 ? block / bm : row_tiles / 4;
+  if (of_block > want) want = of_block > 8 ? 8 : of_block;
+  int log2 = 0;
+  while (1 << log2 < want) ++log2;
+  return log2;
 }
 
 constexpr int kMaxCols = 1 << 20;
@@ -637,10 +667,11 @@ constexpr int kMaxCols = 1 << 20;
 template <int DIR>
 int product(const void* a, const void* b, int dtype, const int32_t* sid, const int32_t* eob, const int32_t* npp, int M,
             int k, int E, int K, int N, int block, int x_rows, int out_dtype, void* out, void* stream, int tile = 0) {
+  const int rows = tile & ~MRS_TILE_NARROW;
   if (M < 0 || k < 1 || k > 64 || E < 1 || E > 4096 || K < 1 || K > kMaxCols || N < 1 || N > kMaxCols || block < 16 ||
       block % 16 != 0 || (dtype != MRS_DTYPE_BF16 && dtype != MRS_DTYPE_F16) ||
       (out_dtype != dtype && out_dtype != MRS_DTYPE_F32) || (x_rows != MRS_X_TOKENS && x_rows != MRS_X_SORTED) ||
-      (tile != 0 && ((tile != 16 && tile != 32 && tile != 64 && tile != 128) || block % tile != 0)))
+      (tile != 0 && ((rows != 16 && rows != 32 && rows != 64 && (rows != 128 || tile != rows)) || block % rows != 0)))
     return MRS_ERR_INVALID_ARG;
   const int64_t max_rows = moe_route_sort_max_rows(M, E, k, block);
   if (max_rows < 0) return MRS_ERR_OVERFLOW;
@@ -663,27 +694,41 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
   int bm, bn = kCols;
   int64_t grid;
   if constexpr (DIR == kWeights) {
-    typedef ShapeOf<kWeights, 256> Large;
-    typedef ShapeOf<kWeights, 128> Staged;
-    bm = direct ? Large::BM : Staged::BM, bn = direct ? Large::BN : Staged::BN;
+    const int64_t large = (int64_t)E * ((N + 255) / 256) * ((K + 255) / 256);
+    // us, 256 x 256 / 128 x 128: 200 tokens of 16 experts, top-2, K 512, N 256 (32 large tiles) 7.7 /
+    // 5.0; 32 of 16, K 768, N 512 (96) 7.9 / 7.0; 777 of 24, top-6, K 1000, N 400 (192) 15.5 / 19.6
+    bm = direct && large >= 128 ? 256 : 128;
+    if (bm == 128) bn = 128;
     g.I = N, g.J = K;
     g.nrt = (N + bm - 1) / bm, g.nct = (K + bn - 1) / bn;
     grid = ((int64_t)E * g.nct + kXcds - 1) / kXcds * kXcds * g.nrt;
   } else {
     g.C = DIR == kForward ? K : N, g.J = DIR == kForward ? N : K;
-    // The largest tile that divides the block, but a smaller one where fewer than 128
-    // workgroups would come of it (us; 300 tokens of 8 experts, top-2, K 2048, N 1024, blocks
-    // of 128: tiles of 128 26.8, 64 21.5, 32 17.3; 777 tokens of 24, top-6, K 1000, N 400: 19.1,
-    // 16.6, 26.7).
+    // The largest tile that divides the block, but 64 rows where fewer than 128 workgroups would
+    // come of it, and then narrow tiles where they are fewer still (kForward: fewer than 256 where
+    // an expert is one tile, so that its weights are read once either way).  us, wide / narrow,
+    // kForward: 300 tokens of 8 experts, top-2, K 2048, N 1024 20.8 / 15.4; 200 of 24, top-6, K
+    // 1000, N 400 12.1 / 8.7; 48 of 31, top-3, K 1713, N 109 30.8 / 12.9; one of 896, top-16, K
+    // 3584, N 768 26.2 / 18.0, four of them 59.8 / 53.4; 512 of 8, top-2, K 3584, N 1536 (96
+    // workgroups) 34 / 45; 777 of 24 (192) 17.1 / 23.  kRows: 200 of 24 8.0 / 7.1, one of 896
+    // (224) 16.1 / 16.5, 48 of 31 (217) 9.1 / 11.1.  Narrow tiles of few rows an expert are of 32
+    // rows (48 of 31 16.7, so 12.9; 100 rows an expert 12.7 for 13.6).
     bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
-    const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E;
-    while (bm > 32 && used * ((routes / used + bm - 1) / bm) * ((g.J + bn - 1) / bn) < 128) bm /= 2;
-    if (tile != 0) bm = tile;
+    const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E, average = (routes + used - 1) / used;
+    auto tiles = [&] { return used * ((average + bm - 1) / bm) * ((g.J + bn - 1) / bn); };
+    while (bm > 64 && tiles() < 128) bm /= 2;
+    if (bm <= 64 && tiles() < (DIR == kForward && average <= bm ? 256 : 128)) {
+      bn = narrow(DIR);
+      if (bm == 64 && average <= 32) bm = 32;
+    }
+    if (tile != 0) bm = rows, bn = tile == rows ? kCols : narrow(DIR);
     g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
-    grid = ((int64_t)g.nrt + kXcds * kRun - 1) / (kXcds * kRun) * kRun * kXcds * g.nct;
+    g.run = run_of(average, used * ((average + bm - 1) / bm), bm, block);
+    const int64_t group = kXcds << g.run;
+    grid = (g.nrt + group - 1) / group * group * g.nct;
   }
-  const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, direct)
-                                           : product_kernel<FP16, DIR>(f32, bm, direct);
+  const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, bn, direct)
+                                           : product_kernel<FP16, DIR>(f32, bm, bn, direct);
   if (grid * p.threads > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   void* params[] = {&g};
   return hipLaunchKernel(p.kernel, dim3((unsigned)grid), dim3(p.threads), params, 0,

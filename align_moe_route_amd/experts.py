@@ -110,8 +110,8 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     x holds max_rows rows in sorted order and row(r) = r.  w: [E, N, K] of x's type.
     Any K and N; block: a multiple of 16.  out_dtype: x's type (default) or float32.
     Returns y [max_rows, N]; rows at or past num_post_pad are left as they were.  tile:
-    rows of a tile (16, 32, 64 or 128, dividing block) in place of the choice by sizes,
-    for tests and tuning."""
+    rows of a tile (16, 32, 64 or 128, dividing block; MRS_TILE_NARROW | 16, 32 or 64) in
+    place of the choice by sizes, for tests and tuning."""
     dt, dev, index = _first(x, 2, "x")
     _matrix(w, 3, "w", index, x.dtype)
     E, N, K = w.shape

@@ -60,7 +60,9 @@ int moe_grouped_gemm_dx(const void* dy, const void* w, int dtype, const int32_t*
                         int block, int dx_dtype, void* dx, void* stream);
 
 /* The two products above by tiles of `tile` rows (16, 32, 64 or 128, dividing block; 0
- * for the choice by sizes), for tests and tuning: the same results. */
+ * for the choice by sizes), the first three of them also with fewer columns (or'ed with
+ * MRS_TILE_NARROW), for tests and tuning: the same results. */
+enum { MRS_TILE_NARROW = 1 << 16 };
 int moe_grouped_gemm_ex(const void* x, const void* w, int dtype, const int32_t* sorted_ids,
                         const int32_t* expert_of_block, const int32_t* num_post_pad, int M, int k, int E, int K, int N,
                         int block, int x_rows, int y_dtype, void* y, void* stream, int tile);

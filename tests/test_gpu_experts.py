@@ -75,7 +75,8 @@ def test_products(shape, by_tokens, f32, dtype):
 
 
 @pytest.mark.parametrize("K,N", [(200, 72), (1096, 520), (203, 77), (64, 1040), (771, 9)])
-@pytest.mark.parametrize("tile", [16, 32, 64, 128])
+@pytest.mark.parametrize("tile", [16, 32, 64, 128, 16 | amr.MRS_TILE_NARROW, 32 | amr.MRS_TILE_NARROW,
+                                  64 | amr.MRS_TILE_NARROW])
 def test_tiles(tile, K, N):
     """Every tile size, with rows of whole chunks and of others, short and long sums, tiles
     whose waves have no row with a slot, and both kinds of x rows."""

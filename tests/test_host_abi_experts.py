@@ -127,3 +127,11 @@ def test_empty_tensors_have_no_address():
     L = amr.lib()
     assert L.moe_combine_backward(None, P, 1, None, P, P, None, 64, 0, 2, 8, P, None, None) == 0
     assert L.moe_int4_matvec(None, 1, P, P, None, None, 0, 2, 8, 64, 16, 32, 0, 2, None, None) == 0
+
+
+@pytest.mark.parametrize("tile,code", [(amr.MRS_TILE_NARROW, -1), (amr.MRS_TILE_NARROW | 128, -1),
+                                       (amr.MRS_TILE_NARROW | 64, 0), (amr.MRS_TILE_NARROW * 2 | 64, -1)])
+def test_narrow_tile_codes(tile, code):
+    L = amr.lib()
+    assert L.moe_grouped_gemm_ex(P, P, 1, P, P, P, 0, 2, 8, 40, 24, 128, 0, 1, P, None, tile) == code
+    assert L.moe_grouped_gemm_dx_ex(P, P, 1, P, P, P, 0, 2, 8, 40, 24, 128, 1, P, None, tile) == code
