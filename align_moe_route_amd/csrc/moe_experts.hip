@@ -174,6 +174,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   const int wi = wv / WJ * FM * 32, wj = wv % WJ * FN * 32;  // this wave's part of the tile
   int i0, j0, e, c_first = 0, c_end;  // the tile, its expert, the range of c
   uint64_t has = ~0ull;               // this wave's rows that hold a slot
+  bool any = true;                    // some row of the tile does
   if constexpr (DIR == kWeights) {
     const int h = blockIdx.x, x = h % kXcds, q = h / kXcds, u = q / g.nrt * kXcds + x;
     e = u / g.nct;
@@ -198,6 +199,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
     }
     __syncthreads();
     has = __ballot(lane < FM * 32 && l.row[wi + lane % (FM * 32)] >= 0);
+    any = __ballot(l.row[lane % TR] >= 0 || l.row[(lane + 64) % TR] >= 0) != 0;
   }
   e = __builtin_amdgcn_readfirstlane(e);
 
@@ -495,7 +497,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
       run(used, true);
     }
   } else {
-    run((c_end + kStep - 1) / kStep, has != 0);
+    if (any) run((c_end + kStep - 1) / kStep, has != 0);  // a tile of padding reads nothing
   }
 
   // Result register v of lane l: column (of j) 8 (v / 4) + 4 (l / 32) + v mod 4, row (of i)
