@@ -714,14 +714,19 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     // 3584, N 768 26.2 / 18.0, four of them 59.8 / 53.4; 512 of 8, top-2, K 3584, N 1536 (96
     // workgroups) 34 / 45; 777 of 24 (192) 17.1 / 23.  kRows: 200 of 24 8.0 / 7.1, one of 896
     // (224) 16.1 / 16.5, 48 of 31 (217) 9.1 / 11.1.  Narrow tiles of few rows an expert are of 32
-    // rows (48 of 31 16.7, so 12.9; 100 rows an expert 12.7 for 13.6).
+    // rows (48 of 31 16.7, so 12.9; 100 rows an expert 12.7 for 13.6), and kForward takes them for
+    // any number of such experts where operands go through registers, which are slower to fill
+    // (256 of 256, top-8, K 1203, N 515 102 / 76; 40 of 120, top-14, K 1209, N 676 58 / 39; 64 of
+    // 896, top-16, K 1001, N 397 129 / 111; with whole chunks, K 2048, N 768, 512 of 128 97 / 99).
     bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
     const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E, average = (routes + used - 1) / used;
     auto tiles = [&] { return used * ((average + bm - 1) / bm) * ((g.J + bn - 1) / bn); };
     while (bm > 64 && tiles() < 128) bm /= 2;
-    if (bm <= 64 && tiles() < (DIR == kForward && average <= bm ? 256 : 128)) {
+    const bool short_rows = DIR == kForward && !direct && average <= 32;
+    const bool fits = row_limit * ((g.J + 63) / 64) < 1 << 28;  // more threads than wide ones, fewer than 2^32
+    if (fits && (short_rows || (bm <= 64 && tiles() < (DIR == kForward && average <= bm ? 256 : 128)))) {
       bn = narrow(DIR);
-      if (bm == 64 && average <= 32) bm = 32;
+      if (bm > 32 && average <= 32) bm = 32;
     }
     if (tile != 0) bm = rows, bn = tile == rows ? kCols : narrow(DIR);
     g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
