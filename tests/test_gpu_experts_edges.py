@@ -44,6 +44,29 @@ def test_longest_rows(K, N):
     assert torch.equal(dw.float(), want)
 
 
+@pytest.mark.parametrize("M,E,k,K,N,block", [
+    (20, 6, 2, 203, 77, 256), (20, 6, 2, 200, 72, 1024), (300, 2, 1, 64, 600, 512), (700, 3, 1, 203, 600, 64),
+    (4000, 2, 1, 64, 2100, 128), (2000, 100, 2, 64, 520, 2048), (500, 40, 2, 64, 264, 48), (1500, 300, 1, 67, 130, 32),
+    (900, 300, 1, 72, 136, 96), (64, 64, 1, 40, 2048, 4096)])
+def test_choices_of_tiles(M, E, k, K, N, block):
+    """Tiles chosen by the sizes: few and many rows an expert, blocks of one tile and of many."""
+    r = Routed(ids_of(M, E, k, 3, 0.05), E, block)
+    x, w, dy = whole((M, K), 1, 1), whole((E, N, K), 2, 1), whole((r.cap, N), 3, 1)
+    live = np.flatnonzero(r.live)
+    expert = r.eob[live // block]
+    y = amr.grouped_gemm(x, w, *r.meta, k, block, out_dtype=torch.float32)
+    dx = amr.grouped_gemm_dx(dy, w, *r.meta, M, k, block, out_dtype=torch.float32)
+    dw = amr.grouped_gemm_dw(dy, x, E, *r.meta, k, block, out_dtype=torch.float32)
+    pad = torch.from_numpy(~r.live).cuda()
+    assert not y[:r.npp][pad].any() and not dx[:r.npp][pad].any()
+    for e in range(E):
+        at = torch.from_numpy(live[expert == e]).cuda()
+        a, b, d = x[torch.from_numpy(r.sid[live[expert == e]] // k).long().cuda()].double(), w[e].double(), dy[at].double()
+        assert torch.equal(y[at].double(), a @ b.t())
+        assert torch.equal(dx[at].double(), d @ b)
+        assert torch.equal(dw[e].double(), d.t() @ a)
+
+
 def test_most_experts_and_picks():
     M, E, k, K, N, block = 3, 4096, 64, 40, 24, 16
     ids = ids_of(M, E, k, 2)
