@@ -201,12 +201,31 @@ def raw_call(logits_ptr, bias_ptr, M, E, k, n_group, topk_group, block, out_ids_
                                        dtype, ws_ptr, ws_bytes, stream_ptr, flags, stats_ptr))
 
 
-class RouteSortOutput(NamedTuple):
+class _Route(NamedTuple):
     ids: "torch.Tensor"              # [M, k] int32, ascending expert ids per token
     weights: "torch.Tensor"          # [M, k] float32
     sorted_ids: "torch.Tensor"       # [max_rows] int32; [0, num_post_pad) defined
     expert_of_block: "torch.Tensor"  # [max_blocks] int32; [0, num_post_pad/block) defined
     num_post_pad: "torch.Tensor"     # [1] int32 (device)
+
+
+class RouteSortOutput(_Route):
+    """A call's ids, weights and metadata.  One that a call of this package returned also
+    says how many experts the metadata numbers and the block that it was made for, for
+    checks by what reads it; made by hand, or of another's parts, it does not know."""
+    experts: Optional[int] = None
+    block: Optional[int] = None
+
+    def _replace(self, **kwargs):
+        same = kwargs.keys() <= {"ids", "weights"}  # the metadata, which is what the two are about
+        return _routed(super()._replace(**kwargs), self.experts if same else None, self.block if same else None)
+
+
+def _routed(out, experts: Optional[int], block: Optional[int]):
+    """`out`, which now holds metadata of so many experts and this block."""
+    if isinstance(out, RouteSortOutput):
+        out.experts, out.block = experts, block
+    return out
 
 
 # (device, stream handle) -> the workspaces made for that stream, the last the
@@ -348,7 +367,7 @@ def route_sort(logits, bias, k: int, n_group: int, topk_group: int, block: int, 
             out.expert_of_block.data_ptr(), out.num_post_pad.data_ptr(), dt, ws_ptr, ws_len, stream.cuda_stream))
         if rc != MRS_OK:
             raise RouteSortError(rc)
-        return out
+        return _routed(out, EL, block)
     args = (logits.data_ptr(), bias.data_ptr(), M, E, k, n_group, topk_group, block,
             out.ids.data_ptr(), out.weights.data_ptr(), out.sorted_ids.data_ptr(),
             out.expert_of_block.data_ptr(), out.num_post_pad.data_ptr(), dt, ws_ptr, ws_len,
@@ -364,11 +383,11 @@ def route_sort(logits, bias, k: int, n_group: int, topk_group: int, block: int, 
         rc = int(lib().moe_route_sort_profiled(*args, handles, ctypes.byref(n)))
         if rc != MRS_OK:
             raise RouteSortError(rc)
-        return out, n.value
+        return _routed(out, E, block), n.value
     rc = int(lib().moe_route_sort_ex(*args))
     if rc != MRS_OK:
         raise RouteSortError(rc)
-    return out
+    return _routed(out, E, block)
 
 
 def route_sort_static(logits, bias, k: int, n_group: int, topk_group: int, block: int, *,
@@ -409,7 +428,7 @@ def route_sort_static(logits, bias, k: int, n_group: int, topk_group: int, block
                                          stream.cuda_stream))
     if rc != MRS_OK:
         raise RouteSortError(rc)
-    return out
+    return _routed(out, E, block)
 
 
 def sigmoid_probe(x):
@@ -604,7 +623,7 @@ def gate_route_sort(hidden, w_gate, bias, k: int, n_group: int, topk_group: int,
                                        stream.cuda_stream))
     if rc != MRS_OK:
         raise RouteSortError(rc)
-    return logits, out
+    return logits, _routed(out, E, block)
 
 
 class MXFP4(NamedTuple):
@@ -1038,7 +1057,8 @@ def route_sort_train(logits, bias, k: int, n_group: int, topk_group: int, block:
     call balance_loss and router_backward themselves."""
     w, loss, ids, sid, eob, npp, counts, tokens, shares = _route_train_function().apply(
         logits, bias, (k, n_group, topk_group, block), float(balance_coef), seq_offsets, mask)
-    return RouteSortOutput(ids, w, sid, eob, npp), BalanceOutput(loss, counts, tokens, shares)
+    route = _routed(RouteSortOutput(ids, w, sid, eob, npp), logits.shape[1], block)
+    return route, BalanceOutput(loss, counts, tokens, shares)
 
 
 _EXPERTS = ("Int4", "combine", "combine_backward", "experts_train", "grouped_gemm", "grouped_gemm_dw", "grouped_gemm_dx",

@@ -109,9 +109,10 @@ def grouped_gemm(x, w, sorted_ids, expert_of_block, num_post_pad, k: int, block:
     x: [M, K] bfloat16 or float16, row(r) = sorted_ids[r] // k; with `tokens` = M given
     x holds max_rows rows in sorted order and row(r) = r.  w: [E, N, K] of x's type.
     Any K and N; block: a multiple of 16.  out_dtype: x's type (default) or float32.
-    Returns y [max_rows, N]; rows at or past num_post_pad are left as they were.  tile:
-    rows of a tile (16, 32, 64 or 128, dividing block; MRS_TILE_NARROW | 16, 32 or 64) in
-    place of the choice by sizes, for tests and tuning."""
+    Returns y [max_rows, N]; rows at or past num_post_pad, and those of a block whose
+    expert w does not hold, are left as they were.  tile: rows of a tile (16, 32, 64 or
+    128, dividing block; MRS_TILE_NARROW | 16, 32 or 64) in place of the choice by sizes,
+    for tests and tuning."""
     dt, dev, index = _first(x, 2, "x")
     _matrix(w, 3, "w", index, x.dtype)
     E, N, K = w.shape
@@ -145,8 +146,9 @@ def grouped_gemm_dx(dy, w, sorted_ids, expert_of_block, num_post_pad, tokens: in
 
     dy: [max_rows, N], w: [E, N, K] of dy's type (bfloat16 or float16), tokens: M.
     Returns dx [max_rows, K] of dy's type (default) or float32; rows at or past
-    num_post_pad are left as they were.  Of an x that holds the tokens' rows the
-    gradient is combine(dx, slot_rows(...)).  tile: as for grouped_gemm."""
+    num_post_pad, and those of a block whose expert w does not hold, are left as they
+    were.  Of an x that holds the tokens' rows the gradient is combine(dx,
+    slot_rows(...)).  tile: as for grouped_gemm."""
     dt, dev, index = _first(dy, 2, "dy")
     _matrix(w, 3, "w", index, dy.dtype)
     E, N, K = w.shape
@@ -342,19 +344,40 @@ def combine_backward(dout, rows, sorted_ids, num_post_pad, *, weights=None, y=No
     return out if dv is None else (out, dv)
 
 
+def _holds_experts(route, E: int, block: int) -> bool:
+    """Whether the weights of E experts are known to hold every expert of the route; one
+    that is known to be of more experts or of another block is refused."""
+    experts, made_for = getattr(route, "experts", None), getattr(route, "block", None)
+    if experts is not None and experts > E:
+        raise ValueError(f"the route is of {experts} experts, w_up and w_down hold {E}")
+    if made_for is not None and made_for != block:
+        raise ValueError(f"the route was made for blocks of {made_for}, not {block}")
+    if experts is not None:
+        return True
+    M, k = route.weights.shape
+    rows, blocks = _sizes(M, E, k, block)  # they grow with the experts up to M k
+    return M * k > E and (route.sorted_ids.numel(), route.expert_of_block.numel()) == (rows, blocks)
+
+
+def _rows_of(whole: bool, sorted_ids, columns: int, dtype):
+    """The rows that a product writes into: NaN where it may leave some out."""
+    return None if whole else torch.full((sorted_ids.numel(), columns), float("nan"), dtype=dtype, device=sorted_ids.device)
+
+
 @functools.lru_cache(maxsize=1)
 def _experts_function():
     class Experts(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, w_up, w_down, weights, sorted_ids, expert_of_block, num_post_pad, block):
+        def forward(ctx, x, w_up, w_down, weights, sorted_ids, expert_of_block, num_post_pad, block, whole):
             meta = (sorted_ids, expert_of_block, num_post_pad)
             M, k = weights.shape
-            a = grouped_gemm(x, w_up, *meta, k, block)
+            a = grouped_gemm(x, w_up, *meta, k, block, out=_rows_of(whole, sorted_ids, w_up.shape[1], x.dtype))
             h = swiglu(a, num_post_pad)
-            y = grouped_gemm(h, w_down, *meta, k, block, tokens=M)
+            y = grouped_gemm(h, w_down, *meta, k, block, tokens=M,
+                             out=_rows_of(whole, sorted_ids, w_down.shape[1], x.dtype))
             rows = slot_rows(sorted_ids, num_post_pad, M, k)
             ctx.save_for_backward(x, w_up, w_down, weights, a, h, y, rows, *meta)
-            ctx.block = block
+            ctx.block, ctx.whole = block, whole
             return combine(y, rows, weights)
 
         @staticmethod
@@ -371,12 +394,15 @@ def _experts_function():
             if need_down:
                 d_down = grouped_gemm_dw(dy, h, E, *meta, k, block, tokens=M)
             if need_x or need_up:
-                da = swiglu_backward(a, grouped_gemm_dx(dy, w_down, *meta, M, k, block), num_post_pad)
+                dh = grouped_gemm_dx(dy, w_down, *meta, M, k, block,
+                                     out=_rows_of(ctx.whole, sorted_ids, w_down.shape[2], x.dtype))
+                da = swiglu_backward(a, dh, num_post_pad)
                 if need_up:
                     d_up = grouped_gemm_dw(da, x, E, *meta, k, block)
                 if need_x:
-                    dx = combine(grouped_gemm_dx(da, w_up, *meta, M, k, block), rows)
-            return dx, d_up, d_down, dv, None, None, None, None
+                    dx = combine(grouped_gemm_dx(da, w_up, *meta, M, k, block,
+                                                 out=_rows_of(ctx.whole, sorted_ids, w_up.shape[2], x.dtype)), rows)
+            return dx, d_up, d_down, dv, None, None, None, None, None
 
     return Experts
 
@@ -388,8 +414,11 @@ def experts_train(x, w_up, w_down, route, block: int):
     x: [M, H] bfloat16 or float16; w_up: [E, 2 I, H] (the gates' rows first) and w_down:
     [E, H, I] of x's type; route: what route_sort, or route_sort_train (whose weights
     pass the gradient on to the logits), returned for `block`.  Returns [M, H] with
-    gradients to x, both weights and route.weights.  To capture a training step in a
-    graph call the entry points themselves, as for route_sort_train."""
+    gradients to x, both weights and route.weights.  A route of more experts than the
+    weights hold, or of another block, is refused; of one made by hand, whose sizes do
+    not tell, tokens with a pick of an expert past the last get NaN, and so do their
+    gradients.  To capture a training step in a graph call the entry points themselves,
+    as for route_sort_train."""
     _, _, index = _first(x, 2, "x")
     _matrix(w_up, 3, "w_up", index, x.dtype)
     _matrix(w_down, 3, "w_down", index, x.dtype)
@@ -397,8 +426,10 @@ def experts_train(x, w_up, w_down, route, block: int):
     E, two, H = w_up.shape
     if x.shape[1] != H or two % 2 or tuple(w_down.shape) != (E, H, two // 2) or route.weights.shape[0] != x.shape[0]:
         raise ValueError("w_up must be [E, 2 I, H], w_down [E, H, I] and route.weights [M, k] for x [M, H]")
-    return _experts_function().apply(x, w_up, w_down, route.weights, route.sorted_ids, route.expert_of_block,
-                                     route.num_post_pad, block)
+    meta = (route.sorted_ids, route.expert_of_block, route.num_post_pad)
+    whole = _holds_experts(route, E, block)
+    _metadata(*meta, *_sizes(x.shape[0], E, route.weights.shape[1], block), x.device, index)
+    return _experts_function().apply(x, w_up, w_down, route.weights, *meta, block, whole)
 
 
 class Int4(NamedTuple):

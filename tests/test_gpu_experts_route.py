@@ -1,0 +1,81 @@
+"""experts_train with a route that does not belong to its weights: refused where that is
+known, NaN for the tokens that it concerns where it is not."""
+import numpy as np
+import pytest
+import torch
+
+import align_moe_route_amd as amr
+from experts_cases import Routed, ids_of, normal
+
+pytestmark = pytest.mark.gpu
+H, I, block = 40, 24, 32
+
+
+def weights(E):
+    return normal((E, 2 * I, H), torch.bfloat16, 2, H ** -0.5), normal((E, H, I), torch.bfloat16, 3, I ** -0.5)
+
+
+@pytest.mark.parametrize("M", [1, 50])
+def test_route_of_more_experts(M):
+    E, k = 16, 4
+    x, logits, bias = normal((M, H), torch.bfloat16, 1), normal((M, E), torch.float32, 4), torch.zeros(E, device="cuda")
+    hidden = normal((M, H), torch.bfloat16, 5)
+    routes = [amr.route_sort(logits, bias, k, 4, 2, block), amr.route_sort_train(logits, bias, k, 4, 2, block)[0],
+              amr.route_sort_static(logits, bias, k, 4, 2, block),
+              amr.gate_route_sort(hidden, normal((E, H), torch.bfloat16, 6), bias, k, 4, 2, block)[1]]
+    routes.append(amr.route_sort(logits, bias, k, 4, 2, block, out=amr.RouteSortOutput(*(t.clone() for t in routes[0]))))
+    for route in routes:
+        assert (route.experts, route.block) == (E, block)
+        amr.experts_train(x, *weights(E), route, block)
+        with pytest.raises(ValueError):
+            amr.experts_train(x, *weights(E // 2), route, block)
+        with pytest.raises(ValueError):
+            amr.experts_train(x, *weights(E), route, block // 2)
+    local = amr.route_sort(logits, bias, k, 4, 2, block, local=(3, 6))
+    amr.experts_train(x, *weights(6), local, block)
+    with pytest.raises(ValueError):
+        amr.experts_train(x, *weights(5), local, block)
+
+
+@pytest.mark.parametrize("M,E,held", [(3, 12, 7), (40, 9, 6)])
+def test_route_made_by_hand(M, E, held):
+    """Weights of the first experts only: the others' tokens are NaN, with their gradients."""
+    k = 2
+    ids = ids_of(M, E, k, 1)
+    ids[0] = 0, 1
+    ids[1] = 0, E - 1
+    r = Routed(ids, E, block)
+    w = weights(E)
+    v, dout = torch.rand(M, k, device="cuda"), normal((M, H), torch.bfloat16, 7)
+
+    def run(*w):
+        leaves = [t.clone().requires_grad_() for t in (normal((M, H), torch.bfloat16, 4), *w, v)]
+        out = amr.experts_train(*leaves[:3], amr.RouteSortOutput(r.ids, leaves[3], *r.meta), block)
+        out.backward(dout)
+        return [out, *(t.grad for t in leaves)]
+    out, dx, d_up, d_down, dv = run(*(t[:held].contiguous() for t in w))
+    want = run(*w)
+    gone = torch.from_numpy((ids >= held)).cuda()
+    token = gone.any(1)
+    assert out[token].isnan().all() and dx[token].isnan().all() and dv[gone].isnan().all()
+    assert torch.equal(out[~token], want[0][~token]) and torch.equal(dx[~token], want[1][~token])
+    assert torch.equal(dv[~gone], want[4][~gone])
+    assert torch.equal(d_up, want[2][:held]) and torch.equal(d_down, want[3][:held])
+    assert np.array_equal(token.cpu().numpy(), (ids >= held).any(1)) and 0 < int(token.sum()) < M
+
+
+def test_longer_buffers():
+    """Metadata in buffers that are longer than these sizes need."""
+    M, E, k = 30, 5, 2
+    r = Routed(ids_of(M, E, k, 1), E, block)
+    longer = [torch.cat([r.meta[0], torch.full((700,), 3, dtype=torch.int32, device="cuda")]),
+              torch.cat([r.meta[1], torch.full((9,), 77, dtype=torch.int32, device="cuda")]), r.meta[2]]
+    w, v, dout = weights(E), torch.rand(M, k, device="cuda"), normal((M, H), torch.bfloat16, 7)
+
+    def run(meta):
+        leaves = [t.clone().requires_grad_() for t in (normal((M, H), torch.bfloat16, 4), *w, v)]
+        out = amr.experts_train(*leaves[:3], amr.RouteSortOutput(r.ids, leaves[3], *meta), block)
+        out.backward(dout)
+        return [out, *(t.grad for t in leaves)]
+    for a, b in zip(run(longer), run(r.meta)):
+        assert a.isfinite().all() and torch.equal(a, b)
