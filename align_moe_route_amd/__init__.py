@@ -221,6 +221,13 @@ class RouteSortOutput(_Route):
         return _routed(super()._replace(**kwargs), self.experts if same else None, self.block if same else None)
 
 
+def _overwritten(*tensors):
+    """The caller's tensors, which a call is about to write: autograd is told, so that a
+    backward pass whose saved tensors they are is refused, and not wrong."""
+    import torch
+    torch._C._increment_version(tensors)
+
+
 def _routed(out, experts: Optional[int], block: Optional[int]):
     """`out`, which now holds metadata of so many experts and this block."""
     if isinstance(out, RouteSortOutput):
@@ -295,7 +302,8 @@ def route_sort(logits, bias, k: int, n_group: int, topk_group: int, block: int, 
 
     logits: [M, E] float32 or bfloat16 CUDA/HIP tensor, contiguous.
     bias:   [E] float32 tensor on the same device.
-    out:    optional preallocated RouteSortOutput (reused, nothing else written).
+    out:    optional preallocated RouteSortOutput (reused, nothing else written; a
+            backward pass that still needs what it held is refused by autograd).
     workspace: optional uint8 tensor of at least workspace_bytes() bytes that
             was zeroed once; by default a cached buffer of the call's stream
             (calls on different streams may then overlap in time).  Make the
@@ -349,6 +357,7 @@ def route_sort(logits, bias, k: int, n_group: int, topk_group: int, block: int, 
         )
     else:
         _check_route_output(out, M, k, rows, blocks, dev)
+        _overwritten(out.ids, out.weights, out.sorted_ids, out.expert_of_block, out.num_post_pad)
     if stats is not None:
         _check_tensor(stats, dev, torch.int32, 3, "stats")
     nbytes = workspace_bytes(M, E, k, block)
@@ -420,6 +429,7 @@ def route_sort_static(logits, bias, k: int, n_group: int, topk_group: int, block
                               torch.empty((1,), dtype=torch.int32, device=dev))
     else:
         _check_route_output(out, M, k, rows, blocks, dev)
+        _overwritten(out.ids, out.weights, out.sorted_ids, out.expert_of_block, out.num_post_pad)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     rc = int(lib().moe_route_sort_static(logits.data_ptr(), bias.data_ptr(), M, E, k, n_group, topk_group, block,
@@ -506,6 +516,7 @@ def sort_from_ids(ids, E: int, block: int, *, out: Optional[SortOutput] = None, 
                          torch.empty((1,), dtype=torch.int32, device=dev))
     else:
         _check_metadata(out.sorted_ids, out.expert_of_block, out.num_post_pad, rows, blocks, dev)
+        _overwritten(out.sorted_ids, out.expert_of_block, out.num_post_pad)
     nbytes = workspace_bytes(M, E, k, block)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
@@ -606,6 +617,8 @@ def gate_route_sort(hidden, w_gate, bias, k: int, n_group: int, topk_group: int,
     elif not (logits.dtype == torch.float32 and tuple(logits.shape) == (M, E) and logits.is_contiguous() and
               logits.device == dev):
         raise ValueError("logits must be a contiguous float32 [M, E] tensor on hidden's device")
+    else:
+        _overwritten(logits)
     if out is None:
         out = RouteSortOutput(torch.empty((M, k), dtype=torch.int32, device=dev),
                               torch.empty((M, k), dtype=torch.float32, device=dev),
@@ -614,6 +627,7 @@ def gate_route_sort(hidden, w_gate, bias, k: int, n_group: int, topk_group: int,
                               torch.empty((1,), dtype=torch.int32, device=dev))
     else:
         _check_route_output(out, M, k, rows, blocks, dev)
+        _overwritten(out.ids, out.weights, out.sorted_ids, out.expert_of_block, out.num_post_pad)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     rc = int(lib().moe_gate_route_sort(hidden.data_ptr(), w_gate.data_ptr(), bias.data_ptr(), M, E, H, k, n_group,

@@ -6,7 +6,9 @@ Checks of arguments, allocation and streams as in the package's other calls: eve
 call runs on the current stream, or on `stream`, which the caller then orders after
 what made the inputs and before what reads the results.  The calls that have an
 explicit backward entry point take no part in autograd and refuse, in grad mode,
-inputs whose gradient they would drop; experts_train joins them under autograd.
+inputs whose gradient they would drop; experts_train joins them under autograd.  Nor
+does autograd hear of what they write into `out`: that must be no tensor which a
+backward pass still reads.
 """
 from __future__ import annotations
 

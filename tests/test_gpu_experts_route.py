@@ -1,5 +1,6 @@
 """experts_train with a route that does not belong to its weights: refused where that is
-known, NaN for the tokens that it concerns where it is not."""
+known, NaN for the tokens that it concerns where it is not; and with buffers that a later
+route is written into before the backward pass."""
 import numpy as np
 import pytest
 import torch
@@ -79,3 +80,32 @@ def test_longer_buffers():
         return [out, *(t.grad for t in leaves)]
     for a, b in zip(run(longer), run(r.meta)):
         assert a.isfinite().all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("which", ["route", "static", "gate", "sort"])
+def test_route_written_over_before_the_backward_pass(which):
+    """The backward pass of the first layer would read the second one's metadata."""
+    M, E, k = 20, 16, 4
+    x, bias = normal((M, H), torch.bfloat16, 1).requires_grad_(), torch.zeros(E, device="cuda")
+    logits = [normal((M, E), torch.float32, 4 + i) for i in range(2)]
+    gate = [normal((E, H), torch.bfloat16, 6 + i) for i in range(2)]
+    ids = [torch.from_numpy(ids_of(M, E, k, 8 + i)).cuda() for i in range(2)]
+
+    def layer(i, buf):
+        if which == "route":
+            return amr.route_sort(logits[i], bias, k, 4, 2, block, out=buf)
+        if which == "static":
+            return amr.route_sort_static(logits[i], bias, k, 4, 2, block, out=buf)
+        if which == "gate":
+            return amr.gate_route_sort(x.detach(), gate[i], bias, k, 4, 2, block, out=buf)[1]
+        meta = amr.sort_from_ids(ids[i], E, block, out=buf and amr.SortOutput(*buf[2:]))
+        return amr.RouteSortOutput(ids[i], torch.full((M, k), 0.25, device="cuda"), *meta)
+    first = layer(0, None)
+    out = amr.experts_train(x, *weights(E), first, block)
+    layer(1, None)  # another call in buffers of its own takes nothing away
+    out.sum().backward(retain_graph=True)
+    layer(1, first)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    out = amr.experts_train(x, *weights(E), first, block)  # of what the buffers hold now
+    out.sum().backward()
