@@ -9,6 +9,7 @@
 #include "half.h"
 #include "moe_experts.h"
 #include "moe_route_sort.h"
+#include "product_runs.h"
 
 namespace {
 
@@ -129,8 +130,7 @@ __device__ __forceinline__ void segment(const int32_t* eob, int n, int e, int& f
   last = lo[1];
 }
 
-constexpr int kXcds = 8;
-// Workgroup h goes to XCD h mod 8.  Runs of consecutive row tiles (run_of below) go to the XCDs
+// Workgroup h goes to XCD h mod 8.  Runs of consecutive row tiles (run_of) go to the XCDs
 // in turn, the column tiles of a row tile one after another.  kWeights: an expert's column tiles
 // go to the XCDs in turn with all their row tiles, so that large experts are everyone's (whole
 // experts in turn 541 us, so 435).
@@ -647,23 +647,6 @@ Launch product_kernel(bool f32, int bm, int bn, bool direct) {
   return f32 ? product_kernel<H, DIR, true, false>(bm, bn) : product_kernel<H, DIR, false, false>(bm, bn);
 }
 
-// The row tiles of a run, as a power of two: those that share an expert's weights, up to four
-// (twice the average, for experts are uneven), and the tiles of a block, of which the first
-// ones hold the routes, as long as that leaves runs for every XCD.  Runs of 1, 2 and 4 (us):
-// 64 tokens of 896 experts, top-16, K 3584, N 768, blocks of 16 441, 441, 457; 512 tokens of
-// 64, top-8, blocks of 128 71, 71, 99; 2048 tokens of them, blocks of 64 227, 191, 180; 777
-// of 24, top-6, K 1000, N 397 18.7, 17.5, 17.1; runs of 1, 2, 4, 8, 16, 32: the case above 1333,
-// 1285, 1261, 1272, 1285, 1258.
-int run_of(int64_t average, int64_t row_tiles, int bm, int block) {
-  int64_t want = (2 * average + bm - 1) / bm;
-  want = want > 4 ? 4 : want;
-  const int64_t of_block = block / bm < row_tiles / 4 ? block / bm : row_tiles / 4;
-  if (of_block > want) want = of_block > 8 ? 8 : of_block;
-  int log2 = 0;
-  while (1 << log2 < want) ++log2;
-  return log2;
-}
-
 constexpr int kMaxCols = 1 << 20;
 
 template <int DIR>
@@ -730,12 +713,14 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     }
     if (tile != 0) bm = rows, bn = tile == rows ? kCols : narrow(DIR);
     g.nrt = (int)(row_limit / bm), g.nct = (g.J + bn - 1) / bn;
-    g.run = run_of(average, used * ((average + bm - 1) / bm), bm, block);
+    g.run = run_of(used, average, bm, block);
     const int64_t group = kXcds << g.run;
     grid = (g.nrt + group - 1) / group * group * g.nct;
   }
   const Launch p = dtype == MRS_DTYPE_BF16 ? product_kernel<BF16, DIR>(f32, bm, bn, direct)
                                            : product_kernel<FP16, DIR>(f32, bm, bn, direct);
+  if (DIR != kWeights && grid * p.threads > UINT32_MAX)  // the shortest runs have the fewest tiles past the last
+    g.run = 0, grid = (g.nrt + kXcds - 1) / kXcds * (int64_t)kXcds * g.nct;
   if (grid * p.threads > UINT32_MAX) return MRS_ERR_OVERFLOW;  // a launch has to have fewer than 2^32 threads
   void* params[] = {&g};
   return hipLaunchKernel(p.kernel, dim3((unsigned)grid), dim3(p.threads), params, 0,
