@@ -74,4 +74,13 @@ inline int run_of(int64_t experts, int64_t average, int bm, int block) {
   return best;
 }
 
+// Whether an XCD's tiles of `columns` column tiles each run at once, two to each of its 32 compute
+// units, where experts get a sixteenth more than the average (they are uneven): a third one to a
+// unit has to wait for one of the first to end.
+inline bool at_once(int64_t experts, int64_t average, int bm, int block, int64_t columns) {
+  const int64_t most = average + average / 16;
+  const XcdTiles x(experts, block_tiles(most, bm, block), live_tiles(most, bm), run_of(experts, most, bm, block));
+  return x.busiest() * columns <= 64;
+}
+
 #endif  // MRS_PRODUCT_RUNS_H_

@@ -9,19 +9,36 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "align_moe_route_amd", "csrc")
 
+SOURCE = """#include "product_runs.h"
+extern "C" int runs(int64_t experts, int64_t average, int bm, int block) { return run_of(experts, average, bm, block); }
+extern "C" bool fits(int64_t experts, int64_t average, int bm, int block, int64_t columns) {
+  return at_once(experts, average, bm, block, columns);
+}
+"""
+
 
 @pytest.fixture(scope="module")
-def run_of(tmp_path_factory):
+def library(tmp_path_factory):
     if not shutil.which("g++"):
         pytest.skip("no host compiler")
     at = tmp_path_factory.mktemp("runs")
-    (at / "runs.cpp").write_text('#include "product_runs.h"\nextern "C" int runs(int64_t experts, int64_t average, int bm, '
-                                 'int block) { return run_of(experts, average, bm, block); }\n')
+    (at / "runs.cpp").write_text(SOURCE)
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-Wall", "-Werror", "-I", CSRC, str(at / "runs.cpp"), "-o",
                     str(at / "runs.so")], check=True)
-    fn = ctypes.CDLL(str(at / "runs.so")).runs
-    fn.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
-    return fn
+    lib = ctypes.CDLL(str(at / "runs.so"))
+    lib.runs.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    lib.fits.argtypes, lib.fits.restype = lib.runs.argtypes + [ctypes.c_int64], ctypes.c_bool
+    return lib
+
+
+@pytest.fixture
+def run_of(library):
+    return library.runs
+
+
+@pytest.fixture
+def at_once(library):
+    return library.fits
 
 
 def tiles_of_xcds(experts, average, bm, block, run):
@@ -83,3 +100,11 @@ def test_it_is_chosen_in_no_time(run_of):
         for _ in range(100):
             run_of(*sizes)
         assert time.perf_counter() - start < 0.05, sizes  # half a millisecond each
+
+
+@pytest.mark.parametrize("sizes,columns,fits", [
+    ((8, 75, 64, 128), 16, True), ((8, 100, 64, 128), 20, True), ((4, 100, 64, 128), 64, True), ((1, 512, 64, 128), 32, True),
+    ((8, 128, 64, 128), 24, False),   # an expert of 128 rows on average has more than two tiles as often as not
+    ((2, 1000, 64, 128), 16, False), ((5, 280, 64, 128), 20, False), ((1, 10 ** 6, 64, 128), 16, False)])
+def test_narrow_tiles_at_once(at_once, sizes, columns, fits):
+    assert at_once(*sizes, columns) == fits
