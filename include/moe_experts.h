@@ -11,6 +11,10 @@
  *
  * Every call is asynchronous on `stream`, allocates nothing, reads num_post_pad on
  * the device, and returns MRS_OK or a negative MRS_ERR_* code before any launch.
+ * Sizes that would take 2^32 threads or more in a launch are MRS_ERR_OVERFLOW.  None of
+ * a product are with R * ceil(J / 256) below 2^27, for R = max_rows and J columns of y or
+ * dx, and none of the weights' gradient with E * ceil(N / 128) * ceil(K / 128) below
+ * 2^22; the other calls state theirs.
  * Matrices are row-major and contiguous; every pointer is aligned to its element
  * size (products of matrices at multiples of 16 bytes whose rows are as well take a
  * faster path).
@@ -102,6 +106,7 @@ int moe_swiglu_backward(const void* a, const void* dh, int dtype, const int32_t*
  * moe_slot_rows -- rows[s] = the row r < *num_post_pad with sorted_ids[r] = s, -1
  * for a slot that has none (a dropped route).  One or two launches, by the sizes.
  *   sorted_ids  `capacity` entries;  rows  [M, k] int32 (written whole)
+ *   capacity and M * k at most 2^31 - 257, k 1 .. 64
  */
 int moe_slot_rows(const int32_t* sorted_ids, const int32_t* num_post_pad, int64_t capacity, int M, int k,
                   int32_t* rows, void* stream);
@@ -113,7 +118,8 @@ int moe_slot_rows(const int32_t* sorted_ids, const int32_t* num_post_pad, int64_
  *   y         [capacity, N]
  *   rows      [M, k] int32, or NULL: rows[t, j] = t k + j (y in slot order)
  *   weights   [M, k] FP32, or NULL for ones
- *   N         1 .. 2^20;  k  1 .. 64
+ *   N         1 .. 2^20;  k  1 .. 64;  capacity and M * k below 2^31;
+ *             M * ceil(N / 512) at most 2^26 - 4
  *   out       [M, N] of y's type or FP32
  */
 int moe_combine(const void* y, int dtype, const int32_t* rows, const float* weights, int64_t capacity, int M, int k,
@@ -130,6 +136,7 @@ int moe_combine(const void* y, int dtype, const int32_t* rows, const float* weig
  *   y, dweights  both given, or both NULL (no gradient of the weights is wanted); not
  *             looked at where M is 0
  *   dy        [capacity, N] (rows below *num_post_pad are written)
+ *   N, k      as for moe_combine;  M * k + capacity / 64 at most 2^26 - 12
  */
 int moe_combine_backward(const void* dout, const void* y, int dtype, const int32_t* rows, const int32_t* sorted_ids,
                          const int32_t* num_post_pad, const float* weights, int64_t capacity, int M, int k, int N,

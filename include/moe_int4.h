@@ -32,7 +32,8 @@ extern "C" {
  *
  *   w           [rows, K], consecutive columns, row r at w + r * row_stride
  *               elements (row_stride >= K), aligned to its element size
- *   rows        >= 0;  K  1 .. 262144;  group  32, 64 or 128
+ *   rows        >= 0, rows * Kp / 8 at most 2^38 (else MRS_ERR_OVERFLOW);  K  1 .. 262144;
+ *               group  32, 64 or 128
  *   scale_dtype MRS_DTYPE_BF16 or MRS_DTYPE_F16
  *   codes       [rows, Kp / 2] (written), 4-byte aligned
  *   scales      [rows, Kp / group] (written), 2-byte aligned
@@ -68,8 +69,8 @@ enum {
  *   ids       [M, k] int32
  *   weights   [M, k] FP32 (MRS_INT4_SUM only, else NULL; not looked at where M is 0)
  *   M         >= 0;  k  1 .. 64;  E  1 .. 4096;  K  1 .. 262144, any with the codes' Kp
- *   N         1 .. 2^20, even for MRS_INT4_GATED; N * Kp / 2 below 2^31 bytes
- *             (MRS_ERR_OVERFLOW)
+ *   N         1 .. 2^20, even for MRS_INT4_GATED; N * Kp / 2 below 2^31 bytes and
+ *             M * k * ceil(N / 32) below 2^24 (else MRS_ERR_OVERFLOW)
  *   y         of x's dtype, 2-byte aligned
  * Asynchronous on `stream`; one launch; allocates nothing.  Returns MRS_OK or a
  * negative MRS_ERR_* code before any launch.
