@@ -106,9 +106,11 @@ constexpr int64_t kQLaunch = int64_t(1) << 31;
 // time.  A code c is made a 16-bit float by putting it into the top of the
 // mantissa of 16.0: the value 16 + c costs one shift and one and-or for two codes,
 // v_dot2 multiplies pairs into FP32, and 24 times the sum of x is taken off per
-// chunk: sum x (16 + c) - 24 sum x = sum x (c - 8), with partial sums at most 55 / 8 of
-// those of c - 8.  Scale and pick weight enter once a chunk.  The low and high half of
-// a dword's pair hold codes i and i + 4, so x is paired alike.
+// chunk: sum x (16 + c) - 24 sum x = sum x (c - 8).  The partial sums are at most 55 sum |x|,
+// whatever the codes, and are rounded 33 times (sum x, at 24, as often), so a chunk is off by up
+// to 50 * 55 * 2^-24 scale sum |x|, also where its weights are all zero (codes 8).  Scale and pick
+// weight enter once a chunk.  The low and high half of a dword's pair hold codes i and i + 4,
+// so x is paired alike.
 //
 // Bound by the weights' bytes where there are many, by a chain of two round trips (the
 // pick's id, then everything else) where there are few: one token of 896 experts,
