@@ -90,7 +90,8 @@ __device__ __forceinline__ u32x4 operand(const u32x4* tile, int m0, int kk) {
 // 16 bytes a lane from memory into LDS, lane l's at dst + 16 l.  Written out because
 // the compiler waits for all such loads before any LDS read that it cannot tell from
 // their targets, which leaves none in flight; the loop below counts them itself.  No
-// register is written but m0, which the compiler keeps nothing in.
+// register is written but m0: a reserved one, which the compiler sets right before an
+// instruction that reads it, and refuses to take as clobbered.
 __device__ __forceinline__ void load_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
 }
@@ -229,18 +230,14 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   const uint32_t lds_a = (uint32_t)(uintptr_t)(lds_t)(char*)l.a + (uint32_t)wv * 1024;
   const uint32_t lds_b = (uint32_t)(uintptr_t)(lds_t)(char*)l.b + (uint32_t)wv * 1024;
   const void* const zeros = &kZeros;
-  // kWeights: the sources of a step's rows, -1 for none; the same for both operands where
-  // their tiles are equally wide
-  constexpr bool kOneMap = WA == WB;
-  constexpr int RP = DIR != kWeights ? 1 : kOneMap ? AP : AP + BP;
+  // kWeights: the sources of a step's rows, -1 for none; the same for both operands, whose
+  // tiles are equally wide
+  static_assert(DIR != kWeights || WA == WB, "one map of rows");
+  constexpr int RP = DIR != kWeights ? 1 : AP;
   auto find = [&](int (&to)[RP], int t) {
     if constexpr (DIR == kWeights) {
 #pragma unroll
       for (int p = 0; p < AP; ++p) to[p] = l.row[t * kStep + tid / WA + p * SA];
-      if constexpr (!kOneMap) {
-#pragma unroll
-        for (int p = 0; p < BP; ++p) to[AP + p] = l.row[t * kStep + tid / WB + p * SB];
-      }
     }
   };
   // Chunks whose rows run across the tile: the last chunk of a row ends with it, and so
@@ -260,7 +257,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   auto chunk_b = [&](int t, int p, const int (&rows)[RP]) {
     if constexpr (DIR == kForward) return pb[p] + along(t);
     else if constexpr (DIR == kRows) return pb[p] + (int64_t)t * kStep * g.J + j_at;
-    else return g.b + (int64_t)max(rows[kOneMap ? p : AP + p], 0) * g.J + j_at;
+    else return g.b + (int64_t)max(rows[p], 0) * g.J + j_at;
   };
   // Whether a chunk's row of c (or, along c and straight into LDS, the chunk) exists.
   auto has_a = [&](int t, int p, const int (&rows)[RP]) {
@@ -269,7 +266,7 @@ __global__ __launch_bounds__(P::kThreads, P::kPerSimd) void k_product(GArgs g) {
   auto has_b = [&](int t, int p, const int (&rows)[RP]) {
     return DIR == kForward ? !DIRECT || t * kStep + sc < c_end
            : DIR == kRows  ? t * kStep + tid / WB + p * SB < c_end
-                           : rows[DIR != kWeights ? 0 : kOneMap ? p : AP + p] >= 0;
+                           : rows[DIR != kWeights ? 0 : p] >= 0;
   };
   // A part of step t of c, a KK-th (all of it where kPart is KK), into stage `buf` of LDS.
   auto issue = [&](int t, int buf, const int (&rows)[RP], auto part) {
