@@ -520,7 +520,8 @@ def int4_matvec(x, w: Int4, ids, *, gated: bool = False, weights=None, out=None,
         raise ValueError("gated results need an even N and take no weights")
     if weights is not None:
         _check_weights(weights, M, k, dev, index)
-    _no_grad("int4_matvec", x, weights, w.scales)
+    if x.requires_grad or w.scales.requires_grad or (weights is not None and weights.requires_grad):
+        _no_grad("int4_matvec", x, w.scales, weights)
     foreign = None if stream is None else _foreign(stream, dev)
     out = _output(out, (M, N) if weights is not None else (M, k, N // 2 if gated else N), xdt, dev, foreign)
     mode = MRS_INT4_GATED if gated else MRS_INT4_PLAIN if weights is None else MRS_INT4_SUM
