@@ -361,9 +361,9 @@ def _holds_experts(route, E: int, block: int) -> bool:
     return M * k > E and (route.sorted_ids.numel(), route.expert_of_block.numel()) == (rows, blocks)
 
 
-def _rows_of(whole: bool, sorted_ids, columns: int, dtype):
-    """The rows that a product writes into: NaN where it may leave some out."""
-    return None if whole else torch.full((sorted_ids.numel(), columns), float("nan"), dtype=dtype, device=sorted_ids.device)
+def _rows_of_nan(rows: int, columns: int, like):
+    """Rows for a product that may leave some out, where any are asked for."""
+    return torch.full((rows, columns), float("nan"), dtype=like.dtype, device=like.device) if rows else None
 
 
 @functools.lru_cache(maxsize=1)
@@ -373,13 +373,14 @@ def _experts_function():
         def forward(ctx, x, w_up, w_down, weights, sorted_ids, expert_of_block, num_post_pad, block, whole):
             meta = (sorted_ids, expert_of_block, num_post_pad)
             M, k = weights.shape
-            a = grouped_gemm(x, w_up, *meta, k, block, out=_rows_of(whole, sorted_ids, w_up.shape[1], x.dtype))
+            # as many as M k routes to any number of experts may take
+            fill = 0 if whole else max(min(sorted_ids.numel(), M * k * block), 1)
+            a = grouped_gemm(x, w_up, *meta, k, block, out=_rows_of_nan(fill, w_up.shape[1], x))
             h = swiglu(a, num_post_pad)
-            y = grouped_gemm(h, w_down, *meta, k, block, tokens=M,
-                             out=_rows_of(whole, sorted_ids, w_down.shape[1], x.dtype))
+            y = grouped_gemm(h, w_down, *meta, k, block, tokens=M, out=_rows_of_nan(fill, w_down.shape[1], x))
             rows = slot_rows(sorted_ids, num_post_pad, M, k)
             ctx.save_for_backward(x, w_up, w_down, weights, a, h, y, rows, *meta)
-            ctx.block, ctx.whole = block, whole
+            ctx.block, ctx.fill = block, fill
             return combine(y, rows, weights)
 
         @staticmethod
@@ -396,14 +397,13 @@ def _experts_function():
             if need_down:
                 d_down = grouped_gemm_dw(dy, h, E, *meta, k, block, tokens=M)
             if need_x or need_up:
-                dh = grouped_gemm_dx(dy, w_down, *meta, M, k, block,
-                                     out=_rows_of(ctx.whole, sorted_ids, w_down.shape[2], x.dtype))
+                dh = grouped_gemm_dx(dy, w_down, *meta, M, k, block, out=_rows_of_nan(ctx.fill, w_down.shape[2], x))
                 da = swiglu_backward(a, dh, num_post_pad)
                 if need_up:
                     d_up = grouped_gemm_dw(da, x, E, *meta, k, block)
-                if need_x:
-                    dx = combine(grouped_gemm_dx(da, w_up, *meta, M, k, block,
-                                                 out=_rows_of(ctx.whole, sorted_ids, w_up.shape[2], x.dtype)), rows)
+                if need_x:  # of 16-bit rows, which combine takes: each pick's is rounded before their FP32 sum
+                    dx = grouped_gemm_dx(da, w_up, *meta, M, k, block, out=_rows_of_nan(ctx.fill, w_up.shape[2], x))
+                    dx = combine(dx, rows)
             return dx, d_up, d_down, dv, None, None, None, None, None
 
     return Experts

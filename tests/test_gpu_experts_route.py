@@ -65,9 +65,10 @@ def test_route_made_by_hand(M, E, held):
     assert np.array_equal(token.cpu().numpy(), (ids >= held).any(1)) and 0 < int(token.sum()) < M
 
 
-def test_longer_buffers():
-    """Metadata in buffers that are longer than these sizes need."""
-    M, E, k = 30, 5, 2
+@pytest.mark.parametrize("M", [2, 30])
+def test_longer_buffers(M):
+    """Metadata in buffers that are longer than these sizes need, and than any could."""
+    E, k = 5, 2
     r = Routed(ids_of(M, E, k, 1), E, block)
     longer = [torch.cat([r.meta[0], torch.full((700,), 3, dtype=torch.int32, device="cuda")]),
               torch.cat([r.meta[1], torch.full((9,), 77, dtype=torch.int32, device="cuda")]), r.meta[2]]
