@@ -343,8 +343,7 @@ def route_sort(logits, bias, k: int, n_group: int, topk_group: int, block: int, 
         if flags or stats is not None or events is not None:
             raise ValueError("a local range is not combined with flags, stats or events")
     EL = E if local is None else lc
-    rows = max_rows(M, EL, k, block)
-    blocks = max_blocks(M, EL, k, block)
+    rows, blocks = _capacity(M, EL, k, block)
     if rows < 0:
         raise ValueError("invalid sizes or row capacity overflow")
     if out is None:
@@ -506,8 +505,7 @@ def sort_from_ids(ids, E: int, block: int, *, out: Optional[SortOutput] = None, 
             rows = int(out.sorted_ids.numel()) if rows_capacity is None else int(rows_capacity)
             blocks = rows // block
     else:
-        rows = max_rows(M, E, k, block)
-        blocks = max_blocks(M, E, k, block)
+        rows, blocks = _capacity(M, E, k, block)
         if rows < 0:
             raise ValueError("invalid sizes or row capacity overflow")
     if out is None:
