@@ -20,17 +20,19 @@ namespace {
 //             (rows along j)
 // on v_mfma_f32_32x32x16, which sums 16 products in FP32.
 //
-// What bounds them is how fast a compute unit takes operands out of its L2 (measured:
-// 120 GB/s in whole 128-byte lines, 62 in halves of lines, 37 at odd addresses; LDS reads
-// are 350 to 450), beside the matrix units at the clock that the power leaves. So: tiles as
-// large as the registers hold where there are enough of them for every compute unit, and
-// narrow ones where there are not; operands straight into LDS in whole lines where rows are
-// whole chunks (steps of 64 along c); loads, LDS reads and matrix instructions of a wave
+// What bounds the large ones is what passes the L2s: 8.0 GB for y, 2.7 for dx and 1.8 for dw of
+// the cases below, 6.4, 5.8 and 4.2 TB/s (a copy moves 4.9; the 256 MB cache answers a part).  y
+// must move 5.3 GB, dx 0.95 and dw 0.5: XCDs and column tiles read operands again.  What bounds
+// small and odd ones is how fast a compute unit takes operands out of its L2 (measured: 120 GB/s
+// in whole 128-byte lines, 62 in halves of lines, 37 at odd addresses; LDS reads are 350 to 450).
+// So: tiles as large as the registers hold where there are enough of them for every compute
+// unit, and narrow ones where there are not; operands straight into LDS in whole lines where rows
+// are whole chunks (steps of 64 along c); loads, LDS reads and matrix instructions of a wave
 // interleaved; and what an expert's tiles share read from one L2 at about the same time.
 //   8192 tokens, 896 experts, top-16, K 3584, N 768, blocks of 128: y in 1250 us; the bytes
 //   that must move take 1075 at a copy's 4.9 TB/s (weights 4.9 GB); 577 TFLOP/s of routes
-//   8192 tokens, 64 experts, top-8, the same K and N: dx in 480 us, dw in 400 (750 and 900
-//   TFLOP/s; an 8192^3 library product 1395; even experts of 2048 rows: 840 and 1030)
+//   8192 tokens, 64 experts, top-8, the same K and N: dx in 440 to 470 us, dw in 400 to 440 (the
+//   matrix units busy 43 to 50 % of it; an 8192^3 library product 1395 TFLOP/s, these 770 to 900)
 enum Dir { kForward, kRows, kWeights };
 
 struct GArgs {
@@ -570,7 +572,8 @@ constexpr int kCols = 256;
 //     top-8, blocks of 64); seven stages of steps of 32: 22.6 for 18.7 (777 tokens of 24)
 //   kRows: B runs across, in whole lines at any step: 128 rows by 4 waves and steps of 32
 //     485, by 8 waves and steps of 64 512, pairs of blocks as tiles of 256 x 256 506 (the
-//     case above; experts that share a pair take two passes)
+//     case above; experts that share a pair take two passes); through registers they use all
+//     256 and keep 8 (FP32 results) or 20 bytes a lane in scratch
 //   kWeights: 256 x 256 by 8 waves 440, 128 x 256 by 8 waves 480, 128 x 128 487 (the case
 //     above); 512 tokens of 896 experts 955, 1213, 1122
 //   kWeights through registers: 128 x 128 by 8 waves 21.3 (777 tokens of 24 experts, K 1000,

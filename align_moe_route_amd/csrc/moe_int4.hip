@@ -115,7 +115,7 @@ constexpr int64_t kQLaunch = int64_t(1) << 31;
 // Bound by the weights' bytes where there are many, by a chain of two round trips (the
 // pick's id, then everything else) where there are few: one token of 896 experts,
 // top-16, K 3584, N 768, gated: 23 MB in 8.3 us; 16 tokens 319 MB in 73 us, 4.4 TB/s;
-// the second product and the sum of one token, 12 MB, 6.1 us.  64 tokens read shared
+// the second product and the sum of one token, 12 MB, 4.8 to 5.5 us.  64 tokens read shared
 // experts again (872 MB once, 1.46 GB in all) and take 250 us, about half of it the
 // 12 vector instructions for eight codes.
 

@@ -58,9 +58,10 @@ enum {
  *
  * and y as the mode says; a pick whose e lies outside [0, E) has p = 0 (and y = 0).
  * Sums and the mode's arithmetic are held in FP32 and rounded once to y's type.
- * The weights' bytes bound it: each pick reads its expert's matrix, so for more
- * than some tens of tokens the grouped products over the sorted metadata fit
- * better.
+ * The weights' bytes bound it: each pick reads its expert's matrix, so tokens that
+ * share experts read them again.  The grouped products, which read an expert once for
+ * many tokens, take 16-bit (moe_experts.h) or 4-bit microscaled weights
+ * (moe_mxfp4.h), not these.
  *
  *   x         [M, K] (per_slot 0) or [M, k, K] (per_slot 1), dtype MRS_DTYPE_BF16 or
  *             MRS_DTYPE_F16, 2-byte aligned; |x| below 2^96 (an infinity or a NaN
