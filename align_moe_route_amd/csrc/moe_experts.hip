@@ -694,7 +694,7 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     // an expert is one tile, so that its weights are read once either way; where it is more, tiles
     // of 64 rows and whole chunks, if the narrow ones run at once.  us, wide / narrow, kForward:
     // 300 tokens of 8 experts, top-2, K 2048, N 1024 21.5 / 13.6; 400 of 8, N 1280 26.7 / 16.1; 200
-    // of 4, N 4096 29.0 / 23.7; 512 of 8, K 3584, N 1536 (four tiles on an XCD of 24 columns each)
+    // of 4, N 4096 29.0 / 23.7; 512 of 8, K 3584, N 1536 (three row tiles of 24 columns on an XCD)
     // 47.4 / 67.4; 400 of 5, K 2048, N 1280 20.4 / 27.3; 2000 of 2, top-1, N 1024 20.2 / 26.9; 200 of
     // 24, top-6, K 1000, N 400 12.1 / 8.7; 48 of 31, top-3, K 1713, N 109 30.8 / 12.9; one of 896,
     // top-16, K 3584, N 768 26.2 / 18.0, four of them 59.8 / 53.4; 777 of 24 (192 workgroups) 17.1 /
