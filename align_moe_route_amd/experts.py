@@ -429,8 +429,8 @@ def experts_train(x, w_up, w_down, route, block: int):
     if x.shape[1] != H or two % 2 or tuple(w_down.shape) != (E, H, two // 2) or route.weights.shape[0] != x.shape[0]:
         raise ValueError("w_up must be [E, 2 I, H], w_down [E, H, I] and route.weights [M, k] for x [M, H]")
     meta = (route.sorted_ids, route.expert_of_block, route.num_post_pad)
-    whole = _holds_experts(route, E, block)
     _metadata(*meta, *_sizes(x.shape[0], E, route.weights.shape[1], block), x.device, index)
+    whole = _holds_experts(route, E, block)
     return _experts_function().apply(x, w_up, w_down, route.weights, *meta, block, whole)
 
 

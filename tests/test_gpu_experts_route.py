@@ -38,6 +38,13 @@ def test_route_of_more_experts(M):
         amr.experts_train(x, *weights(5), local, block)
 
 
+def test_route_of_no_tensors():
+    x, v = normal((4, H), torch.bfloat16, 1), torch.ones(4, 2, device="cuda")
+    for bad in (None, 7, torch.zeros(4), torch.zeros(999, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            amr.experts_train(x, *weights(3), amr.RouteSortOutput(None, v, bad, bad, bad), block)
+
+
 @pytest.mark.parametrize("M,E,held", [(3, 12, 7), (40, 9, 6)])
 def test_route_made_by_hand(M, E, held):
     """Weights of the first experts only: the others' tokens are NaN, with their gradients."""
