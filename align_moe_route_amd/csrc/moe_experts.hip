@@ -694,17 +694,17 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     // an expert is one tile, so that its weights are read once either way; where it is more, tiles
     // of 64 rows and whole chunks, if the narrow ones run at once.  us, wide / narrow, kForward:
     // 300 tokens of 8 experts, top-2, K 2048, N 1024 21.5 / 13.6; 400 of 8, N 1280 26.7 / 16.1; 200
-    // of 4, N 4096 29.0 / 23.7; 512 of 8, K 3584, N 1536 (three row tiles of 24 columns on an XCD)
-    // 47.4 / 67.4; 400 of 5, K 2048, N 1280 20.4 / 27.3; 2000 of 2, top-1, N 1024 20.2 / 26.9; 200 of
-    // 24, top-6, K 1000, N 400 12.1 / 8.7; 48 of 31, top-3, K 1713, N 109 30.8 / 12.9; one of 896,
-    // top-16, K 3584, N 768 26.2 / 18.0, four of them 59.8 / 53.4; 777 of 24 (192 workgroups) 17.1 /
-    // 23; rows that are no whole chunks, 1000 of 8, top-2, K 1001, N 515 26.1 / 15.5.  kRows: 200 of
-    // 24 8.0 / 7.1, one of 896 (224) 16.1 / 16.5, 48 of 31 (217) 9.1 / 11.1.  Narrow tiles of few rows
-    // an expert are of 32 rows (48 of 31 16.7, so 12.9; 100 rows an expert 12.7 for 13.6), and
-    // kForward takes them for any number of such experts where operands go through registers, which
-    // are slower to fill (256 of 256, top-8, K 1203, N 515 102 / 76; 40 of 120, top-14, K 1209, N 676
-    // 58 / 39; 64 of 896, top-16, K 1001, N 397 129 / 111; with whole chunks, K 2048, N 768, 512 of
-    // 128 97 / 99).
+    // of 4, N 4096 29.0 / 23.7; 2000 of 2, top-1, N 1024 20.2 / 26.9; 512 of 8, K 3584, N 1536 (three
+    // row tiles of 24 columns on an XCD) 47.4 / 67.4, and where their average just fits, but not an
+    // uneven XCD, K 2048, N 1280 28.0 / 33.8; 200 of 24, top-6, K 1000, N 400 12.1 / 8.7; 48 of 31,
+    // top-3, K 1713, N 109 30.8 / 12.9; one of 896, top-16, K 3584, N 768 26.2 / 18.0, four of them
+    // 59.8 / 53.4; 777 of 24 (192 workgroups) 17.1 / 23; rows that are no whole chunks, 1000 of 8,
+    // top-2, K 1001, N 515 26.1 / 15.5.  kRows: 200 of 24 8.0 / 7.1, one of 896 (224) 16.1 / 16.5, 48
+    // of 31 (217) 9.1 / 11.1.  Narrow tiles of few rows an expert are of 32 rows (48 of 31 16.7, so
+    // 12.9; 100 rows an expert 12.7 for 13.6), and kForward takes them for any number of such
+    // experts where operands go through registers, which are slower to fill (256 of 256, top-8, K
+    // 1203, N 515 102 / 76; 40 of 120, top-14, K 1209, N 676 58 / 39; 64 of 896, top-16, K 1001, N
+    // 397 129 / 111; with whole chunks, K 2048, N 768, 512 of 128 97 / 99).
     bm = block % 128 == 0 ? 128 : block % 64 == 0 ? 64 : block % 32 == 0 ? 32 : 16;
     const int64_t routes = (int64_t)M * k, used = routes < E ? routes : E, average = (routes + used - 1) / used;
     auto tiles = [&] { return used * ((average + bm - 1) / bm) * ((g.J + bn - 1) / bn); };
@@ -713,8 +713,8 @@ int product(const void* a, const void* b, int dtype, const int32_t* sid, const i
     const bool fits = row_limit * ((g.J + 63) / 64) < 1 << 28;  // more threads than wide ones, fewer than 2^32
     auto few = [&] {
       if (DIR == kForward && average <= bm) return tiles() < 256;
-      if (DIR == kRows || !direct || bm < 64 || tiles() > 128) return tiles() < 128;
-      return at_once(used, average, bm, block, (g.J + narrow(DIR) - 1) / narrow(DIR));
+      if (DIR == kRows || !direct || bm < 64) return tiles() < 128;
+      return tiles() <= 128 && at_once(used, average, bm, block, (g.J + narrow(DIR) - 1) / narrow(DIR));
     };
     if (fits && (short_rows || (bm <= 64 && few()))) {
       bn = narrow(DIR);
